@@ -8,6 +8,7 @@ missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -81,6 +82,17 @@ _SIGS = {
                                _vp]),
     "lutq_gemm_typed": (_i32, [_vp, _i64, _vp, _vp, _i32, _i32, _i64, _i64, _vp, _vp, _i64, _vp,
                                _vp]),
+    "lutq_mx_packed_bytes": (_i64, [_i64, _i64, _i32]),
+    "lutq_mx_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "lutq_mx_dequantize": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp]),
+    "lutq_mx_pack": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "lutq_mx_gemm": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp]),
+    "lutq_mx_gemv": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp]),
+    "lutq_route": (_i32, [_vp, _i32, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                          ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "lutq_mx_experts_workspace_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32]),
+    "lutq_mx_experts": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _i64,
+                               _i32, _vp, _vp, _i64, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -485,3 +497,219 @@ def lutq_fit_codebook(hist, bits: int, init: torch.Tensor, max_iter: int = 100) 
     _check(lib.lutq_fit_codebook(h.data_ptr(), bits, init_c.data_ptr(), max_iter, out.data_ptr()),
            "lutq_fit_codebook")
     return out
+
+
+# ---- microscaled 4-bit floating point and experts
+
+MX_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+_MX_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+SCORES = {"softmax": 0, "sigmoid": 1}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _format(fmt: str) -> int:
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"format must be one of {tuple(MX_FORMATS)}")
+    return MX_FORMATS[fmt]
+
+
+def _dtype(dtype, name: str) -> int:
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32")
+    return _DTYPES[dtype]
+
+
+def _here(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The current stream of the current device, which must hold the tensors."""
+    dev = torch.cuda.current_device()
+    if first.get_device() != dev:
+        raise ValueError("tensors must be on the current CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _values(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return _dtype(t.dtype, name)
+
+
+def _mx_need(t: torch.Tensor, nbytes: int, name: str) -> None:
+    _need(t, torch.uint8, name)
+    if nbytes < 0 or t.numel() != nbytes:
+        raise LutqError(2, f"{name}: not a packed matrix of this shape")
+
+
+def _mx_out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise LutqError(2, f"{name} must have the shape {tuple(shape)}")
+    return t
+
+
+@functools.lru_cache(maxsize=None)
+def lutq_mx_packed_bytes(n: int, k: int, fmt: str) -> int:
+    """Bytes of a packed n x k matrix ("mxfp4" or "nvfp4"); -1 if invalid."""
+    return int(lib.lutq_mx_packed_bytes(n, k, _format(fmt)))
+
+
+def lutq_mx_quantize(w: torch.Tensor, fmt: str, packed: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """w [N, K] or [B, N, K] (bf16, fp16 or fp32) to microscaled 4-bit floating
+    point: packed uint8 [bytes] or [B, bytes]; see include/lutq.h."""
+    dt = _values(w, "w")
+    if w.dim() not in (2, 3):
+        raise LutqError(2, "lutq_mx_quantize: w must be [N, K] or [B, N, K]")
+    n, k = w.shape[-2:]
+    b = w.shape[0] if w.dim() == 3 else 1
+    nb = lutq_mx_packed_bytes(n, k, fmt) if n else 0
+    if nb < 0:
+        raise LutqError(2, "lutq_mx_quantize")
+    packed = _mx_out(packed, (b, nb) if w.dim() == 3 else (nb,), torch.uint8, w, "packed")
+    _check(lib.lutq_mx_quantize(w.data_ptr(), dt, b, n, k, _format(fmt), packed.data_ptr(),
+                                _ptr(status), _here(w, packed, status)), "lutq_mx_quantize")
+    return packed
+
+
+def lutq_mx_dequantize(packed: torch.Tensor, n: int, k: int, fmt: str, dtype=torch.bfloat16,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of a packed matrix [bytes] as [n, k], or of [B, bytes] as [B, n, k]."""
+    nb = lutq_mx_packed_bytes(n, k, fmt)
+    b = packed.shape[0] if packed.dim() == 2 else 1
+    _mx_need(packed, b * nb if nb >= 0 else -1, "packed")
+    out = _mx_out(out, (b, n, k) if packed.dim() == 2 else (n, k), dtype, packed, "out")
+    _check(lib.lutq_mx_dequantize(packed.data_ptr(), b, n, k, _format(fmt), out.data_ptr(),
+                                  _dtype(dtype, "dtype"), _here(packed, out)),
+           "lutq_mx_dequantize")
+    return out
+
+
+def lutq_mx_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: str,
+                 row_scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """codes uint8 [N, K/2] (two a byte, the even element low), scale bytes uint8
+    [N, K/32 or K/16] and, for "nvfp4", row_scales fp32 [N] (None: 1) into a
+    packed matrix; with a leading dimension B, into B of them."""
+    _need(codes, torch.uint8, "codes")
+    _need(scales, torch.uint8, "scales")
+    if codes.dim() not in (2, 3):
+        raise LutqError(2, "lutq_mx_pack: codes must be [N, K/2] or [B, N, K/2]")
+    n, k = codes.shape[-2], codes.shape[-1] * 2
+    b = codes.shape[0] if codes.dim() == 3 else 1
+    f = _format(fmt)
+    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (k // _MX_BLOCK[fmt],):
+        raise LutqError(2, "lutq_mx_pack: scales shape")
+    if row_scales is not None:
+        _need(row_scales, torch.float32, "row_scales")
+        if fmt != "nvfp4" or tuple(row_scales.shape) != tuple(codes.shape[:-1]):
+            raise LutqError(2, "lutq_mx_pack: row_scales shape")
+    nb = lutq_mx_packed_bytes(n, k, fmt) if n else 0
+    if nb < 0:
+        raise LutqError(2, "lutq_mx_pack")
+    packed = torch.empty((b, nb) if codes.dim() == 3 else (nb,), dtype=torch.uint8,
+                         device=codes.device)
+    _check(lib.lutq_mx_pack(codes.data_ptr(), scales.data_ptr(), _ptr(row_scales), b, n, k, f,
+                            packed.data_ptr(), _here(codes, scales, row_scales)), "lutq_mx_pack")
+    return packed
+
+
+def lutq_mx_gemm(x_packed: torch.Tensor, m: int, packed: torch.Tensor, n: int, k: int, fmt: str,
+                 dtype=torch.float32, y: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[m, n] = x w^T of two packed matrices, x [m, k] (lutq_mx_quantize) and
+    w [n, k]; see lutq_mx_gemm in include/lutq.h."""
+    _mx_need(x_packed, lutq_mx_packed_bytes(m, k, fmt) if m else 0, "x_packed")
+    _mx_need(packed, lutq_mx_packed_bytes(n, k, fmt), "packed")
+    y = _mx_out(y, (m, n), dtype, packed, "y")
+    _check(lib.lutq_mx_gemm(x_packed.data_ptr(), m, packed.data_ptr(), n, k, _format(fmt),
+                            y.data_ptr(), _dtype(dtype, "dtype"), _ptr(status),
+                            _here(packed, x_packed, y, status)), "lutq_mx_gemm")
+    return y
+
+
+def lutq_mx_gemv(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, fmt: str,
+                 dtype=torch.float32, y: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[M, n] for M = 0..16 rows of x [M, k] (bf16, fp16 or fp32), quantized
+    inside the kernel; see lutq_mx_gemv in include/lutq.h."""
+    dt = _values(x, "x")
+    if x.dim() != 2 or x.shape[1] != k:
+        raise LutqError(2, "lutq_mx_gemv: x must be [M, k]")
+    _mx_need(packed, lutq_mx_packed_bytes(n, k, fmt), "packed")
+    m = x.shape[0]
+    y = _mx_out(y, (m, n), dtype, packed, "y")
+    _check(lib.lutq_mx_gemv(x.data_ptr(), dt, m, packed.data_ptr(), n, k, _format(fmt),
+                            y.data_ptr(), _dtype(dtype, "dtype"), _ptr(status),
+                            _here(packed, x, y, status)), "lutq_mx_gemv")
+    return y
+
+
+def lutq_route(logits: torch.Tensor, top_k: int, score: str = "softmax",
+               bias: Optional[torch.Tensor] = None, groups: int = 1, top_groups: int = 1,
+               group_best: int = 1, renormalize: bool = False, scale: float = 1.0,
+               status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """logits [T, E] -> (ids int32 [T, top_k], weights fp32 [T, top_k]): the
+    experts of every token; see lutq_route in include/lutq.h."""
+    dt = _values(logits, "logits")
+    if logits.dim() != 2:
+        raise LutqError(2, "lutq_route: logits must be [T, E]")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {tuple(SCORES)}")
+    t, e = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != e:
+            raise LutqError(2, "lutq_route: bias must have one value per expert")
+    if not 1 <= top_k <= 32:
+        raise LutqError(2, "lutq_route: top_k")
+    ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    _check(lib.lutq_route(logits.data_ptr(), dt, t, e, _ptr(bias), SCORES[score], groups,
+                          top_groups, group_best, top_k, int(renormalize), scale,
+                          ids.data_ptr(), weights.data_ptr(), _ptr(status),
+                          _here(logits, bias, status)), "lutq_route")
+    return ids, weights
+
+
+def lutq_mx_experts_workspace_bytes(t: int, top_k: int, e: int, d: int, f: int, fmt: str) -> int:
+    return int(lib.lutq_mx_experts_workspace_bytes(t, top_k, e, d, f, _format(fmt)))
+
+
+def lutq_mx_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                    gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, f: int, fmt: str,
+                    y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture-of-experts feed-forward layer: x [T, D], ids and weights
+    [T, top_k] (lutq_route), gate and up packed [E, bytes of f x D], down
+    packed [E, bytes of D x f]; y [T, D] of x's type.  workspace: uint8, at
+    least lutq_mx_experts_workspace_bytes, any contents (None: allocated for
+    the call); see lutq_mx_experts in include/lutq.h."""
+    dt = _values(x, "x")
+    _need(ids, torch.int32, "ids")
+    _need(weights, torch.float32, "weights")
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0] or weights.shape != ids.shape:
+        raise LutqError(2, "lutq_mx_experts: x [T, D], ids and weights [T, top_k]")
+    if gate.dim() != 2:
+        raise LutqError(2, "lutq_mx_experts: gate must be [E, bytes]")
+    (t, d), top_k, e = x.shape, ids.shape[1], gate.shape[0]
+    n1, n2 = lutq_mx_packed_bytes(f, d, fmt), lutq_mx_packed_bytes(d, f, fmt)
+    for w, nb, name in ((gate, n1, "gate"), (up, n1, "up"), (down, n2, "down")):
+        _mx_need(w, e * nb if nb >= 0 else -1, name)
+    y = _mx_out(y, (t, d), x.dtype, x, "y")
+    if workspace is None:
+        nb = lutq_mx_experts_workspace_bytes(t, top_k, e, d, f, fmt)
+        if nb < 0:
+            raise LutqError(2, "lutq_mx_experts")
+        workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    _check(lib.lutq_mx_experts(x.data_ptr(), dt, t, ids.data_ptr(), weights.data_ptr(), top_k, e,
+                               gate.data_ptr(), up.data_ptr(), down.data_ptr(), d, f,
+                               _format(fmt), y.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), _ptr(status),
+                               _here(x, ids, weights, gate, up, down, y, workspace, status)),
+           "lutq_mx_experts")
+    return y

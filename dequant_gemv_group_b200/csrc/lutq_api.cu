@@ -7,7 +7,7 @@
 
 #include "lutq.h"
 #include "lutq_trace.h"
-#include "lutq_common.cuh"
+#include "lutq_mx.cuh"
 
 namespace lutq {
 cudaError_t launch_quantize(const void* W, int64_t N, int64_t K, const void* codebook, int bits,
@@ -44,6 +44,27 @@ cudaError_t launch_rht(const void* in, int64_t rows, int64_t K, const int8_t* si
                        bool activations, void* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_fit_histogram(const void* W, int64_t N, int64_t K, uint64_t* hist,
                                  int32_t* dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t K,
+                               int fmt, const int32_t* gather, const int32_t* count, void* packed,
+                               int32_t* dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_dequantize(const void* packed, int64_t batch, int64_t rows, int64_t K,
+                                 int fmt, void* out, int dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
+                           int64_t batch, int64_t rows, int64_t K, int fmt, void* packed,
+                           int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_product(const void* x, int x_dtype, bool xq, int64_t M, const void* packed,
+                              int fmt, int64_t N, int64_t K, void* y, int y_dtype,
+                              int32_t* dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_route(const void* logits, int dtype, int64_t T, int E, const float* bias,
+                         int score, int groups, int top_groups, int group_best, int top_k,
+                         int renormalize, float scale, int32_t* ids, float* weights,
+                         int32_t* dev_status, cudaStream_t stream);
+int64_t moe_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F, int fmt);
+cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t* ids,
+                              const float* weights, int top_k, int E, const void* gate,
+                              const void* up, const void* down, int fmt, int64_t D, int64_t F,
+                              void* y, void* workspace, int32_t* dev_status, int num_sms,
+                              cudaStream_t stream);
 int64_t gemv_workspace_bytes(int64_t M, int64_t N);
 void gemv_plan(int64_t N, int64_t K, int num_sms, int32_t* out);
 int64_t gemm_counter_bytes(int64_t M, int64_t N);
@@ -502,6 +523,164 @@ lutq_status lutq_gemm_typed(const void* x_bf16, int64_t M, const void* packed,
   if ((st = current_sms(&sms)) != LUTQ_OK) return st;
   return from_cuda(lutq::launch_gemm(x_bf16, M, packed, codebooks_bf16, bits, N, K, y, workspace,
                                      dev_status, sms, static_cast<cudaStream_t>(stream), types));
+}
+
+// ---- microscaled 4-bit floating point and experts ---------------------------
+
+static bool mx_format_ok(int format) { return format == LUTQ_MXFP4 || format == LUTQ_NVFP4; }
+static bool dtype_ok(int dtype) {
+  return dtype == LUTQ_BF16 || dtype == LUTQ_FP16 || dtype == LUTQ_FP32;
+}
+// Element coordinates of the tensor maps and tile counts are 32-bit.
+static bool mx_shape_ok(int64_t N, int64_t K) {
+  return N >= 1 && N < (int64_t(1) << 30) && K >= 32 && K % 32 == 0 && K < (int64_t(1) << 30);
+}
+
+int64_t lutq_mx_packed_bytes(int64_t N, int64_t K, int format) {
+  LUTQ_TRACE_RANGE("lutq_mx_packed_bytes");
+  if (!mx_format_ok(format) || !mx_shape_ok(N, K)) return -1;
+  return lutq::mx_bytes(N, K, format);
+}
+
+static lutq_status check_mx(int64_t batch, int64_t N, int64_t K, int format) {
+  if (!mx_format_ok(format)) return LUTQ_ERR_INVALID_ARG;
+  if (batch < 0 || batch > 65535 || N < 0 || !mx_shape_ok(N == 0 ? 1 : N, K)) return LUTQ_ERR_SHAPE;
+  return LUTQ_OK;
+}
+
+lutq_status lutq_mx_quantize(const void* W, int dtype, int64_t batch, int64_t N, int64_t K,
+                             int format, void* packed, int32_t* dev_status, void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_quantize");
+  lutq_status st = check_mx(batch, N, K, format);
+  if (st != LUTQ_OK) return st;
+  if (!dtype_ok(dtype)) return LUTQ_ERR_INVALID_ARG;
+  if (batch == 0 || N == 0) return LUTQ_OK;
+  if (!W || !packed) return LUTQ_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(packed)) return LUTQ_ERR_ALIGN;
+  int sms = 0;
+  if ((st = current_sms(&sms)) != LUTQ_OK) return st;
+  return from_cuda(lutq::launch_mx_quantize(W, dtype, batch, N, K, format, nullptr, nullptr,
+                                            packed, dev_status, sms,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+lutq_status lutq_mx_dequantize(const void* packed, int64_t batch, int64_t N, int64_t K, int format,
+                               void* out, int dtype, void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_dequantize");
+  lutq_status st = check_mx(batch, N, K, format);
+  if (st != LUTQ_OK) return st;
+  if (!dtype_ok(dtype)) return LUTQ_ERR_INVALID_ARG;
+  if (batch == 0 || N == 0) return LUTQ_OK;
+  if (!packed || !out) return LUTQ_ERR_INVALID_ARG;
+  if (!aligned16(packed) || !aligned16(out)) return LUTQ_ERR_ALIGN;
+  int sms = 0;
+  if ((st = current_sms(&sms)) != LUTQ_OK) return st;
+  return from_cuda(lutq::launch_mx_dequantize(packed, batch, N, K, format, out, dtype, sms,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+lutq_status lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
+                         int64_t batch, int64_t N, int64_t K, int format, void* packed,
+                         void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_pack");
+  lutq_status st = check_mx(batch, N, K, format);
+  if (st != LUTQ_OK) return st;
+  if (batch == 0 || N == 0) return LUTQ_OK;
+  if (!codes || !scales || !packed) return LUTQ_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(packed) || !aligned16(row_scales))
+    return LUTQ_ERR_ALIGN;
+  int sms = 0;
+  if ((st = current_sms(&sms)) != LUTQ_OK) return st;
+  return from_cuda(lutq::launch_mx_pack(codes, scales, row_scales, batch, N, K, format, packed,
+                                        sms, static_cast<cudaStream_t>(stream)));
+}
+
+static lutq_status mx_product(const void* x, int x_dtype, bool values, int64_t M,
+                              const void* packed, int64_t N, int64_t K, int format, void* y,
+                              int y_dtype, int32_t* dev_status, void* stream) {
+  if (!mx_format_ok(format) || !dtype_ok(y_dtype) || !dtype_ok(x_dtype))
+    return LUTQ_ERR_INVALID_ARG;
+  if (!mx_shape_ok(N, K) || M < 0 || M > (values ? 16 : (int64_t(1) << 30) - 1))
+    return LUTQ_ERR_SHAPE;
+  if (M == 0) return LUTQ_OK;
+  if (!x || !packed || !y) return LUTQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(y)) return LUTQ_ERR_ALIGN;
+  int sms = 0;
+  lutq_status st = current_sms(&sms);
+  if (st != LUTQ_OK) return st;
+  return from_cuda(lutq::launch_mx_product(x, x_dtype, values, M, packed, format, N, K, y, y_dtype,
+                                           dev_status, sms, static_cast<cudaStream_t>(stream)));
+}
+
+lutq_status lutq_mx_gemm(const void* x_packed, int64_t M, const void* packed, int64_t N, int64_t K,
+                         int format, void* y, int y_dtype, int32_t* dev_status, void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_gemm");
+  return mx_product(x_packed, LUTQ_BF16, false, M, packed, N, K, format, y, y_dtype, dev_status,
+                    stream);
+}
+
+lutq_status lutq_mx_gemv(const void* x, int x_dtype, int64_t M, const void* packed, int64_t N,
+                         int64_t K, int format, void* y, int y_dtype, int32_t* dev_status,
+                         void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_gemv");
+  return mx_product(x, x_dtype, true, M, packed, N, K, format, y, y_dtype, dev_status, stream);
+}
+
+lutq_status lutq_route(const void* logits, int dtype, int64_t T, int E, const float* bias,
+                       int score, int groups, int top_groups, int group_best, int top_k,
+                       int renormalize, float scale, int32_t* ids, float* weights,
+                       int32_t* dev_status, void* stream) {
+  LUTQ_TRACE_RANGE("lutq_route");
+  if (!dtype_ok(dtype) || (score != LUTQ_SCORE_SOFTMAX && score != LUTQ_SCORE_SIGMOID))
+    return LUTQ_ERR_INVALID_ARG;
+  if (T < 0 || T > (int64_t(1) << 31) || E < 1 || E > 1024 || groups < 1 || groups > 32 ||
+      E % groups != 0 || top_groups < 1 || top_groups > groups || group_best < 1 ||
+      group_best > 2 || top_k < 1 || top_k > 32 || top_k > top_groups * (E / groups))
+    return LUTQ_ERR_SHAPE;
+  if (T == 0) return LUTQ_OK;
+  if (!logits || !ids || !weights) return LUTQ_ERR_INVALID_ARG;
+  auto off = [](const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) != 0; };
+  if (off(logits, dtype == LUTQ_FP32 ? 4 : 2) || off(bias, 4) || off(ids, 4) || off(weights, 4))
+    return LUTQ_ERR_ALIGN;
+  return from_cuda(lutq::launch_route(logits, dtype, T, E, bias, score, groups, top_groups,
+                                      group_best, top_k, renormalize != 0, scale, ids, weights,
+                                      dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+static bool experts_shape_ok(int64_t T, int top_k, int E, int64_t D, int64_t F) {
+  return T >= 0 && top_k >= 1 && top_k <= 64 && E >= 1 && E <= 1024 && mx_shape_ok(D, D) &&
+         mx_shape_ok(F, F) && T <= (int64_t(1) << 24) && T * top_k <= (int64_t(1) << 24);
+}
+
+int64_t lutq_mx_experts_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F,
+                                        int format) {
+  LUTQ_TRACE_RANGE("lutq_mx_experts_workspace_bytes");
+  if (!mx_format_ok(format) || !experts_shape_ok(T, top_k, E, D, F)) return -1;
+  return T == 0 ? 0 : lutq::moe_workspace_bytes(T, top_k, E, D, F, format);
+}
+
+lutq_status lutq_mx_experts(const void* x, int dtype, int64_t T, const int32_t* ids,
+                            const float* weights, int top_k, int E, const void* gate,
+                            const void* up, const void* down, int64_t D, int64_t F, int format,
+                            void* y, void* workspace, int64_t workspace_bytes,
+                            int32_t* dev_status, void* stream) {
+  LUTQ_TRACE_RANGE("lutq_mx_experts");
+  if (!mx_format_ok(format) || !dtype_ok(dtype)) return LUTQ_ERR_INVALID_ARG;
+  if (!experts_shape_ok(T, top_k, E, D, F)) return LUTQ_ERR_SHAPE;
+  if (T == 0) return LUTQ_OK;
+  if (!x || !ids || !weights || !gate || !up || !down || !y) return LUTQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(gate) || !aligned16(up) || !aligned16(down) || !aligned16(y) ||
+      !aligned16(workspace) || reinterpret_cast<uintptr_t>(ids) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(weights) % 4 != 0)
+    return LUTQ_ERR_ALIGN;
+  if (!workspace || workspace_bytes < lutq::moe_workspace_bytes(T, top_k, E, D, F, format))
+    return LUTQ_ERR_WORKSPACE;
+  int sms = 0;
+  lutq_status st = current_sms(&sms);
+  if (st != LUTQ_OK) return st;
+  return from_cuda(lutq::launch_mx_experts(x, dtype, T, ids, weights, top_k, E, gate, up, down,
+                                           format, D, F, y, workspace, dev_status, sms,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

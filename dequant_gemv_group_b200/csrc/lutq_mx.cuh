@@ -1,0 +1,171 @@
+// Microscaled 4-bit floating point: the packed layout and the conversions
+// shared by the quantizer, the products and the experts' layer.
+//
+// An element is E2M1 (sign, levels 0 .5 1 1.5 2 3 4 6); a block of consecutive
+// elements along K shares a scale byte: mxfp4 has blocks of 32 and E8M0 scales
+// (2^(byte - 127), 0xFF = NaN), nvfp4 blocks of 16, E4M3 scales and one fp32
+// scale per row.
+//
+// Packed layout of a matrix of `rows` x K (K % 32 == 0):
+//   codes   rows * K / 2 bytes, row-major, element 2i in the low nibble;
+//           padded to 128 bytes;
+//   scales  [ceil(rows/128)][ceil(K/256)] chunks, each of 2 (mxfp4) or 4
+//           (nvfp4) blocks of 512 bytes; a block holds four scales along K of
+//           each of 128 rows: row r, scale j at byte 16 (r % 32) + 4 (r / 32)
+//           + j.  Tensor memory takes such a block in one copy (32 lanes of
+//           four 32-bit columns).  Bytes of rows and columns beyond the
+//           matrix are zero, so that a padded product adds 0 * 0;
+//   rows    nvfp4: fp32 [rows], padded to 128 bytes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "lutq_common.cuh"
+
+namespace lutq {
+
+constexpr int kMxChunk = 256;     // elements of K per scale chunk (128 bytes of codes)
+constexpr int kMxRowTile = 128;   // rows per scale block
+
+__host__ __device__ constexpr int mx_block(int fmt) { return fmt == LUTQ_MXFP4 ? 32 : 16; }
+__host__ __device__ constexpr int mx_chunk_bytes(int fmt) { return fmt == LUTQ_MXFP4 ? 1024 : 2048; }
+__host__ __device__ constexpr int64_t mx_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ constexpr int64_t mx_scale_off(int64_t rows, int64_t K) {
+  return mx_ceil(rows * (K / 2), 128) * 128;
+}
+__host__ __device__ constexpr int64_t mx_row_off(int64_t rows, int64_t K, int fmt) {
+  return mx_scale_off(rows, K) +
+         mx_ceil(rows, kMxRowTile) * mx_ceil(K, kMxChunk) * mx_chunk_bytes(fmt);
+}
+__host__ __device__ constexpr int64_t mx_bytes(int64_t rows, int64_t K, int fmt) {
+  return mx_row_off(rows, K, fmt) + (fmt == LUTQ_NVFP4 ? mx_ceil(rows, 32) * 128 : 0);
+}
+
+// Eight floats to eight E2M1 codes (round to nearest, ties to the even code,
+// saturating at 6), element 0 in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1_x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// The value of E2M1 code c (0..15).
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t m = c & 7u;
+  // codes 2..7: exponent (m >> 1) - 1, one mantissa bit; code 1 is 0.5
+  const float a = m < 2u ? 0.5f * float(m) : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
+  return (c & 8u) ? -a : a;
+}
+
+// One float >= 0 to E4M3 (round to nearest even, saturating at 448).
+__device__ __forceinline__ uint32_t e4m3_byte(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
+  return r & 0xffu;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(uint16_t(b)));
+  return __half2float(__ushort_as_half(uint16_t(h2)));
+}
+
+// E8M0: the scale's exponent byte from the block's largest magnitude (as fp32
+// bits): floor(log2 amax) - 2 + 127, at least 0 (a subnormal amax is far below
+// 2^-125).
+__device__ __forceinline__ uint32_t e8m0_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e > 2u ? e - 2u : 0u;
+}
+// 2^(127 - byte) for byte <= 252: the exact reciprocal of the scale.
+__device__ __forceinline__ float e8m0_inverse(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  // 2^-127 is subnormal; 0xFF stands for NaN
+  return byte == 0u ? __uint_as_float(0x00400000u)
+                    : (byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(byte << 23));
+}
+
+// nvfp4's row scale: 2^(floor(log2 m) - 10) of the row's largest finite
+// magnitude m (1 for a row of zeros), at least 2^-126.  Then m / 6 / g lies in
+// [170, 342), inside E4M3's range.  A power of two keeps s * g, m / g and so
+// every rounding decision on 16-bit inputs exact in fp32.
+__device__ __forceinline__ float nv_row_scale(uint32_t max_bits) {
+  if (max_bits == 0u) return 1.f;
+  const uint32_t e = max_bits >> 23;
+  return __uint_as_float((e > 11u ? e - 10u : 1u) << 23);
+}
+__device__ __forceinline__ float nv_row_scale_inverse(float g) {
+  return __uint_as_float((254u - (__float_as_uint(g) >> 23)) << 23);
+}
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Eight consecutive values of a row as fp32 from global memory (16 bytes of
+// bf16 or fp16, 32 of fp32); the address is 16-byte aligned.
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+  if constexpr (DT == LUTQ_FP32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == LUTQ_BF16) {
+        v[2 * j] = bf16_lo_to_f32(w[j]);
+        v[2 * j + 1] = bf16_hi_to_f32(w[j]);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Value v rounded once to the output type, at element i of y.
+template <int DT>
+__device__ __forceinline__ void store1(void* y, int64_t i, float v) {
+  if constexpr (DT == LUTQ_FP32) {
+    static_cast<float*>(y)[i] = v;
+  } else if constexpr (DT == LUTQ_BF16) {
+    static_cast<uint16_t*>(y)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  } else {
+    static_cast<uint16_t*>(y)[i] = __half_as_ushort(__float2half_rn(v));
+  }
+}
+
+// Launch with the next kernel of the stream allowed to start early: every
+// kernel of this family waits for the one before it (griddepcontrol.wait)
+// before it reads or writes anything.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+}  // namespace lutq

@@ -1,0 +1,249 @@
+// A mixture-of-experts feed-forward layer on microscaled 4-bit weights:
+//   y[t] = sum_j weights[t, j] * W_down_e (silu(W_gate_e x[t]) * (W_up_e x[t])),
+//   e = ids[t, j],
+// with x and the hidden values quantized like the weights, so that both
+// products run on the tensor cores as they are (lutq_mx_gemm.cu).
+//
+// (token, choice) pairs are laid out by expert: expert e's rows begin at a
+// multiple of 128 (the height of a scale block) and keep the order of the
+// pairs.  Steps, each one launch: plan (rows of every expert), x quantized
+// into its rows, gate and up product with silu, hidden values quantized, down
+// product, weighted sum over a token's choices in their order.  Rows do not
+// depend on one another, so a token's result does not depend on its batch.
+#include <algorithm>
+#include <cstring>
+
+#include "lutq_mx_gemm.cuh"
+
+namespace lutq {
+
+constexpr int kPlanThreads = 512;
+
+// The plan of a call (int32 arrays in the workspace).
+struct MoePlan {
+  int32_t* counts;  // [E] rows of an expert
+  int32_t* bases;   // [E] its first row
+  int32_t* total;   // rows in use, padding included
+  int32_t* slot;    // [pairs] a pair's row, or -1 (id outside 0..E-1)
+  int32_t* source;  // [cap] a row's token, or -1 (padding)
+  int32_t* self;    // [cap] the row itself, or -1
+};
+
+// Block e: counts every expert's pairs (shared-memory histogram), adds up the
+// rows before its own, then hands out its rows: each thread owns a run of
+// pairs, so a scan over the threads' counts keeps the pairs' order.
+__global__ void __launch_bounds__(kPlanThreads)
+    moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int top_k, int E, MoePlan p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ int32_t hist[];
+  __shared__ int32_t warp_sum[kPlanThreads / 32];
+  __shared__ int32_t base_s;
+  const int e = blockIdx.x, th = threadIdx.x, lane = th & 31, warp = th >> 5;
+  for (int i = th; i < E; i += kPlanThreads) hist[i] = 0;
+  if (th == 0) base_s = 0;
+  __syncthreads();
+  for (int i = th; i < pairs; i += kPlanThreads) {
+    const int id = ids[i];
+    if (uint32_t(id) < uint32_t(E)) atomicAdd(&hist[id], 1);
+    else if (e == 0) p.slot[i] = -1;
+  }
+  __syncthreads();
+  int before = 0;
+  for (int i = th; i < e; i += kPlanThreads) before += (hist[i] + 127) / 128 * 128;
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) atomicAdd(&base_s, before);
+  __syncthreads();
+  const int base = base_s, count = hist[e], padded = (count + 127) / 128 * 128;
+  if (th == 0) {
+    p.counts[e] = count;
+    p.bases[e] = base;
+    if (e == E - 1) *p.total = base + padded;
+  }
+  if (count == 0) return;
+  const int per = (pairs + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = th * per, i1 = min(pairs, i0 + per);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) mine += ids[i] == e;
+  int scan = mine;
+  for (int x = 1; x < 32; x *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, x);
+    if (lane >= x) scan += v;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  int row = base + scan - mine;
+  for (int w = 0; w < warp; ++w) row += warp_sum[w];
+  for (int i = i0; i < i1; ++i)
+    if (ids[i] == e) {
+      p.slot[i] = row;
+      p.source[row] = i / top_k;
+      p.self[row] = row;
+      ++row;
+    }
+  for (int i = count + th; i < padded; i += kPlanThreads) {
+    p.source[base + i] = -1;
+    p.self[base + i] = -1;
+  }
+}
+
+// y[t] = sum_j weights[t, j] * out[slot[t, j]] in fp32, rounded once.
+template <int DT>
+__global__ void __launch_bounds__(256)
+    moe_combine_kernel(const float* __restrict__ out, const int32_t* __restrict__ slot,
+                       const float* __restrict__ weights, int top_k, int64_t D, void* y) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t t = blockIdx.x;
+  const int64_t d = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  if (d >= D) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < top_k; ++j) {
+    const int r = slot[t * top_k + j];
+    if (r < 0) continue;
+    const float w = weights[t * top_k + j];
+    const float4 v = *reinterpret_cast<const float4*>(out + int64_t(r) * D + d);
+    s.x += w * v.x;
+    s.y += w * v.y;
+    s.z += w * v.z;
+    s.w += w * v.w;
+  }
+  store1<DT>(y, t * D + d, s.x);
+  store1<DT>(y, t * D + d + 1, s.y);
+  store1<DT>(y, t * D + d + 2, s.z);
+  store1<DT>(y, t * D + d + 3, s.w);
+}
+
+// ------------------------------------------------------------------ host side
+
+cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t K,
+                               int fmt, const int32_t* gather, const int32_t* count, void* packed,
+                               int32_t* dev_status, int num_sms, cudaStream_t stream);
+
+// Rows of all experts at most: every pair, and each expert in use padded to 128.
+static int64_t moe_rows(int64_t T, int top_k, int E) {
+  const int64_t pairs = T * top_k;
+  return mx_ceil(pairs + 127 * std::min<int64_t>(E, pairs), 128) * 128;
+}
+
+struct MoeSpace {
+  int64_t counts, bases, total, slot, source, self, xq, h, hq, out, bytes;
+};
+static MoeSpace moe_space(int64_t T, int top_k, int E, int64_t D, int64_t F, int fmt) {
+  const int64_t cap = moe_rows(T, top_k, E);
+  MoeSpace s;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += mx_ceil(bytes, 256) * 256;
+    return here;
+  };
+  s.counts = take(4 * int64_t(E));
+  s.bases = take(4 * int64_t(E));
+  s.total = take(4);
+  s.slot = take(4 * T * top_k);
+  s.source = take(4 * cap);
+  s.self = take(4 * cap);
+  s.xq = take(mx_bytes(cap, D, fmt));
+  s.h = take(2 * cap * F);
+  s.hq = take(mx_bytes(cap, F, fmt));
+  s.out = take(4 * cap * D);
+  s.bytes = at;
+  return s;
+}
+int64_t moe_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F, int fmt) {
+  return moe_space(T, top_k, E, D, F, fmt).bytes;
+}
+
+cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t* ids,
+                              const float* weights, int top_k, int E, const void* gate,
+                              const void* up, const void* down, int fmt, int64_t D, int64_t F,
+                              void* y, void* workspace, int32_t* dev_status, int num_sms,
+                              cudaStream_t stream) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const MoeSpace s = moe_space(T, top_k, E, D, F, fmt);
+  auto ints = [&](int64_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+  const MoePlan p = {ints(s.counts), ints(s.bases),  ints(s.total),
+                     ints(s.slot),   ints(s.source), ints(s.self)};
+  const int64_t cap = moe_rows(T, top_k, E);
+  const int pairs = int(T * top_k);
+  // tokens per tile: an expert has at most T rows, T top_k / E on average
+  const int64_t mean = mx_ceil(pairs, E);
+  const int nt = T <= 16 ? 16 : mean <= 32 ? 32 : 128;
+  CUtensorMap up_maps[3], down_maps[3];
+  std::memset(up_maps, 0, sizeof(up_maps));
+  std::memset(down_maps, 0, sizeof(down_maps));
+  const int64_t w1 = mx_bytes(F, D, fmt), w2 = mx_bytes(D, F, fmt);
+  cudaError_t err;
+  if ((err = make_mx_map(&up_maps[0], gate, F, D, E, w1, 128)) != cudaSuccess) return err;
+  if ((err = make_mx_map(&up_maps[1], up, F, D, E, w1, 128)) != cudaSuccess) return err;
+  if ((err = make_mx_map(&up_maps[2], ws + s.xq, cap, D, 1, mx_bytes(cap, D, fmt), nt)) !=
+      cudaSuccess)
+    return err;
+  if ((err = make_mx_map(&down_maps[0], down, D, F, E, w2, 128)) != cudaSuccess) return err;
+  down_maps[1] = down_maps[0];
+  if ((err = make_mx_map(&down_maps[2], ws + s.hq, cap, F, 1, mx_bytes(cap, F, fmt), nt)) !=
+      cudaSuccess)
+    return err;
+
+  if ((err = launch_pdl(moe_plan_kernel, dim3(unsigned(E)), dim3(kPlanThreads), size_t(E) * 4,
+                        stream, ids, pairs, top_k, E, p)) != cudaSuccess)
+    return err;
+  if ((err = launch_mx_quantize(x, dtype, 1, cap, D, fmt, p.source, p.total, ws + s.xq,
+                                dev_status, num_sms, stream)) != cudaSuccess)
+    return err;
+
+  MxGemmArgs a = {};
+  a.dev_status = dev_status;
+  a.counts = p.counts;
+  a.bases = p.bases;
+  a.experts = E;
+  a.M = cap;
+  // tiles at most: an expert in use has one row tile of tokens at least
+  const int64_t token_tiles = std::min<int64_t>(E, pairs) + pairs / nt;
+  auto bytes = [](const void* q, int64_t off) { return static_cast<const uint8_t*>(q) + off; };
+  a.a_scales[0] = bytes(gate, mx_scale_off(F, D));
+  a.a_scales[1] = bytes(up, mx_scale_off(F, D));
+  a.a_rows[0] = reinterpret_cast<const float*>(bytes(gate, mx_row_off(F, D, fmt)));
+  a.a_rows[1] = reinterpret_cast<const float*>(bytes(up, mx_row_off(F, D, fmt)));
+  a.a_stride = w1;
+  a.b_scales = ws + s.xq + mx_scale_off(cap, D);
+  a.b_rows = reinterpret_cast<const float*>(ws + s.xq + mx_row_off(cap, D, fmt));
+  a.y = ws + s.h;
+  a.N = F;
+  a.K = D;
+  a.chunks = int(mx_ceil(D, kMxChunk));
+  a.mtiles = int(mx_ceil(F, 128));
+  int split, clusters;
+  mx_split(token_tiles * a.mtiles, a.chunks, nt, true, num_sms, &split, &clusters);
+  if ((err = launch_mx_gemm(up_maps, a, fmt, kMxGateUp, nt, split, clusters, false, stream)) !=
+      cudaSuccess)
+    return err;
+  if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, cap, F, fmt, p.self, p.total, ws + s.hq,
+                                dev_status, num_sms, stream)) != cudaSuccess)
+    return err;
+
+  a.a_scales[0] = a.a_scales[1] = bytes(down, mx_scale_off(D, F));
+  a.a_rows[0] = a.a_rows[1] = reinterpret_cast<const float*>(bytes(down, mx_row_off(D, F, fmt)));
+  a.a_stride = w2;
+  a.b_scales = ws + s.hq + mx_scale_off(cap, F);
+  a.b_rows = reinterpret_cast<const float*>(ws + s.hq + mx_row_off(cap, F, fmt));
+  a.y = ws + s.out;
+  a.N = D;
+  a.K = F;
+  a.chunks = int(mx_ceil(F, kMxChunk));
+  a.mtiles = int(mx_ceil(D, 128));
+  mx_split(token_tiles * a.mtiles, a.chunks, nt, false, num_sms, &split, &clusters);
+  if ((err = launch_mx_gemm(down_maps, a, fmt, kMxDown, nt, split, clusters, false, stream)) !=
+      cudaSuccess)
+    return err;
+  auto combine = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 1024))), dim3(256), 0, stream,
+                      reinterpret_cast<const float*>(ws + s.out), p.slot, weights, top_k, D, y);
+  };
+  return dtype == LUTQ_BF16   ? combine(moe_combine_kernel<LUTQ_BF16>)
+         : dtype == LUTQ_FP16 ? combine(moe_combine_kernel<LUTQ_FP16>)
+                              : combine(moe_combine_kernel<LUTQ_FP32>);
+}
+
+}  // namespace lutq

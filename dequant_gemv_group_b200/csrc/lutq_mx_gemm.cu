@@ -1,0 +1,664 @@
+// Products of microscaled 4-bit matrices on the tensor cores (tcgen05.mma
+// with block scales): y[m, n] = sum_k x[m, k] w[n, k], both operands E2M1.
+//
+// The tensor core multiplies the codes and applies both scales itself, so
+// nothing is dequantized: the kernel only moves bytes.  A tile is 128 rows of
+// the weight matrix (the lanes of tensor memory) by NT tokens (its columns);
+// taking the weights as the first operand keeps the tile narrow for small
+// batches, and a warp's 32 lanes are 32 neighbouring outputs of one token.
+// A stage is 256 elements of K: 128 bytes a row of each operand by tensor-map
+// copies with the 128-byte swizzle, the scale chunks by bulk copies, and per
+// stage four MMAs of 64 elements.  Scale blocks go from shared memory to
+// tensor memory with one copy instruction each, ordered before the MMAs.
+//
+// A cluster of `split` blocks shares a tile by K: block r takes chunks
+// [C r / split, C (r+1) / split), and each block sums its share of the columns
+// over the cluster through distributed shared memory, in rank order, so that
+// results do not depend on timing and no workspace is needed.
+//
+// Warps: 0 copies, 1 issues, 2..5 read tensor memory and write y, 6..9 (token
+// values quantized in the kernel) turn x into the second operand's codes.
+#include "lutq_mx_gemm.cuh"
+
+#include <algorithm>
+#include <cstring>
+
+#include "lutq_sm100.cuh"
+
+namespace lutq {
+
+using namespace sm100;
+
+constexpr uint64_t kMxWaitNs = 2000000000ull;
+constexpr int kMxMaxStages = 8;
+constexpr int kMxMaxExperts = 1024;
+constexpr int kMxEpiWarp = 2, kMxQuantWarp = 6;
+
+template <int FMT, int NT, int MODE>
+struct MxCfg {
+  static constexpr int ND = MODE == kMxGateUp ? 2 : 1;     // weight matrices a tile multiplies
+  static constexpr int CH = mx_chunk_bytes(FMT);
+  static constexpr int BLOCKS = CH / 512;                  // scale blocks per chunk
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = NT * 128;
+  static constexpr int STAGE = ND * A_BYTES + B_BYTES + (ND + 1) * CH;
+  static constexpr int RECV = ND * NT * 128 * 4;           // partial sums of a split tile
+  // tensor memory: accumulators (two sets where they fit), then two sets of scales
+  static constexpr int SF_COLS = 2 * (ND + 1) * BLOCKS * 4;
+  static constexpr int ACC = 2 * ND * NT + SF_COLS <= 512 ? 2 : 1;
+  static constexpr int COLS = ACC * ND * NT + SF_COLS;
+  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+};
+
+// Shared memory behind the stages: barriers, flags, small tables.
+struct MxShared {
+  uint64_t full[kMxMaxStages], empty[kMxMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t part_full, part_empty, max_full, drain;
+  uint32_t tmem;
+  int abort;
+  uint32_t row_max[8][16];   // the cluster's largest magnitudes per token (nvfp4)
+  float row_scale[16];       // tokens quantized here: their row scales
+};
+
+// Walks the tiles t = first, first + step, ... of a launch: plain products go
+// over the row tiles first, experts' over each expert's tiles in turn.
+template <int MODE>
+struct MxTiles {
+  const int32_t* counts;
+  int mtiles, nt, experts, e = 0, e_tiles = 0;
+  int64_t e_first = 0, tokens;
+  __device__ MxTiles(const MxGemmArgs& a, int nt_, const int32_t* counts_)
+      : counts(counts_), mtiles(a.mtiles), nt(nt_), experts(a.experts), tokens(a.M) {
+    if (MODE != kMxPlain) e_tiles = int(mx_ceil(counts[0], nt)) * mtiles;
+  }
+  // false: no tile t; else its expert, row tile, first token and tokens
+  __device__ bool at(int64_t t, int* expert, int* mt, int* m0, int* valid) {
+    if constexpr (MODE == kMxPlain) {
+      const int64_t n = t / mtiles;
+      if (n * nt >= tokens) return false;
+      *expert = 0;
+      *mt = int(t - n * mtiles);
+      *m0 = int(n * nt);
+      *valid = int(min(int64_t(nt), tokens - n * nt));
+      return true;
+    } else {
+      while (t >= e_first + e_tiles) {
+        e_first += e_tiles;
+        if (++e >= experts) {
+          e = experts - 1;
+          e_tiles = 0;
+          return false;
+        }
+        e_tiles = int(mx_ceil(counts[e], nt)) * mtiles;
+      }
+      const int i = int(t - e_first), n = i / mtiles;
+      *expert = e;
+      *mt = i - n * mtiles;
+      *m0 = n * nt;
+      *valid = min(nt, counts[e] - n * nt);
+      return true;
+    }
+  }
+};
+
+__device__ __forceinline__ void store_any(void* y, int dtype, int64_t i, float v) {
+  if (dtype == LUTQ_FP32) store1<LUTQ_FP32>(y, i, v);
+  else if (dtype == LUTQ_BF16) store1<LUTQ_BF16>(y, i, v);
+  else store1<LUTQ_FP16>(y, i, v);
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g / (1.f + __expf(-g)) * u;
+}
+
+// Bounded wait for work already in flight, whatever the abort flag says.
+__device__ __forceinline__ void mx_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_ns() - t0 > kMxWaitNs) return;
+}
+
+template <int FMT, int NT, int MODE, bool XQ>
+__global__ void __launch_bounds__(XQ ? 320 : 192)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                   const __grid_constant__ CUtensorMap tmap_a2,
+                   const __grid_constant__ CUtensorMap tmap_b, const MxGemmArgs a, int split) {
+  using Cfg = MxCfg<FMT, NT, MODE>;
+  constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int ST = a.stages;
+  float* recv = reinterpret_cast<float*>(smem + ST * Cfg::STAGE);
+  MxShared* sh = reinterpret_cast<MxShared*>(smem + ST * Cfg::STAGE + (split > 1 ? Cfg::RECV : 0));
+  int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);  // experts' row counts, then bases
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &sh->abort;
+  auto full = [&](int s) { return smem_addr(&sh->full[s]); };
+  auto empty = [&](int s) { return smem_addr(&sh->empty[s]); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full(s), XQ ? 5 : 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&sh->acc_full[b]), 1);
+      mbar_init(smem_addr(&sh->acc_empty[b]), 4);
+    }
+    mbar_init(smem_addr(&sh->part_full), 4 * split);
+    mbar_init(smem_addr(&sh->part_empty), 4 * split);
+    mbar_init(smem_addr(&sh->max_full), 4 * split);
+    mbar_init(smem_addr(&sh->drain), 1);
+    sh->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sh->tmem), Cfg::TMEM);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (MODE != kMxPlain) {
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+      counts[e] = a.counts[e];
+      counts[a.experts + e] = a.bases[e];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (split > 1) cluster_sync_all();  // every block's barriers are set up
+  const uint32_t tmem = sh->tmem;
+  const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
+  const int64_t first = blockIdx.x / split, step = gridDim.x / split;
+  const int c0 = int(int64_t(a.chunks) * rank / split);
+  const int c1 = int(int64_t(a.chunks) * (rank + 1) / split);
+  MxTiles<MODE> tiles(a, NT, counts);
+  int expert, mt, m0, valid;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
+        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+        const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
+        const uint8_t* bs = a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
+        for (int c = c0; c < c1; ++c) {
+          if (!(ok = mbar_wait(empty(s), ph, abort, kMxWaitNs))) break;
+          const uint32_t st = sbase + s * Cfg::STAGE;
+          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
+          mbar_expect_tx(full(s), ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : Cfg::B_BYTES + CH));
+          tma_3d_g2s(st, &tmap_a, c * 128, mt * 128, expert, full(s));
+          bulk_g2s(sf, a.a_scales[0] + a_off + int64_t(c) * CH, CH, full(s));
+          if (ND == 2) {
+            tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, c * 128, mt * 128, expert, full(s));
+            bulk_g2s(sf + CH, a.a_scales[1] + a_off + int64_t(c) * CH, CH, full(s));
+          }
+          if (!XQ) {
+            tma_3d_g2s(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0, 0, full(s));
+            bulk_g2s(sf + ND * CH, bs + int64_t(c) * CH, CH, full(s));
+          }
+          ++issued;
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // given up: the copies in flight must land before the block may exit
+      if (*abort) {
+        const int64_t n = issued < ST ? issued : ST;
+        for (int64_t i = issued - n; i < issued; ++i)
+          if (!XQ) mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
+        if (XQ) {
+          // the quantizing warps may not arrive any more: arrive for them,
+          // so that the barrier follows the copies alone
+          for (int64_t i = issued - n; i < issued; ++i) {
+            for (int w = 0; w < 4; ++w) mbar_arrive(full(int(i % ST)));
+            mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      constexpr bool E8 = FMT == LUTQ_MXFP4;
+      int s = 0, it = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true, any = false;
+      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+        const int b = Cfg::ACC == 2 ? n & 1 : 0;
+        const uint32_t use = uint32_t(Cfg::ACC == 2 ? n >> 1 : n);
+        if (!(ok = mbar_wait(smem_addr(&sh->acc_empty[b]), (use & 1u) ^ 1u, abort, kMxWaitNs)))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(b * ND * NT);
+        // tokens below the first row of a 128-row scale tile: their columns
+        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+        const uint32_t sb_shift = XQ ? 0u : uint32_t(row0 % kMxRowTile) / 32u;
+        for (int c = c0; c < c1; ++c, ++it) {
+          if (!(ok = mbar_wait(full(s), ph, abort, kMxWaitNs))) break;
+          tc_fence_after();
+          const uint32_t st = sbase + s * Cfg::STAGE;
+          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
+          const uint32_t sf_tmem = tmem + uint32_t(Cfg::ACC * ND * NT + (it & 1) * (Cfg::SF_COLS / 2));
+#pragma unroll
+          for (int i = 0; i < (ND + 1) * BLOCKS; ++i)
+            tmem_cp_scales(sf_tmem + 4 * i, smem_desc_scales(sf + 512 * i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // mxfp4: a block holds the scales of two MMAs, nvfp4: of one
+            const int blk = E8 ? j >> 1 : j, id = E8 ? (j & 1) * 2 : 0;
+            const uint32_t idesc = idesc_e2m1(128, NT, E8, id);
+            const uint64_t bd = smem_desc_k_sw128(st + ND * Cfg::A_BYTES + 32 * j);
+            const uint32_t sb = sf_tmem + 4 * (ND * BLOCKS + blk) + sb_shift;
+#pragma unroll
+            for (int w = 0; w < ND; ++w)
+              mma_e2m1_ss<!E8>(d + w * NT, smem_desc_k_sw128(st + w * Cfg::A_BYTES + 32 * j), bd,
+                               idesc, sf_tmem + 4 * (w * BLOCKS + blk), sb,
+                               (c > c0 || j > 0) ? 1u : 0u);
+          }
+          mma_commit(empty(s));
+          any = true;
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit(smem_addr(&sh->acc_full[b]));
+      }
+      if (*abort && any) {
+        mma_commit(smem_addr(&sh->drain));
+        mx_drain(smem_addr(&sh->drain), 0);
+      }
+    }
+  } else if (warp < kMxQuantWarp) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    int n = 0;
+    bool ok = true;
+    // (NT / split) columns of the tile are this block's to sum and write
+    const int own = NT / split;
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+      const int b = Cfg::ACC == 2 ? n & 1 : 0;
+      const uint32_t use = uint32_t(Cfg::ACC == 2 ? n >> 1 : n);
+      ok = mbar_wait(smem_addr(&sh->acc_full[b]), use & 1u, abort, kMxWaitNs);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int64_t row = int64_t(mt) * 128 + quarter * 32 + lane;
+      const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(b * ND * NT);
+      float ga[2] = {1.f, 1.f};
+      if (FMT == LUTQ_NVFP4 && row < a.N) {
+#pragma unroll
+        for (int w = 0; w < ND; ++w)
+          ga[w] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.a_rows[w]) +
+                                                  int64_t(expert) * a.a_stride + row * 4);
+      }
+      auto put = [&](int m, float v0, float v1) {
+        if (FMT == LUTQ_NVFP4) {
+          const float gb = XQ ? sh->row_scale[m] : a.b_rows[token0 + m];
+          v0 = v0 * ga[0] * gb;
+          if (ND == 2) v1 = v1 * ga[1] * gb;
+        }
+        if (row >= a.N) return;
+        const int64_t i = (token0 + m) * a.N + row;
+        if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, i, silu_mul(v0, v1));
+        else if (MODE == kMxDown) store1<LUTQ_FP32>(a.y, i, v0);
+        else store_any(a.y, a.y_dtype, i, v0);
+      };
+      if (split == 1) {
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          if (c >= valid) break;
+          uint32_t v[ND][16];
+#pragma unroll
+          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x16(d + w * NT + c, v[w]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < valid)
+              put(c + j, __uint_as_float(v[0][j]), __uint_as_float(v[ND - 1][j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[b]));
+      } else {
+        // send every column to the block that sums it: recv[rank][w][column][lane]
+        ok = n == 0 || mbar_wait_cluster(smem_addr(&sh->part_empty), uint32_t(n - 1) & 1u, abort,
+                                         kMxWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t slot = smem_addr(recv) + (rank * ND * own * 128 + quarter * 32 + lane) * 4;
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          if (c >= valid) break;
+          uint32_t v[ND][16];
+#pragma unroll
+          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x16(d + w * NT + c, v[w]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int col = c + j;
+            if (col < valid) {
+              const uint32_t to = cluster_map(slot, uint32_t(col / own));
+#pragma unroll
+              for (int w = 0; w < ND; ++w)
+                cluster_st_f32(to + (w * own + col % own) * 512, __uint_as_float(v[w][j]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[b]));
+        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_full), lane));
+        ok = mbar_wait_cluster(smem_addr(&sh->part_full), uint32_t(n) & 1u, abort, kMxWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        for (int j = 0; j < own; ++j) {
+          const int col = int(rank) * own + j;
+          if (col >= valid) break;
+          float v[2] = {0.f, 0.f};
+          for (int r = 0; r < split; ++r)
+#pragma unroll
+            for (int w = 0; w < ND; ++w)
+              v[w] += recv[((r * ND + w) * own + j) * 128 + quarter * 32 + lane];
+          put(col, v[0], v[ND - 1]);
+        }
+        __syncwarp();
+        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_empty), lane));
+      }
+    }
+  } else if (XQ) {
+    // ------------------------------------------------------------ x into codes
+    // thread: token i, block of 32 elements q of each chunk
+    const int th = threadIdx.x - kMxQuantWarp * 32, i = th >> 3, q = th & 7;
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true, bad = false;
+    const int64_t esize = a.x_dtype == LUTQ_FP32 ? 4 : 2;
+    auto load32 = [&](int64_t k, float (&v)[32]) {
+      const bool in = i < a.M && k < a.K;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (in) {
+          const void* p = static_cast<const uint8_t*>(a.x) + (int64_t(i) * a.K + k + 8 * j) * esize;
+          if (a.x_dtype == LUTQ_BF16) load8<LUTQ_BF16>(p, 0, u);
+          else if (a.x_dtype == LUTQ_FP16) load8<LUTQ_FP16>(p, 0, u);
+          else load8<LUTQ_FP32>(p, 0, u);
+        }
+#pragma unroll
+        for (int l = 0; l < 8; ++l) v[8 * j + l] = u[l];
+      }
+    };
+    float g = 1.f, g_inv = 1.f;
+    if (FMT == LUTQ_NVFP4) {
+      // the token's largest finite magnitude: this block's chunks, then the cluster's
+      uint32_t m = 0;
+      for (int c = c0; c < c1; ++c) {
+        float v[32];
+        load32(int64_t(c) * kMxChunk + q * 32, v);
+#pragma unroll
+        for (int l = 0; l < 32; ++l) {
+          const uint32_t u = abs_bits(v[l]);
+          m = max(m, u < kInfBits ? u : 0u);
+        }
+      }
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+      if (split > 1) {
+        const uint32_t slot = smem_addr(&sh->row_max[rank][i]);
+        if (q < split) cluster_st_u32(cluster_map(slot, q), m);
+        __syncwarp();
+        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->max_full), lane));
+        ok = mbar_wait_cluster(smem_addr(&sh->max_full), 0, abort, kMxWaitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok)
+          for (int r = 0; r < split; ++r) m = max(m, sh->row_max[r][i]);
+      }
+      g = nv_row_scale(m);
+      g_inv = nv_row_scale_inverse(g);
+      if (q == 0) sh->row_scale[i] = g;
+    }
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
+      for (int c = c0; c < c1; ++c) {
+        float v[32];
+        const int64_t k = int64_t(c) * kMxChunk + q * 32;
+        load32(k, v);
+        uint32_t codes[4] = {0u, 0u, 0u, 0u}, sc[2] = {0u, 0u};
+        constexpr int H = FMT == LUTQ_MXFP4 ? 1 : 2;  // blocks per 32 elements
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int l = 0; l < 32 / H; ++l) m = max(m, abs_bits(v[h * 16 + l]));
+          float mul = 0.f, s4 = 0.f;
+          const bool nan = m >= kInfBits;
+          if (nan) {
+            bad = true;
+            sc[h] = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
+          } else if (FMT == LUTQ_MXFP4) {
+            sc[h] = e8m0_byte(m);
+            mul = e8m0_inverse(sc[h]);
+          } else {
+            sc[h] = e4m3_byte(__uint_as_float(m) * g_inv / 6.0f);
+            s4 = e4m3_value(sc[h]) * g;
+          }
+          if (!nan) {
+#pragma unroll
+            for (int w = 0; w < 4 / H; ++w) {
+              float u[8];
+#pragma unroll
+              for (int l = 0; l < 8; ++l) {
+                const float z = v[h * 16 + 8 * w + l];
+                u[l] = FMT == LUTQ_MXFP4 ? z * mul
+                                         : (s4 > 0.f ? __fdiv_rn(z, s4) : copysignf(0.f, z));
+              }
+              codes[h * 2 + w] = e2m1_x8(u);
+            }
+          }
+        }
+        if (k >= a.K) sc[0] = sc[1] = 0u;
+        ok = mbar_wait(empty(s), ph, abort, kMxWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * Cfg::STAGE;
+        *reinterpret_cast<uint4*>(st + ND * Cfg::A_BYTES + i * 128 + ((q ^ (i & 7)) * 16)) =
+            make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        uint8_t* sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES + ND * CH;
+        if (FMT == LUTQ_MXFP4) {
+          sf[(q >> 2) * 512 + i * 16 + (q & 3)] = uint8_t(sc[0]);
+        } else {
+          *reinterpret_cast<uint16_t*>(sf + (q >> 1) * 512 + i * 16 + (q & 1) * 2) =
+              uint16_t(sc[0] | (sc[1] << 8));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(s));
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync_all();  // no block leaves while another may write to it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM);
+  }
+  if (threadIdx.x == 0 && *abort) report(a.dev_status, LUTQ_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ host side
+
+// A block that holds c of an SM's 512 columns of tensor memory asks for at
+// least c / 512 of its 228 KB of shared memory (1 KB of which a block always
+// takes), so that no two blocks of these kernels on one SM can want more
+// columns than it has: an allocation then never waits, and clusters cannot
+// wait for one another.
+static int mx_smem_floor(int cols) { return 228 * 1024 / 512 * cols - 1024; }
+constexpr int kMxSmemMax = 227 * 1024;
+
+template <int FMT, int NT, int MODE, bool XQ>
+static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int clusters,
+                              cudaStream_t stream) {
+  using Cfg = MxCfg<FMT, NT, MODE>;
+  // narrow plain tiles leave room for a second block on the SM
+  constexpr int budget = Cfg::TMEM <= 256 && Cfg::STAGE * 4 <= 104 * 1024 ? 113 * 1024 : kMxSmemMax;
+  const int fixed = 1024 + (split > 1 ? Cfg::RECV : 0) + int(sizeof(MxShared)) +
+                    (MODE != kMxPlain ? 8 * a.experts : 0);
+  a.stages = std::min(kMxMaxStages, (budget - fixed) / Cfg::STAGE);
+  if (a.stages < 2) return cudaErrorInvalidValue;
+  const int smem = std::max(fixed + a.stages * Cfg::STAGE, mx_smem_floor(Cfg::TMEM));
+  static bool granted[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kernel = mx_gemm_kernel<FMT, NT, MODE, XQ>;
+  if (!granted[dev]) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemMax);
+    if (err != cudaSuccess) return err;
+    granted[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(clusters * split));
+  cfg.blockDim = dim3(XQ ? 320 : 192);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {unsigned(split), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, t[0], t[1], t[2], a, split);
+}
+
+template <int FMT>
+static cudaError_t launch_fmt(const CUtensorMap* t, const MxGemmArgs& a, int mode, int nt,
+                              int split, int clusters, bool xq, cudaStream_t stream) {
+#define LUTQ_MX_CASE(NT, MODE, XQ) \
+  if (nt == NT && mode == MODE && xq == XQ) \
+    return launch_one<FMT, NT, MODE, XQ>(t, a, split, clusters, stream);
+  LUTQ_MX_CASE(16, kMxPlain, true)
+  LUTQ_MX_CASE(16, kMxPlain, false)
+  LUTQ_MX_CASE(32, kMxPlain, false)
+  LUTQ_MX_CASE(64, kMxPlain, false)
+  LUTQ_MX_CASE(128, kMxPlain, false)
+  LUTQ_MX_CASE(16, kMxGateUp, false)
+  LUTQ_MX_CASE(32, kMxGateUp, false)
+  LUTQ_MX_CASE(128, kMxGateUp, false)
+  LUTQ_MX_CASE(16, kMxDown, false)
+  LUTQ_MX_CASE(32, kMxDown, false)
+  LUTQ_MX_CASE(128, kMxDown, false)
+#undef LUTQ_MX_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_mx_gemm(const CUtensorMap* t, const MxGemmArgs& a, int fmt, int mode, int nt,
+                           int split, int clusters, bool xq, cudaStream_t stream) {
+  return fmt == LUTQ_MXFP4 ? launch_fmt<LUTQ_MXFP4>(t, a, mode, nt, split, clusters, xq, stream)
+                           : launch_fmt<LUTQ_NVFP4>(t, a, mode, nt, split, clusters, xq, stream);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The codes of `batch` matrices [rows, K/2 bytes], `stride` bytes apart, in
+// boxes of 128 bytes x box_rows with the 128-byte swizzle; rows and columns
+// beyond a matrix read as zero.
+cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K,
+                        int64_t batch, int64_t stride, int box_rows) {
+  static EncodeTiledFn enc = nullptr;
+  if (enc == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return cudaErrorNotSupported;
+    enc = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  const cuuint64_t dims[3] = {cuuint64_t(K / 2), cuuint64_t(rows), cuuint64_t(batch)};
+  const cuuint64_t strides[2] = {cuuint64_t(K / 2), cuuint64_t(stride)};
+  const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Split a tile's K over a cluster while that gives idle multiprocessors work
+// (two blocks fit a multiprocessor for narrow plain tiles).
+void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
+              int* clusters) {
+  const int64_t slots = int64_t(num_sms) * (nt <= 32 && !gate_up ? 2 : 1);
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
+  *split = s;
+  *clusters = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / s)));
+}
+
+static int mx_tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// y[M, N] = x w^T.  x: the packed tokens, or (xq) M <= 16 rows of values.
+cudaError_t launch_mx_product(const void* x, int x_dtype, bool xq, int64_t M, const void* packed,
+                              int fmt, int64_t N, int64_t K, void* y, int y_dtype,
+                              int32_t* dev_status, int num_sms, cudaStream_t stream) {
+  const int nt = mx_tile_tokens(M);
+  CUtensorMap t[3];
+  std::memset(t, 0, sizeof(t));
+  const uint8_t* w = static_cast<const uint8_t*>(packed);
+  const uint8_t* xp = static_cast<const uint8_t*>(x);
+  cudaError_t err = make_mx_map(&t[0], w, N, K, 1, mx_bytes(N, K, fmt), 128);
+  if (err != cudaSuccess) return err;
+  t[1] = t[0];
+  if (xq) t[2] = t[0];
+  else if ((err = make_mx_map(&t[2], xp, M, K, 1, mx_bytes(M, K, fmt), nt)) != cudaSuccess)
+    return err;
+  MxGemmArgs a = {};
+  a.a_scales[0] = a.a_scales[1] = w + mx_scale_off(N, K);
+  a.a_rows[0] = a.a_rows[1] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));
+  a.a_stride = 0;
+  if (xq) {
+    a.x = x;
+    a.x_dtype = x_dtype;
+  } else {
+    a.b_scales = xp + mx_scale_off(M, K);
+    a.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
+  }
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.dev_status = dev_status;
+  a.N = N;
+  a.M = M;
+  a.K = K;
+  a.chunks = int(mx_ceil(K, kMxChunk));
+  a.mtiles = int(mx_ceil(N, 128));
+  const int64_t tiles = a.mtiles * mx_ceil(M, nt);
+  int split, clusters;
+  mx_split(tiles, a.chunks, nt, false, num_sms, &split, &clusters);
+  return launch_mx_gemm(t, a, fmt, kMxPlain, nt, split, clusters, xq, stream);
+}
+
+}  // namespace lutq

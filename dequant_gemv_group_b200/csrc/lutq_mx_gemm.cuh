@@ -1,0 +1,50 @@
+// The product of two microscaled 4-bit matrices: what its launchers share.
+#pragma once
+
+#include <cuda.h>
+
+#include "lutq_mx.cuh"
+
+namespace lutq {
+
+// What a launch computes.  Rows of the weight matrix (A) are tensor-memory
+// lanes, tokens (B) are columns.
+enum MxMode {
+  kMxPlain = 0,   // y[m, n] = sum_k x[m, k] w[n, k]
+  kMxGateUp = 1,  // per expert: h = silu(x gate^T) * (x up^T), rounded to bf16
+  kMxDown = 2,    // per expert: out = h down^T, fp32
+};
+
+struct MxGemmArgs {
+  const uint8_t* a_scales[2];  // scale chunks of the weight matrices (of expert 0)
+  const float* a_rows[2];      // nvfp4: their row scales
+  int64_t a_stride;            // bytes from one expert's matrix to the next
+  const uint8_t* b_scales;     // tokens: scale chunks and row scales
+  const float* b_rows;
+  const void* x;               // tokens quantized in the kernel: the values
+  int x_dtype;
+  void* y;
+  int y_dtype;
+  int32_t* dev_status;
+  int64_t N, M, K;
+  int chunks;                  // ceil(K / 256)
+  int mtiles;                  // ceil(N / 128)
+  int stages;
+  // experts: how many rows each has and where they begin (multiples of 128)
+  const int32_t* counts;
+  const int32_t* bases;
+  int experts;
+};
+
+cudaError_t launch_mx_gemm(const CUtensorMap* tmaps, const MxGemmArgs& a, int fmt, int mode,
+                           int nt, int split, int clusters, bool xq, cudaStream_t stream);
+
+// Tensor map of `batch` matrices of packed codes, `stride` bytes apart.
+cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K,
+                        int64_t batch, int64_t stride, int box_rows);
+
+// Blocks of a launch: how many share a tile by K, and how many tiles run at once.
+void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
+              int* clusters);
+
+}  // namespace lutq

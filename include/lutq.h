@@ -574,6 +574,143 @@ lutq_status lutq_gemm_typed(const void* x_bf16, int64_t M, const void* packed,
                             float* y, void* workspace, int64_t workspace_bytes,
                             int32_t* dev_status, void* stream);
 
+/*
+ * Microscaled 4-bit floating point.
+ *
+ * No counterpart on the pages: the format of the OCP Microscaling
+ * specification and its variant with finer blocks, which the tensor cores of
+ * the B200 multiply as they are.  An element is E2M1 (levels 0, .5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives; code = sign << 3 | index).  A block of
+ * consecutive elements along K shares a scale byte:
+ *   LUTQ_MXFP4  blocks of 32, E8M0: s = 2^(byte - 127), 0xFF = NaN;
+ *   LUTQ_NVFP4  blocks of 16, E4M3, and one fp32 scale g per row.
+ * The value of an element is level * s (* g).
+ *
+ * Quantization of a block with largest magnitude m:
+ *   LUTQ_MXFP4  s = 2^(floor(log2 m) - 2), at least 2^-127;
+ *   LUTQ_NVFP4  g = 2^(floor(log2 r) - 10) for the row's largest finite
+ *               magnitude r (at least 2^-126; 1 for a row of zeros),
+ *               s = m / 6 / g rounded to E4M3 (nearest even);
+ *   the element is the level nearest to x / (s g), ties to the even code,
+ *   magnitudes above 6 to 6; x keeps its sign; a block whose s is 0 is zero.
+ * A block with a NaN or an infinity has the scale NaN and codes 0: all its
+ * values, and every output it enters, are NaN, and dev_status receives
+ * LUTQ_ERR_NONFINITE.  For bf16 and fp16 inputs every decision equals that of
+ * exact arithmetic.
+ *
+ * Packed layout of an N x K matrix (K % 32 == 0, any N >= 1):
+ *   codes  N K / 2 bytes row-major, element 2i in the low nibble, padded with
+ *          unspecified bytes to a multiple of 128;
+ *   scales chunks [ceil(N / 128)][ceil(K / 256)] of 1024 (LUTQ_MXFP4) or 2048
+ *          bytes; a chunk is blocks of 512 bytes, each the next four scales
+ *          along K of 128 rows, row r's j-th at byte
+ *          16 (r % 32) + 4 ((r % 128) / 32) + j; positions outside the matrix
+ *          are 0;
+ *   rows   LUTQ_NVFP4 only: fp32 g [N], padded to a multiple of 128 bytes.
+ * Several matrices of the same shape are one packed buffer after another.
+ */
+typedef enum { LUTQ_MXFP4 = 0, LUTQ_NVFP4 = 1 } lutq_mx_format;
+typedef enum { LUTQ_BF16 = 0, LUTQ_FP16 = 1, LUTQ_FP32 = 2 } lutq_dtype;
+
+/* Bytes of a packed N x K matrix; -1 for an invalid shape or format. */
+int64_t lutq_mx_packed_bytes(int64_t N, int64_t K, int format);
+
+/*
+ * lutq_mx_quantize - W [batch, N, K] of `dtype` into `batch` packed matrices.
+ * lutq_mx_dequantize - the values of packed matrices as `dtype`
+ *   [batch, N, K], rounded once (exact in bf16 and fp32 but for results below
+ *   their range).
+ * lutq_mx_pack - codes uint8 [batch, N, K/2] (two a byte, element 2i low) and
+ *   scale bytes uint8 [batch, N, K/32 or K/16] (and row_scales fp32
+ *   [batch, N] for LUTQ_NVFP4, or NULL for 1) into packed matrices.
+ * All pointers are device memory, 16-byte aligned; asynchronous on `stream`.
+ * batch = 0 or N = 0 does nothing.  LUTQ_ERR_SHAPE: K % 32 != 0, K < 32, or a
+ * size out of range (batch above 65535).
+ */
+lutq_status lutq_mx_quantize(const void* W, int dtype, int64_t batch, int64_t N, int64_t K,
+                             int format, void* packed, int32_t* dev_status, void* stream);
+lutq_status lutq_mx_dequantize(const void* packed, int64_t batch, int64_t N, int64_t K, int format,
+                               void* out, int dtype, void* stream);
+lutq_status lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
+                         int64_t batch, int64_t N, int64_t K, int format, void* packed,
+                         void* stream);
+
+/*
+ * lutq_mx_gemm - y[m, n] = sum_k x[m, k] w[n, k] of two packed matrices of the
+ * same format, x [M, K] and w [N, K]: products on the tensor cores, sums in
+ * fp32, y [M, N] row-major of `y_dtype`, rounded once.  Any M >= 0.
+ *
+ * lutq_mx_gemv - the same for M = 0..16 rows of values x [M, K] of `x_dtype`,
+ * quantized inside the kernel exactly as lutq_mx_quantize does: one launch
+ * for single tokens and small batches.  LUTQ_ERR_SHAPE if M > 16.
+ *
+ * Neither needs a workspace; results do not depend on timing, and a row of y
+ * not on the other rows of x given the number of rows.  dev_status receives
+ * LUTQ_ERR_TIMEOUT if a wait inside the kernel exceeds its bound, and (gemv)
+ * LUTQ_ERR_NONFINITE for a NaN or infinite x.  Pointers 16-byte aligned.
+ */
+lutq_status lutq_mx_gemm(const void* x_packed, int64_t M, const void* packed, int64_t N, int64_t K,
+                         int format, void* y, int y_dtype, int32_t* dev_status, void* stream);
+lutq_status lutq_mx_gemv(const void* x, int x_dtype, int64_t M, const void* packed, int64_t N,
+                         int64_t K, int format, void* y, int y_dtype, int32_t* dev_status,
+                         void* stream);
+
+/*
+ * lutq_route - routing of T tokens to E experts.  For each token, in fp64:
+ *   p_e = exp(z_e) / sum exp(z)  (LUTQ_SCORE_SOFTMAX) or 1 / (1 + exp(-z_e))
+ *   (LUTQ_SCORE_SIGMOID) of its logits z; c_e = p_e + bias_e (bias may be
+ *   NULL) decides the selection, p the weights.
+ *   groups > 1: the experts form `groups` runs of E / groups; a group's score
+ *   is the sum of its group_best (1 or 2) largest c; only experts of the
+ *   top_groups best groups remain.
+ *   ids: the top_k largest c in descending order; weights p of those, divided
+ *   by their sum if `renormalize`, times `scale`, rounded once to fp32.
+ * Ties go to the lowest expert (group).  An expert whose logit is -infinity is
+ * not available: it does not count in a group's score, comes after all
+ * others, lowest first, and its weight is 0 (so a row of -infinity gives
+ * experts 0..top_k-1 with weights 0).  A NaN logit counts as -infinity, +infinity as the
+ * limit; both report LUTQ_ERR_NONFINITE.
+ *
+ * logits  device [T, E] of `dtype`; bias device fp32 [E] or NULL.
+ * ids     device int32 [T, top_k]; weights device fp32 [T, top_k], written.
+ * T = 0 does nothing.  Returns LUTQ_ERR_SHAPE unless 1 <= E <= 1024,
+ * E % groups == 0, groups <= 32, 1 <= top_groups <= groups, group_best 1 or 2,
+ * 1 <= top_k <= min(32, top_groups * E / groups).  Pointers 4-byte aligned (a
+ * logits pointer: its element).
+ */
+typedef enum { LUTQ_SCORE_SOFTMAX = 0, LUTQ_SCORE_SIGMOID = 1 } lutq_score;
+lutq_status lutq_route(const void* logits, int dtype, int64_t T, int E, const float* bias,
+                       int score, int groups, int top_groups, int group_best, int top_k,
+                       int renormalize, float scale, int32_t* ids, float* weights,
+                       int32_t* dev_status, void* stream);
+
+/*
+ * lutq_mx_experts - the feed-forward layer of a mixture of experts:
+ *   y[t] = sum_j weights[t, j] * W_down_e h_e,  e = ids[t, j],
+ *   h_e = bf16(silu(W_gate_e q(x[t])) * (W_up_e q(x[t]))) quantized again,
+ * q the quantization above; silu(v) = v / (1 + exp(-v)); the sum over j in
+ * fp32 in the order of j, y rounded once.
+ *
+ * x       device [T, D] of `dtype`; y device [T, D] of the same type.
+ * ids     device int32 [T, top_k]; an id outside 0..E-1 contributes nothing
+ *         (a token without any valid id gets zeros); an id may repeat.
+ * weights device fp32 [T, top_k].
+ * gate, up  device, E packed matrices [F, D]; down: E packed matrices [D, F].
+ * workspace device, lutq_mx_experts_workspace_bytes(...) bytes, any contents;
+ *         calls that may run at the same time must not share one.
+ * T = 0 does nothing.  LUTQ_ERR_SHAPE unless D % 32 == 0, F % 32 == 0,
+ * 1 <= E <= 1024, 1 <= top_k <= 64 and T * top_k <= 2^24; ids and weights
+ * 4-byte aligned; other errors and dev_status as lutq_mx_gemv
+ * (LUTQ_ERR_NONFINITE also for hidden values beyond bf16).
+ */
+int64_t lutq_mx_experts_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F,
+                                        int format);
+lutq_status lutq_mx_experts(const void* x, int dtype, int64_t T, const int32_t* ids,
+                            const float* weights, int top_k, int E, const void* gate,
+                            const void* up, const void* down, int64_t D, int64_t F, int format,
+                            void* y, void* workspace, int64_t workspace_bytes,
+                            int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

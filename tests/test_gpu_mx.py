@@ -1,0 +1,308 @@
+"""Microscaled 4-bit floating point on the GPU against the oracle: packed
+bytes bit for bit, products within a bound derived here.
+
+Product bound.  Every product of two elements and their scales is exact in
+fp32 (4-bit significands).  The tensor core adds 64 products to the
+accumulator at a time; taking each of those 65 additions to lose at most one
+unit of 2^-23 of the sum of magnitudes A = sum |x w| (truncation of an aligned
+24-bit sum), K / 64 steps lose at most K * 65 / 64 * 2^-23 * A.  nvfp4's row
+scales are two fp32 multiplications (powers of two unless packed by the
+caller): 2^-23 |y|.  A split over at most 8 blocks adds 8 * 2^-24 * A.  The
+output's rounding is half a step of its type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from oracle import mx_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ["mxfp4", "nvfp4"]
+
+
+@pytest.fixture(scope="module")
+def lq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import dequant_gemv_group_b200 as m
+    return m
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _x(m, k, seed, std=1.0):
+    x = workloads.normal_weights(m, k, std, seed=seed, outlier_frac=1e-2)
+    if m > 2:
+        x[2] = 0.0                       # a row of zeros
+    if m > 4:
+        x[4, :32] = 0.0                  # a block of zeros
+        x[4, 1] = -0.0
+    if m > 5:
+        x[5] *= 2.0 ** -100              # far exponents
+    if m > 6:
+        x[6] *= 2.0 ** 100
+    if m > 7:
+        x[7, 0] = 2.0 ** -126            # beside ordinary values: underflows to 0
+    return x
+
+
+def _same_packed(got, codes, scales, rows, fmt):
+    want, known = O.pack(codes, scales, rows, fmt)
+    got = got.cpu().numpy()
+    assert got.shape == want.shape
+    np.testing.assert_array_equal(got[known], want[known])
+
+
+def _bound(y, mag, k, dtype):
+    eps = torch.finfo(dtype).eps / 2
+    return (k * 65 / 64 * 2.0 ** -23 + 2.0 ** -21) * mag + (2.0 ** -23 + eps * 1.01) * np.abs(y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k", [(1, 32), (9, 96), (128, 256), (130, 288), (33, 4096)])
+def test_quantize_bit_exact(lq, fmt, n, k):
+    x = _x(n, k, seed=n + k)
+    st = lq.new_status()
+    got = lq.lutq_mx_quantize(x.cuda(), fmt, status=st)
+    codes, scales, rows = O.quantize(_f64(x), fmt)
+    _same_packed(got, codes, scales, rows, fmt)
+    assert int(st.item()) == 0
+    vals = O.values(codes, scales, rows, fmt)
+    back = lq.lutq_mx_dequantize(got, n, k, fmt, dtype=torch.float32)
+    # below 2^-126 the fp32 values stay exact (subnormals); the levels have 6 bits at most
+    np.testing.assert_array_equal(_f64(back), vals)
+    small = np.abs(vals) < 2.0 ** 15
+    half = lq.lutq_mx_dequantize(got, n, k, fmt, dtype=torch.float16)
+    np.testing.assert_array_equal(half.cpu().numpy()[small], vals[small].astype(np.float16))
+    bf = lq.lutq_mx_dequantize(got, n, k, fmt)
+    normal = (np.abs(vals) >= 2.0 ** -126) | (vals == 0)
+    np.testing.assert_array_equal(_f64(bf)[normal], vals[normal])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_quantize_types(lq, fmt, dtype):
+    x = (torch.randn(40, 320, generator=torch.Generator().manual_seed(1)) * 3)
+    x = x.to(torch.bfloat16 if dtype == torch.float32 else dtype).to(dtype)
+    got = lq.lutq_mx_quantize(x.cuda(), fmt)
+    _same_packed(got, *O.quantize(_f64(x), fmt), fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_every_bf16(lq, fmt):
+    """All finite bf16 values, alone in their blocks and beside 1.0."""
+    bits = torch.arange(0, 65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(torch.bfloat16)
+    v = v[torch.isfinite(v)]
+    x = torch.zeros(v.numel(), 64, dtype=torch.bfloat16)
+    x[:, 0] = v
+    x[:, 32] = v
+    x[:, 33] = 1.0
+    got = lq.lutq_mx_quantize(x.cuda(), fmt)
+    _same_packed(got, *O.quantize(_f64(x), fmt), fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_batched_and_packed(lq, fmt):
+    """Several matrices at once, and the same bytes from codes and scales."""
+    b, n, k = 3, 37, 224
+    x = torch.stack([_x(n, k, seed=i) for i in range(b)])
+    got = lq.lutq_mx_quantize(x.cuda(), fmt)
+    assert got.shape == (b, lq.lutq_mx_packed_bytes(n, k, fmt))
+    parts = [O.quantize(_f64(x[i]), fmt) for i in range(b)]
+    for i in range(b):
+        _same_packed(got[i], *parts[i], fmt)
+    codes = np.stack([p[0] for p in parts])
+    scales = torch.from_numpy(np.stack([p[1] for p in parts])).cuda()
+    rows = torch.from_numpy(np.stack([p[2] for p in parts])).cuda()
+    pair = torch.from_numpy(codes[..., 0::2] | (codes[..., 1::2] << 4)).cuda()
+    again = lq.lutq_mx_pack(pair, scales, fmt, rows if fmt == "nvfp4" else None)
+    for i in range(b):
+        _same_packed(again[i], *parts[i], fmt)
+    deq = lq.lutq_mx_dequantize(got, n, k, fmt, dtype=torch.float32)
+    assert deq.shape == (b, n, k)
+    for i in range(b):
+        np.testing.assert_array_equal(_f64(deq[i]), O.values(*parts[i], fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nonfinite_reported(lq, fmt, bad):
+    x = _x(20, 512, seed=5)
+    x[11, 300] = bad
+    st = lq.new_status()
+    got = lq.lutq_mx_quantize(x.cuda(), fmt, status=st)
+    _same_packed(got, *O.quantize(_f64(x), fmt), fmt)
+    assert int(st.item()) == 5
+    # every output of that row is NaN, the others are not
+    w = lq.lutq_mx_quantize(workloads.normal_weights(64, 512, 0.02, seed=1).cuda(), fmt)
+    y = lq.lutq_mx_gemm(got, 20, w, 64, 512, fmt)
+    assert torch.isnan(y[11]).all() and torch.isfinite(y[:11]).all() and torch.isfinite(y[12:]).all()
+    st = lq.new_status()
+    y = lq.lutq_mx_gemv(x[8:16].contiguous().cuda(), w, 64, 512, fmt, status=st)
+    assert int(st.item()) == 5
+    assert torch.isnan(y[3]).all() and torch.isfinite(y[:3]).all() and torch.isfinite(y[4:]).all()
+
+
+def _case(lq, m, n, k, fmt, seed=0):
+    x = _x(m, k, seed=seed + m)
+    if m > 5:
+        x[5] *= 2.0 ** 100               # back in range of the products
+    if m > 6:
+        x[6] *= 2.0 ** -100
+    w = workloads.normal_weights(n, k, 0.02, seed=seed + n, outlier_frac=1e-3)
+    wp = lq.lutq_mx_quantize(w.cuda(), fmt)
+    xv = O.values(*O.quantize(_f64(x), fmt), fmt)
+    wv = O.values(*O.quantize(_f64(w), fmt), fmt)
+    return x, wp, *O.product(xv, wv)
+
+
+SHAPES = [(1, 1, 32), (1, 128, 256), (2, 7, 96), (3, 256, 512), (8, 1000, 2048), (15, 130, 4128),
+          (16, 64, 14336), (17, 33, 288), (31, 513, 1024), (33, 128, 4096), (64, 640, 800),
+          (65, 96, 2080), (127, 257, 544), (128, 384, 4096), (129, 1024, 256), (200, 200, 3232),
+          (300, 2049, 96), (513, 300, 1056)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_products(lq, fmt, m, n, k):
+    x, wp, ref, mag = _case(lq, m, n, k, fmt)
+    st = lq.new_status()
+    xp = lq.lutq_mx_quantize(x.cuda(), fmt)
+    y = lq.lutq_mx_gemm(xp, m, wp, n, k, fmt, status=st)
+    assert int(st.item()) == 0
+    err = np.abs(_f64(y) - ref)
+    assert (err <= _bound(ref, mag, k, torch.float32)).all(), (err / np.maximum(mag, 1e-300)).max()
+    yb = lq.lutq_mx_gemm(xp, m, wp, n, k, fmt, dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16))
+    yh = lq.lutq_mx_gemm(xp, m, wp, n, k, fmt, dtype=torch.float16)
+    assert torch.equal(yh, y.to(torch.float16))
+    if m <= 16:
+        z = lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt, status=st)
+        assert torch.equal(z, y)
+        assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_gemv_types(lq, fmt, dtype):
+    m, n, k = 5, 200, 1120
+    x = torch.randn(m, k, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(dtype)
+    w = lq.lutq_mx_quantize(workloads.normal_weights(n, k, 0.02, seed=3).cuda(), fmt)
+    y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x.cuda(), fmt), m, w, n, k, fmt)
+    assert torch.equal(lq.lutq_mx_gemv(x.cuda(), w, n, k, fmt), y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 16, 40, 150, 700])
+def test_exact_sums(lq, fmt, m):
+    """Small integers in scales of 1: every partial sum is exact, so y is too, in every tile."""
+    n, k = 391, 1312
+    g = torch.Generator().manual_seed(m)
+    lv = torch.tensor([0.0, 1.0, 2.0, 3.0, 4.0, 6.0])
+    pick = lambda *s: lv[torch.randint(0, 6, s, generator=g)] * (  # noqa: E731
+        torch.randint(0, 2, s, generator=g) * 2 - 1)
+    x, w = pick(m, k), pick(n, k)
+    x[:, 0::32], w[:, 0::32] = 6.0, 6.0
+    x[:, 16::32], w[:, 16::32] = 6.0, 6.0
+    y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x.bfloat16().cuda(), fmt), m,
+                        lq.lutq_mx_quantize(w.bfloat16().cuda(), fmt), n, k, fmt)
+    if fmt == "nvfp4":  # s = 6 / 6 / g = 256 = 1 / g
+        assert float(O.quantize(_f64(x), fmt)[2].max()) == 2.0 ** -8
+    assert torch.equal(y.cpu(), (x.double() @ w.double().t()).float())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_hot(lq, fmt):
+    """A token that is 1 at one position reads a column of the weights, scales and all."""
+    n, k = 160, 1056
+    w = workloads.normal_weights(n, k, 0.02, seed=8, outlier_frac=1e-2)
+    wp = lq.lutq_mx_quantize(w.cuda(), fmt)
+    wv = O.values(*O.quantize(_f64(w), fmt), fmt)
+    pos = list(range(0, k, 5)) + [k - 1]
+    x = torch.zeros(len(pos), k)
+    x[torch.arange(len(pos)), pos] = 1.0
+    y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x.bfloat16().cuda(), fmt), len(pos), wp, n, k, fmt)
+    # nvfp4: 1 = 6 * (170.67 -> 176) / 1024 * ... is not a level: the oracle's value of x scales it
+    xv = O.values(*O.quantize(_f64(x), fmt), fmt)
+    np.testing.assert_allclose(_f64(y), xv @ wv.T, rtol=2.0 ** -22, atol=0)
+
+
+def test_nvfp4_row_scales_from_a_checkpoint(lq):
+    """Row scales that are no powers of two, negative scale-free, and a NULL one."""
+    n, k, m = 70, 256, 20
+    g = torch.Generator().manual_seed(9)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g).to(torch.uint8)
+    scales = torch.randint(0, 0x60, (n, k // 16), generator=g).to(torch.uint8)
+    rows = torch.rand(n, generator=g) + 0.1
+    x = _x(m, k, seed=1)
+    x[5], x[6] = x[0], x[1]
+    xp = lq.lutq_mx_quantize(x.cuda(), "nvfp4")
+    xv = O.values(*O.quantize(_f64(x), "nvfp4"), "nvfp4")
+    c = codes.numpy()
+    c = np.stack([c & 15, c >> 4], -1).reshape(n, k)
+    for r in (rows, None):
+        wp = lq.lutq_mx_pack(codes.cuda(), scales.cuda(), "nvfp4", None if r is None else r.cuda())
+        wv = O.values(c, scales.numpy(), np.ones(n) if r is None else r.numpy(), "nvfp4")
+        ref, mag = O.product(xv, wv)
+        y = lq.lutq_mx_gemm(xp, m, wp, n, k, "nvfp4")
+        assert (np.abs(_f64(y) - ref) <= _bound(ref, mag, k, torch.float32)).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_deterministic_and_in_bounds(lq, fmt):
+    """Twice the same bits; nothing behind y is written; garbage in the codes' padding and in the
+    rows behind the last one does not matter."""
+    for m, n, k in [(1, 1000, 4096), (16, 333, 2048), (50, 130, 1024), (140, 257, 512)]:
+        x, wp, _, _ = _case(lq, m, n, k, fmt, seed=4)
+        xp = lq.lutq_mx_quantize(x.cuda(), fmt)
+        buf = torch.full((m * n + 512,), 7.0, device="cuda")
+        y = buf[:m * n].view(m, n)
+        lq.lutq_mx_gemm(xp, m, wp, n, k, fmt, y=y)
+        assert (buf[m * n:] == 7.0).all()
+        for _ in range(3):
+            assert torch.equal(lq.lutq_mx_gemm(xp, m, wp, n, k, fmt), y)
+            if m <= 16:
+                assert torch.equal(lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt), y)
+
+
+def test_empty(lq):
+    w = lq.lutq_mx_quantize(torch.ones(8, 64, dtype=torch.bfloat16, device="cuda"), "mxfp4")
+    none = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    assert lq.lutq_mx_gemv(none, w, 8, 64, "mxfp4").shape == (0, 8)
+    xp = lq.lutq_mx_quantize(none, "mxfp4")
+    assert xp.numel() == 0
+    assert lq.lutq_mx_gemm(xp, 0, w, 8, 64, "mxfp4").shape == (0, 8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_streams_and_graphs(lq, fmt):
+    """Two streams at once, and a captured chain replayed on new inputs."""
+    m, n, k = 12, 1024, 4096
+    x, wp, _, _ = _case(lq, m, n, k, fmt, seed=6)
+    x = x.cuda()
+    want = lq.lutq_mx_gemv(x, wp, n, k, fmt)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s in (s1, s2):
+            with torch.cuda.stream(s):
+                got.append(lq.lutq_mx_gemv(x, wp, n, k, fmt))
+                got.append(lq.lutq_mx_gemm(lq.lutq_mx_quantize(x, fmt), m, wp, n, k, fmt))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    xin = torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = lq.lutq_mx_gemv(xin, wp, n, k, fmt)
+        b = lq.lutq_mx_gemm(lq.lutq_mx_quantize(xin, fmt), m, wp, n, k, fmt)
+    for scale in (1.0, -2.0):
+        xin.copy_(x * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want * scale) and torch.equal(b, want * scale)
