@@ -613,8 +613,10 @@ cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64
 void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
               int* clusters) {
   const int64_t slots = int64_t(num_sms) * (nt <= 32 && !gate_up ? 2 : 1);
+  // (the partial sums of a wide gate-and-up tile leave no room for stages)
+  const int most = gate_up && nt > 32 ? 1 : 8;
   int s = 1;
-  while (s < 8 && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
+  while (s < most && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
   *split = s;
   *clusters = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / s)));
 }
