@@ -167,24 +167,20 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                      ints(s.slot),   ints(s.source), ints(s.self)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
-  // tokens per tile: an expert has at most T rows, T top_k / E on average
-  const int64_t mean = mx_ceil(pairs, E);
-  const int nt = T <= 16 ? 16 : mean <= 32 ? 32 : 128;
-  CUtensorMap up_maps[3], down_maps[3];
-  std::memset(up_maps, 0, sizeof(up_maps));
-  std::memset(down_maps, 0, sizeof(down_maps));
+  // an expert has at most T rows, T top_k / E on average
+  const int nt = mx_tile_tokens(T);
+  const bool wide = mx_ceil(pairs, E) > 32 && T > 64;
   const int64_t w1 = mx_bytes(F, D, fmt), w2 = mx_bytes(D, F, fmt);
+  const int64_t used = std::min<int64_t>(E, pairs);  // experts in use at most
+  CUtensorMap maps[4];
+  std::memset(maps, 0, sizeof(maps));
   cudaError_t err;
-  if ((err = make_mx_map(&up_maps[0], gate, F, D, E, w1, 128)) != cudaSuccess) return err;
-  if ((err = make_mx_map(&up_maps[1], up, F, D, E, w1, 128)) != cudaSuccess) return err;
-  if ((err = make_mx_map(&up_maps[2], ws + s.xq, cap, D, 1, mx_bytes(cap, D, fmt), nt)) !=
-      cudaSuccess)
-    return err;
-  if ((err = make_mx_map(&down_maps[0], down, D, F, E, w2, 128)) != cudaSuccess) return err;
-  down_maps[1] = down_maps[0];
-  if ((err = make_mx_map(&down_maps[2], ws + s.hq, cap, F, 1, mx_bytes(cap, F, fmt), nt)) !=
-      cudaSuccess)
-    return err;
+  auto token_maps = [&](const void* rows, int64_t width) {
+    const cudaError_t e = make_mx_map(&maps[2], rows, cap, width, 1, mx_bytes(cap, width, fmt), nt);
+    return e != cudaSuccess
+               ? e
+               : make_mx_map(&maps[3], rows, cap, width, 1, mx_bytes(cap, width, fmt), 16);
+  };
 
   if ((err = launch_pdl(moe_plan_kernel, dim3(unsigned(E)), dim3(kPlanThreads), size_t(E) * 4,
                         stream, ids, pairs, top_k, E, p)) != cudaSuccess)
@@ -199,8 +195,6 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.bases = p.bases;
   a.experts = E;
   a.M = cap;
-  // tiles at most: an expert in use has one row tile of tokens at least
-  const int64_t token_tiles = std::min<int64_t>(E, pairs) + pairs / nt;
   auto bytes = [](const void* q, int64_t off) { return static_cast<const uint8_t*>(q) + off; };
   a.a_scales[0] = bytes(gate, mx_scale_off(F, D));
   a.a_scales[1] = bytes(up, mx_scale_off(F, D));
@@ -215,10 +209,17 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.chunks = int(mx_ceil(D, kMxChunk));
   a.mtiles = int(mx_ceil(F, 128));
   int split, clusters;
-  mx_split(token_tiles * a.mtiles, a.chunks, nt, true, num_sms, &split, &clusters);
-  if ((err = launch_mx_gemm(up_maps, a, fmt, kMxGateUp, nt, split, clusters, false, stream)) !=
-      cudaSuccess)
-    return err;
+  if (wide) {
+    err = launch_mx_pair(a, gate, up, w1, ws + s.xq, cap, fmt, kMxGateUp,
+                         (used + pairs / 128) * mx_ceil(F, 256), num_sms, stream);
+  } else {
+    if ((err = make_mx_map(&maps[0], gate, F, D, E, w1, 128)) != cudaSuccess) return err;
+    if ((err = make_mx_map(&maps[1], up, F, D, E, w1, 128)) != cudaSuccess) return err;
+    if ((err = token_maps(ws + s.xq, D)) != cudaSuccess) return err;
+    mx_split((used + pairs / nt) * a.mtiles, a.chunks, nt, true, num_sms, &split, &clusters);
+    err = launch_mx_gemm(maps, a, fmt, kMxGateUp, nt, split, clusters, false, stream);
+  }
+  if (err != cudaSuccess) return err;
   if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, cap, F, fmt, p.self, p.total, ws + s.hq,
                                 dev_status, num_sms, stream)) != cudaSuccess)
     return err;
@@ -233,10 +234,17 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.K = F;
   a.chunks = int(mx_ceil(F, kMxChunk));
   a.mtiles = int(mx_ceil(D, 128));
-  mx_split(token_tiles * a.mtiles, a.chunks, nt, false, num_sms, &split, &clusters);
-  if ((err = launch_mx_gemm(down_maps, a, fmt, kMxDown, nt, split, clusters, false, stream)) !=
-      cudaSuccess)
-    return err;
+  if (wide) {
+    err = launch_mx_pair(a, down, nullptr, w2, ws + s.hq, cap, fmt, kMxDown,
+                         (used + pairs / 256) * mx_ceil(D, 256), num_sms, stream);
+  } else {
+    if ((err = make_mx_map(&maps[0], down, D, F, E, w2, 128)) != cudaSuccess) return err;
+    maps[1] = maps[0];
+    if ((err = token_maps(ws + s.hq, F)) != cudaSuccess) return err;
+    mx_split((used + pairs / nt) * a.mtiles, a.chunks, nt, false, num_sms, &split, &clusters);
+    err = launch_mx_gemm(maps, a, fmt, kMxDown, nt, split, clusters, false, stream);
+  }
+  if (err != cudaSuccess) return err;
   auto combine = [&](auto kernel) {
     return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 1024))), dim3(256), 0, stream,
                       reinterpret_cast<const float*>(ws + s.out), p.slot, weights, top_k, D, y);

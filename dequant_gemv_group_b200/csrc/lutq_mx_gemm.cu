@@ -60,6 +60,11 @@ struct MxShared {
   float row_scale[16];       // tokens quantized here: their row scales
 };
 
+// A tile begins at a multiple of 128 tokens, the height of a scale block
+// (narrower tiles only where one holds all tokens), so that its scales begin
+// at the first column of a block: the MMA faults on others ("misaligned
+// address" with scales one column on).
+//
 // Walks the tiles t = first, first + step, ... of a launch: plain products go
 // over the row tiles first, experts' over each expert's tiles in turn.
 template <int MODE>
@@ -122,7 +127,8 @@ template <int FMT, int NT, int MODE, bool XQ>
 __global__ void __launch_bounds__(XQ ? 320 : 192)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a2,
-                   const __grid_constant__ CUtensorMap tmap_b, const MxGemmArgs a, int split) {
+                   const __grid_constant__ CUtensorMap tmap_b,
+                   const __grid_constant__ CUtensorMap tmap_b16, const MxGemmArgs a, int split) {
   using Cfg = MxCfg<FMT, NT, MODE>;
   constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS;
   extern __shared__ uint8_t smem_raw[];
@@ -187,13 +193,14 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
       bool ok = true;
       for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
         const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+        const int width = (valid + 15) / 16 * 16;  // columns: in boxes of 16 tokens
         const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
         const uint8_t* bs = a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
         for (int c = c0; c < c1; ++c) {
           if (!(ok = mbar_wait(empty(s), ph, abort, kMxWaitNs))) break;
           const uint32_t st = sbase + s * Cfg::STAGE;
           const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
-          mbar_expect_tx(full(s), ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : Cfg::B_BYTES + CH));
+          mbar_expect_tx(full(s), ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : width * 128 + CH));
           tma_3d_g2s(st, &tmap_a, c * 128, mt * 128, expert, full(s));
           bulk_g2s(sf, a.a_scales[0] + a_off + int64_t(c) * CH, CH, full(s));
           if (ND == 2) {
@@ -201,7 +208,13 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
             bulk_g2s(sf + CH, a.a_scales[1] + a_off + int64_t(c) * CH, CH, full(s));
           }
           if (!XQ) {
-            tma_3d_g2s(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0, 0, full(s));
+            if (width == NT) {
+              tma_3d_g2s(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0, 0, full(s));
+            } else {
+              for (int i = 0; i < width; i += 16)
+                tma_3d_g2s(st + ND * Cfg::A_BYTES + i * 128, &tmap_b16, c * 128, row0 + i, 0,
+                           full(s));
+            }
             bulk_g2s(sf + ND * CH, bs + int64_t(c) * CH, CH, full(s));
           }
           ++issued;
@@ -240,9 +253,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
           break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(b * ND * NT);
-        // tokens below the first row of a 128-row scale tile: their columns
-        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-        const uint32_t sb_shift = XQ ? 0u : uint32_t(row0 % kMxRowTile) / 32u;
+        const int width = XQ ? NT : (valid + 15) / 16 * 16;
         for (int c = c0; c < c1; ++c, ++it) {
           if (!(ok = mbar_wait(full(s), ph, abort, kMxWaitNs))) break;
           tc_fence_after();
@@ -256,9 +267,9 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
           for (int j = 0; j < 4; ++j) {
             // mxfp4: a block holds the scales of two MMAs, nvfp4: of one
             const int blk = E8 ? j >> 1 : j, id = E8 ? (j & 1) * 2 : 0;
-            const uint32_t idesc = idesc_e2m1(128, NT, E8, id);
+            const uint32_t idesc = idesc_e2m1(128, width, E8, id);
             const uint64_t bd = smem_desc_k_sw128(st + ND * Cfg::A_BYTES + 32 * j);
-            const uint32_t sb = sf_tmem + 4 * (ND * BLOCKS + blk) + sb_shift;
+            const uint32_t sb = sf_tmem + 4 * (ND * BLOCKS + blk);
 #pragma unroll
             for (int w = 0; w < ND; ++w)
               mma_e2m1_ss<!E8>(d + w * NT, smem_desc_k_sw128(st + w * Cfg::A_BYTES + 32 * j), bd,
@@ -548,7 +559,7 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int
   attr[1].val.clusterDim = {unsigned(split), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, t[0], t[1], t[2], a, split);
+  return cudaLaunchKernelEx(&cfg, kernel, t[0], t[1], t[2], t[3], a, split);
 }
 
 template <int FMT>
@@ -564,9 +575,11 @@ static cudaError_t launch_fmt(const CUtensorMap* t, const MxGemmArgs& a, int mod
   LUTQ_MX_CASE(128, kMxPlain, false)
   LUTQ_MX_CASE(16, kMxGateUp, false)
   LUTQ_MX_CASE(32, kMxGateUp, false)
+  LUTQ_MX_CASE(64, kMxGateUp, false)
   LUTQ_MX_CASE(128, kMxGateUp, false)
   LUTQ_MX_CASE(16, kMxDown, false)
   LUTQ_MX_CASE(32, kMxDown, false)
+  LUTQ_MX_CASE(64, kMxDown, false)
   LUTQ_MX_CASE(128, kMxDown, false)
 #undef LUTQ_MX_CASE
   return cudaErrorInvalidValue;
@@ -583,29 +596,62 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+static EncodeTiledFn encode_fn() {
+  static EncodeTiledFn enc = nullptr;
+  if (enc == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      enc = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return enc;
+}
+
+static cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int dims, const void* base,
+                          const cuuint64_t* dim, const cuuint64_t* stride, const cuuint32_t* box,
+                          CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t one[3] = {1, 1, 1};
+  CUresult r = enc(map, type, cuuint32_t(dims), const_cast<void*>(base), dim, stride, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_mx_scale_map(CUtensorMap* map, const void* packed, int64_t rows, int64_t K,
+                              int64_t batch, int64_t stride, int fmt) {
+  const int per = mx_chunk_bytes(fmt) / 1024;
+  const cuuint64_t dims[3] = {
+      256, cuuint64_t(mx_ceil(rows, kMxRowTile) * mx_ceil(K, kMxChunk) * per), cuuint64_t(batch)};
+  const cuuint64_t strides[2] = {1024, cuuint64_t(stride)};
+  const cuuint32_t box[3] = {256, cuuint32_t(per), 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3,
+                static_cast<const uint8_t*>(packed) + mx_scale_off(rows, K), dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+cudaError_t make_mx_out_map(CUtensorMap* map, void* y, int64_t M, int64_t N, int dtype) {
+  const int es = dtype == LUTQ_FP32 ? 4 : 2;
+  const cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(M)};
+  const cuuint64_t strides[1] = {cuuint64_t(N * es)};
+  const cuuint32_t box[2] = {128, 32};
+  return encode(map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 // The codes of `batch` matrices [rows, K/2 bytes], `stride` bytes apart, in
 // boxes of 128 bytes x box_rows with the 128-byte swizzle; rows and columns
 // beyond a matrix read as zero.
 cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K,
                         int64_t batch, int64_t stride, int box_rows) {
-  static EncodeTiledFn enc = nullptr;
-  if (enc == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return cudaErrorNotSupported;
-    enc = reinterpret_cast<EncodeTiledFn>(p);
-  }
   const cuuint64_t dims[3] = {cuuint64_t(K / 2), cuuint64_t(rows), cuuint64_t(batch)};
   const cuuint64_t strides[2] = {cuuint64_t(K / 2), cuuint64_t(stride)};
   const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Split a tile's K over a cluster while that gives idle multiprocessors work
@@ -621,23 +667,43 @@ void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int*
   *clusters = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / s)));
 }
 
-static int mx_tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+constexpr int64_t kPairMinTokens = 64;
+
+int mx_tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 // y[M, N] = x w^T.  x: the packed tokens, or (xq) M <= 16 rows of values.
 cudaError_t launch_mx_product(const void* x, int x_dtype, bool xq, int64_t M, const void* packed,
                               int fmt, int64_t N, int64_t K, void* y, int y_dtype,
                               int32_t* dev_status, int num_sms, cudaStream_t stream) {
-  const int nt = mx_tile_tokens(M);
-  CUtensorMap t[3];
-  std::memset(t, 0, sizeof(t));
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   const uint8_t* xp = static_cast<const uint8_t*>(x);
+  if (M > kPairMinTokens) {
+    const int64_t tiles = mx_ceil(N, 256) * mx_ceil(M, 256);
+    if (tiles * 4 >= num_sms) {
+      MxGemmArgs g = {};
+      g.a_rows[0] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));
+      g.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
+      g.y = y;
+      g.y_dtype = y_dtype;
+      g.dev_status = dev_status;
+      g.N = N;
+      g.M = M;
+      g.K = K;
+      g.chunks = int(mx_ceil(K, kMxChunk));
+      return launch_mx_pair(g, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain, tiles,
+                            num_sms, stream);
+    }
+  }
+  const int nt = mx_tile_tokens(M);
+  CUtensorMap t[4];
+  std::memset(t, 0, sizeof(t));
   cudaError_t err = make_mx_map(&t[0], w, N, K, 1, mx_bytes(N, K, fmt), 128);
   if (err != cudaSuccess) return err;
   t[1] = t[0];
-  if (xq) t[2] = t[0];
-  else if ((err = make_mx_map(&t[2], xp, M, K, 1, mx_bytes(M, K, fmt), nt)) != cudaSuccess)
-    return err;
+  if (!xq) {
+    if ((err = make_mx_map(&t[2], xp, M, K, 1, mx_bytes(M, K, fmt), nt)) != cudaSuccess) return err;
+    if ((err = make_mx_map(&t[3], xp, M, K, 1, mx_bytes(M, K, fmt), 16)) != cudaSuccess) return err;
+  }
   MxGemmArgs a = {};
   a.a_scales[0] = a.a_scales[1] = w + mx_scale_off(N, K);
   a.a_rows[0] = a.a_rows[1] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));

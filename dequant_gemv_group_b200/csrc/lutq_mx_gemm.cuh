@@ -43,6 +43,23 @@ cudaError_t launch_mx_gemm(const CUtensorMap* tmaps, const MxGemmArgs& a, int fm
 cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K,
                         int64_t batch, int64_t stride, int box_rows);
 
+// Their scale chunks: rows of 1024 bytes, one or two a chunk.
+cudaError_t make_mx_scale_map(CUtensorMap* map, const void* packed, int64_t rows, int64_t K,
+                              int64_t batch, int64_t stride, int fmt);
+// An output [M, N], in boxes of 128 columns x 32 rows.
+cudaError_t make_mx_out_map(CUtensorMap* map, void* y, int64_t M, int64_t N, int dtype);
+
+// The kernel for many tokens (lutq_mx_pair.cu).
+struct MxPairMaps {
+  CUtensorMap a[2], b, b16, sa[2], sb, y;
+};
+cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void* weights2,
+                           int64_t w_bytes, const void* tokens, int64_t token_rows, int fmt,
+                           int mode, int64_t tiles, int num_sms, cudaStream_t stream);
+
+// Tokens per tile of mx_gemm_kernel: one tile for up to 128.
+int mx_tile_tokens(int64_t M);
+
 // Blocks of a launch: how many share a tile by K, and how many tiles run at once.
 void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
               int* clusters);

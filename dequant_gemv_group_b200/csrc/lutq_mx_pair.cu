@@ -1,0 +1,485 @@
+// The product of two microscaled 4-bit matrices for many tokens: pairs of
+// thread blocks (cta_group::2), tiles of 256 weight rows by up to 256 tokens.
+//
+// The arithmetic of lutq_mx_gemm.cu, laid out for a dense contraction.  Two
+// blocks on neighbouring multiprocessors issue one MMA of 256 rows: each loads its
+// own 128 weight rows and half of the tokens, so a 256 x 256 tile takes
+// 64 bytes a clock and multiprocessor from L2 at the tensor core's full rate (one
+// block alone with 128 x 256 would take 96).  Scales of the tokens are loaded
+// by both blocks, which each need all of them in tensor memory.
+//
+// A tile's sums fill 256 of the 512 columns.  The next tile's sums begin where
+// the columns end that remain beside the scales, so that two tiles overlap by
+// 64 (mxfp4) or 96 (nvfp4) columns: the epilogue empties those first, and the
+// next tile's MMAs run while it empties the others.
+//
+// Epilogue: eight warps, 32 columns (tokens) at a time through shared memory
+// and tensor-map stores, which also clip the tile to the output.
+#include <algorithm>
+#include <cstring>
+
+#include "lutq_mx_gemm.cuh"
+#include "lutq_sm100.cuh"
+
+namespace lutq {
+
+using namespace sm100;
+
+constexpr uint64_t kPairWaitNs = 2000000000ull;
+constexpr int kPairMaxStages = 8;
+constexpr int kPairThreads = 64 + 256;
+constexpr int kPairTokenGroup = 16;  // token tiles that share a pass over the weights
+
+template <int FMT, int MODE>
+struct PairCfg {
+  static constexpr int ND = MODE == kMxGateUp ? 2 : 1;
+  static constexpr int NT = 256 / ND;                    // tokens of a tile at most
+  static constexpr int CH = mx_chunk_bytes(FMT);
+  static constexpr int BLOCKS = CH / 512;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = NT / 2 * 128;
+  static constexpr int STAGE = ND * A_BYTES + B_BYTES + (ND + 2) * CH;
+  static constexpr int SF_COLS = (ND + 2) * BLOCKS * 4;  // one set; two are kept
+  static constexpr int SECOND = (512 - 2 * SF_COLS - 256) / 32 * 32;  // the other tile's sums
+  static constexpr int SHARED_COLS = 256 - SECOND;       // columns of both
+};
+
+struct PairShared {
+  uint64_t full[kPairMaxStages], empty[kPairMaxStages];
+  uint64_t acc_full, acc_free, drain;
+  uint32_t tmem;
+  int abort;
+};
+
+struct PairArgs {
+  MxGemmArgs g;
+  int token_tiles;    // plain: ceil(M / NT)
+  int pairs;          // pairs of blocks in the launch
+  int tma_store;      // y by tensor-map stores (row pitch a multiple of 16 bytes)
+};
+
+// Columns of a tile with `valid` tokens: each block loads half of them, in
+// boxes of 16.
+__device__ __forceinline__ int pair_width(int valid) { return (valid + 31) / 32 * 32; }
+
+__device__ __forceinline__ float pair_silu_mul(float g, float u) {
+  return __fdividef(g, 1.f + __expf(-g)) * u;
+}
+
+__device__ __forceinline__ void pair_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_ns() - t0 > kPairWaitNs) return;
+}
+
+// Whether `ok` holds in all 128 threads that meet at named barrier `id`.
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(ok)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Tile t of a launch: token tiles vary fastest (in groups), so that a weight
+// tile is read from memory once per group and then from L2.
+// Tiles begin at multiples of 128 tokens (the height of a scale block), a last
+// one is as wide as its tokens need.
+template <int MODE>
+struct PairTiles {
+  static constexpr int nt = MODE == kMxGateUp ? 128 : 256;
+  const int32_t* counts;
+  int mtiles, experts, token_tiles, e = 0, e_tiles = 0;
+  int64_t e_first = 0, tokens;
+  __device__ PairTiles(const PairArgs& a, const int32_t* c)
+      : counts(c), mtiles(int(mx_ceil(a.g.N, 256))), experts(a.g.experts),
+        token_tiles(a.token_tiles), tokens(a.g.M) {
+    if (MODE != kMxPlain) {
+      tokens = counts[0];
+      token_tiles = int(mx_ceil(tokens, nt));
+      e_tiles = token_tiles * mtiles;
+    }
+  }
+  __device__ bool at(int64_t t, int* expert, int* mt, int* m0, int* valid) {
+    if constexpr (MODE != kMxPlain) {
+      while (t >= e_first + e_tiles) {
+        e_first += e_tiles;
+        if (++e >= experts) {
+          e = experts - 1;
+          e_tiles = 0;
+          return false;
+        }
+        tokens = counts[e];
+        token_tiles = int(mx_ceil(tokens, nt));
+        e_tiles = token_tiles * mtiles;
+      }
+      t -= e_first;
+    } else {
+      if (t >= int64_t(token_tiles) * mtiles) return false;
+    }
+    const int64_t per_group = int64_t(kPairTokenGroup) * mtiles;
+    const int g = int(t / per_group), r = int(t - g * per_group);
+    const int width = min(kPairTokenGroup, token_tiles - g * kPairTokenGroup);
+    const int w = r / width;
+    *expert = e;
+    *mt = w;
+    *m0 = (g * kPairTokenGroup + (r - w * width)) * nt;
+    *valid = int(min(int64_t(nt), tokens - *m0));
+    return true;
+  }
+};
+
+template <int FMT, int MODE, int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                   const __grid_constant__ CUtensorMap tmap_a2,
+                   const __grid_constant__ CUtensorMap tmap_b,
+                   const __grid_constant__ CUtensorMap tmap_b16,
+                   const __grid_constant__ CUtensorMap tmap_sa,
+                   const __grid_constant__ CUtensorMap tmap_sa2,
+                   const __grid_constant__ CUtensorMap tmap_sb,
+                   const __grid_constant__ CUtensorMap tmap_y, const PairArgs p) {
+  using Cfg = PairCfg<FMT, MODE>;
+  constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS;
+  constexpr int ES = DT == LUTQ_FP32 ? 4 : 2;
+  constexpr int SLICE = 32 * 128 * ES;  // a staged slice of 32 tokens
+  const MxGemmArgs& a = p.g;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int ST = a.stages;
+  uint8_t* staging = smem + ST * Cfg::STAGE;                       // [2 groups][2] slices
+  PairShared* sh = reinterpret_cast<PairShared*>(staging + 4 * SLICE);
+  int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  volatile int* abort = &sh->abort;
+  auto full = [&](int s) { return smem_addr(&sh->full[s]); };
+  auto empty = [&](int s) { return smem_addr(&sh->empty[s]); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(smem_addr(&sh->acc_full), 1);
+    mbar_init(smem_addr(&sh->acc_free), 16);  // eight warps of both blocks
+    mbar_init(smem_addr(&sh->drain), 1);
+    sh->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(&sh->tmem), 512);
+    tmem_relinquish_pair();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (MODE != kMxPlain) {
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+      counts[e] = a.counts[e];
+      counts[a.experts + e] = a.bases[e];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const int64_t first = blockIdx.x >> 1, step = p.pairs;
+  PairTiles<MODE> tiles(p, counts);
+  int expert, mt, m0, valid;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies (both blocks)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
+        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+        const int arow = mt * 256 + int(rank) * 128;
+        const int half = pair_width(valid) / 2;
+        // the token scales of one or two tiles of 128 rows
+        const int sb_tiles = half > kMxRowTile / 2 ? 2 : 1;
+        const uint32_t bytes =
+            2u * uint32_t(ND * (Cfg::A_BYTES + CH) + half * 128 + sb_tiles * CH);
+        for (int c = 0; c < a.chunks; ++c) {
+          if (!(ok = mbar_wait(empty(s), ph, abort, kPairWaitNs))) break;
+          const uint32_t st = sbase + s * Cfg::STAGE;
+          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
+          const uint32_t bar = cluster_map(full(s), 0);
+          if (rank == 0) mbar_expect_tx(full(s), bytes);
+          tma_3d_g2s_pair(st, &tmap_a, c * 128, arow, expert, bar);
+          tma_3d_g2s_pair(sf, &tmap_sa, 0, ((arow / 128) * a.chunks + c) * (CH / 1024), expert,
+                          bar);
+          if (ND == 2) {
+            tma_3d_g2s_pair(st + Cfg::A_BYTES, &tmap_a2, c * 128, arow, expert, bar);
+            tma_3d_g2s_pair(sf + CH, &tmap_sa2, 0, ((arow / 128) * a.chunks + c) * (CH / 1024),
+                            expert, bar);
+          }
+          if (2 * half == Cfg::NT) {
+            tma_3d_g2s_pair(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0 + int(rank) * half, 0,
+                            bar);
+          } else {
+            for (int i = 0; i < half; i += 16)
+              tma_3d_g2s_pair(st + ND * Cfg::A_BYTES + i * 128, &tmap_b16, c * 128,
+                              row0 + int(rank) * half + i, 0, bar);
+          }
+          for (int i = 0; i < sb_tiles; ++i)
+            tma_3d_g2s_pair(sf + (ND + i) * CH, &tmap_sb, 0,
+                            ((row0 / kMxRowTile + i) * a.chunks + c) * (CH / 1024), 0, bar);
+          ++issued;
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (*abort && rank == 0) {  // let both blocks' copies land before either leaves
+        const int64_t n = issued < ST ? issued : ST;
+        for (int64_t i = issued - n; i < issued; ++i)
+          pair_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (first block)
+    if (lane == 0 && rank == 0) {
+      constexpr bool E8 = FMT == LUTQ_MXFP4;
+      int s = 0, it = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true, any = false;
+      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+        // the tile before must have left the shared columns
+        if (n > 0 && !(ok = mbar_wait_cluster(smem_addr(&sh->acc_free), uint32_t(n - 1) & 1u,
+                                              abort, kPairWaitNs)))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t((n & 1) * Cfg::SECOND);
+        const int width = pair_width(valid), sb_tiles = width > kMxRowTile ? 2 : 1;
+        for (int c = 0; c < a.chunks; ++c, ++it) {
+          if (!(ok = mbar_wait(full(s), ph, abort, kPairWaitNs))) break;
+          tc_fence_after();
+          const uint32_t st = sbase + s * Cfg::STAGE;
+          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
+          const uint32_t sf_tmem = tmem + 512u - uint32_t(2 - (it & 1)) * Cfg::SF_COLS;
+          const uint32_t sb_tmem = sf_tmem + ND * BLOCKS * 4;
+#pragma unroll
+          for (int i = 0; i < ND * BLOCKS; ++i)
+            tmem_cp_scales_pair(sf_tmem + 4 * i, smem_desc_scales(sf + 512 * i));
+          // the tokens' blocks side by side: [block][row tile]
+          for (int h = 0; h < sb_tiles; ++h)
+#pragma unroll
+            for (int i = 0; i < BLOCKS; ++i)
+              tmem_cp_scales_pair(sb_tmem + 8 * i + 4 * h,
+                                  smem_desc_scales(sf + (ND + h) * CH + 512 * i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int blk = E8 ? j >> 1 : j, id = E8 ? (j & 1) * 2 : 0;
+            const uint32_t idesc = idesc_e2m1(256, width, E8, id);
+            const uint64_t bd = smem_desc_k_sw128(st + ND * Cfg::A_BYTES + 32 * j);
+#pragma unroll
+            for (int w = 0; w < ND; ++w)
+              mma_e2m1_pair<!E8>(d + w * Cfg::NT, smem_desc_k_sw128(st + w * Cfg::A_BYTES + 32 * j),
+                                 bd, idesc, sf_tmem + 4 * (w * BLOCKS + blk),
+                                 sb_tmem + 8 * blk, (c > 0 || j > 0) ? 1u : 0u);
+          }
+          mma_commit_pair(empty(s));
+          any = true;
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(smem_addr(&sh->acc_full));
+      }
+      if (*abort && any) {
+        mma_commit_pair(smem_addr(&sh->drain));
+        pair_drain(smem_addr(&sh->drain), 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, group = (warp - 2) >> 2;  // four warps cover the 128 lanes
+    const bool leader = (warp - 2) % 4 == 0 && lane == 0;
+    uint8_t* stage0 = staging + group * 2 * SLICE;
+    int n = 0, slot = 0;
+    bool ok = true;
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+      ok = mbar_wait(smem_addr(&sh->acc_full), uint32_t(n) & 1u, abort, kPairWaitNs);
+      // the four warps of a group share the barriers below: they go on
+      // together or not at all
+      if (!group_all(1 + group, ok)) break;
+      tc_fence_after();
+      const int row0 = mt * 256 + int(rank) * 128;
+      const int row = row0 + quarter * 32 + lane;
+      const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t((n & 1) * Cfg::SECOND);
+      float ga[2] = {1.f, 1.f};
+      if (FMT == LUTQ_NVFP4 && row < a.N) {
+#pragma unroll
+        for (int w = 0; w < ND; ++w)
+          ga[w] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.a_rows[w]) +
+                                                  int64_t(expert) * a.a_stride + int64_t(row) * 4);
+      }
+      // slices of 32 columns.  Those that the next tile's sums share come
+      // first: the last ones of an even tile (columns SECOND..255), the first
+      // ones of an odd tile.  With two sets the shared columns are the end of
+      // the second or the beginning of the first.
+      constexpr int NS = Cfg::NT / 32;
+      constexpr int SHARED = Cfg::SHARED_COLS / 32 < NS ? Cfg::SHARED_COLS / 32 : NS;
+      int left = SHARED;  // shared slices not yet read (by both groups of warps)
+#pragma unroll 1
+      for (int i = 0; i < NS; ++i) {
+        const int sl = (n & 1) == 0 ? NS - 1 - i : i;
+        const int c = sl * 32;
+        if ((i & 1) == group && c < valid) {
+          uint32_t v[ND][32];
+#pragma unroll
+          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + c, v[w]);
+          tmem_wait_ld();
+          uint8_t* stg = stage0 + slot * SLICE;
+          // the store that read this buffer last must be done
+          if (leader) bulk_wait_read<1>();
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+          const float4* gb = reinterpret_cast<const float4*>(a.b_rows + token0 + c);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float4 s4 = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (FMT == LUTQ_NVFP4) s4 = gb[q];
+            const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+              const int j = 4 * q + l;
+              float f = __uint_as_float(v[0][j]);
+              if (FMT == LUTQ_NVFP4) f = f * ga[0] * sc[l];
+              if (ND == 2) {
+                float u = __uint_as_float(v[ND - 1][j]);
+                if (FMT == LUTQ_NVFP4) u = u * ga[1] * sc[l];
+                f = pair_silu_mul(f, u);
+              }
+              store1<DT>(stg, j * 128 + quarter * 32 + lane, f);
+            }
+          }
+          if (p.tma_store) {
+            fence_async_shared();
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+            if (leader) {
+              tma_2d_s2g(&tmap_y, row0, int(token0) + c, smem_addr(stg));
+              bulk_commit();
+            }
+          } else {
+            // rows that no 16-byte copy can write: each warp its own lanes
+            __syncwarp();
+            if (row < a.N)
+              for (int j = 0; j < 32 && c + j < valid; ++j) {
+                const int64_t at = (token0 + c + j) * a.N + row;
+                if (ES == 4)
+                  static_cast<uint32_t*>(a.y)[at] =
+                      reinterpret_cast<const uint32_t*>(stg)[j * 128 + quarter * 32 + lane];
+                else
+                  static_cast<uint16_t*>(a.y)[at] =
+                      reinterpret_cast<const uint16_t*>(stg)[j * 128 + quarter * 32 + lane];
+              }
+          }
+          slot ^= 1;
+        }
+        if (--left == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), 0));
+        }
+      }
+    }
+    if (leader) bulk_wait<0>();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort) report(a.dev_status, LUTQ_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ host side
+
+template <int FMT, int MODE, int DT>
+static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, int num_sms, cudaStream_t stream) {
+  using Cfg = PairCfg<FMT, MODE>;
+  constexpr int SLICE = 32 * 128 * (DT == LUTQ_FP32 ? 4 : 2);
+  const int fixed = 1024 + 4 * SLICE + int(sizeof(PairShared)) +
+                    (MODE != kMxPlain ? 8 * p.g.experts : 0);
+  constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
+  p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::STAGE);
+  auto kernel = mx_pair_kernel<FMT, MODE, DT>;
+  static bool granted[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!granted[dev]) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    granted[dev] = true;
+  }
+  return launch_pdl(kernel, dim3(unsigned(2 * p.pairs)), dim3(kPairThreads), size_t(smem), stream,
+                    m.a[0], m.a[1], m.b, m.b16, m.sa[0], m.sa[1], m.sb, m.y, p);
+}
+
+template <int FMT>
+static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode, int num_sms,
+                              cudaStream_t stream) {
+  if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16>(m, p, num_sms, stream);
+  if (mode == kMxDown) return launch_one<FMT, kMxDown, LUTQ_FP32>(m, p, num_sms, stream);
+  if (p.g.y_dtype == LUTQ_BF16) return launch_one<FMT, kMxPlain, LUTQ_BF16>(m, p, num_sms, stream);
+  if (p.g.y_dtype == LUTQ_FP16) return launch_one<FMT, kMxPlain, LUTQ_FP16>(m, p, num_sms, stream);
+  return launch_one<FMT, kMxPlain, LUTQ_FP32>(m, p, num_sms, stream);
+}
+
+cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void* weights2,
+                           int64_t w_bytes, const void* tokens, int64_t token_rows, int fmt,
+                           int mode, int64_t tiles, int num_sms, cudaStream_t stream) {
+  MxPairMaps m;
+  std::memset(&m, 0, sizeof(m));
+  const int64_t batch = std::max(1, g.experts);
+  const void* w[2] = {weights, weights2};
+  cudaError_t err;
+  const int nd = mode == kMxGateUp ? 2 : 1;
+  for (int i = 0; i < nd; ++i) {
+    if ((err = make_mx_map(&m.a[i], w[i], g.N, g.K, batch, w_bytes, 128)) != cudaSuccess)
+      return err;
+    if ((err = make_mx_scale_map(&m.sa[i], w[i], g.N, g.K, batch, w_bytes, fmt)) != cudaSuccess)
+      return err;
+  }
+  const int64_t t_bytes = mx_bytes(token_rows, g.K, fmt);
+  const int nt = mode == kMxGateUp ? 128 : 256;
+  if ((err = make_mx_map(&m.b, tokens, token_rows, g.K, 1, t_bytes, nt / 2)) != cudaSuccess)
+    return err;
+  if ((err = make_mx_map(&m.b16, tokens, token_rows, g.K, 1, t_bytes, 16)) != cudaSuccess)
+    return err;
+  if ((err = make_mx_scale_map(&m.sb, tokens, token_rows, g.K, 1, t_bytes, fmt)) != cudaSuccess)
+    return err;
+  const int dt = mode == kMxGateUp ? int(LUTQ_BF16) : mode == kMxDown ? int(LUTQ_FP32) : g.y_dtype;
+  PairArgs p = {};
+  p.g = g;
+  p.token_tiles = int(mx_ceil(g.M, nt));
+  p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms / 2)));
+  p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0;
+  if (p.tma_store) {
+    if ((err = make_mx_out_map(&m.y, g.y, g.M, g.N, dt)) != cudaSuccess) return err;
+  }
+  return fmt == LUTQ_MXFP4 ? launch_fmt<LUTQ_MXFP4>(m, p, mode, num_sms, stream)
+                           : launch_fmt<LUTQ_NVFP4>(m, p, mode, num_sms, stream);
+}
+
+}  // namespace lutq

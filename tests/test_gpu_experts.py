@@ -163,6 +163,18 @@ def test_uneven_skipped_and_repeated(lq, fmt):
     assert (y[10] == 0).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("t,e", [(60, 40), (200, 40)])
+def test_most_tokens_to_one_expert(lq, fmt, t, e):
+    """Few tokens an expert on average, but one has more than a tile holds."""
+    d, f = 160, 96
+    layer = Layer(lq, e, d, f, fmt, seed=e)
+    x, z = _inputs(t, e, 1, d, seed=t)
+    z[:, 3] += 3.5
+    ids, w = lq.lutq_route(z, 2)
+    _close(layer.run(x, ids, w), *layer.reference(x, ids, w))
+
+
 def test_rows_do_not_depend_on_the_batch(lq):
     layer = Layer(lq, 6, 256, 224, "mxfp4", seed=8)
     x, z = _inputs(300, 6, 2, 256, seed=9)

@@ -164,7 +164,11 @@ def _case(lq, m, n, k, fmt, seed=0):
 SHAPES = [(1, 1, 32), (1, 128, 256), (2, 7, 96), (3, 256, 512), (8, 1000, 2048), (15, 130, 4128),
           (16, 64, 14336), (17, 33, 288), (31, 513, 1024), (33, 128, 4096), (64, 640, 800),
           (65, 96, 2080), (127, 257, 544), (128, 384, 4096), (129, 1024, 256), (200, 200, 3232),
-          (300, 2049, 96), (513, 300, 1056)]
+          (300, 2049, 96), (513, 300, 1056),
+          # enough tiles for the kernel of block pairs: 1 and 2 token tiles, row pitches that no
+          # 16-byte copy can write, tokens beyond one pass over the weights
+          (77, 9601, 288), (160, 9480, 64), (300, 8200, 96), (600, 4096, 544), (1000, 2564, 1312),
+          (4099, 640, 160)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
