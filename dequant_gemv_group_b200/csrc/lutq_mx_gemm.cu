@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
   MxShared* sh = reinterpret_cast<MxShared*>(smem + ST * Cfg::STAGE + (split > 1 ? Cfg::RECV : 0));
   int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);  // experts' row counts, then bases
   const uint32_t sbase = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp-uniform for the compiler, too
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   volatile int* abort = &sh->abort;
   auto full = [&](int s) { return smem_addr(&sh->full[s]); };
   auto empty = [&](int s) { return smem_addr(&sh->empty[s]); };
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
   __syncthreads();
   tc_fence_after();
   if (split > 1) cluster_sync_all();  // every block's barriers are set up
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
   const int64_t first = blockIdx.x / split, step = gridDim.x / split;
   const int c0 = int(int64_t(a.chunks) * rank / split);
@@ -241,55 +242,60 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      constexpr bool E8 = FMT == LUTQ_MXFP4;
-      int s = 0, it = 0, n = 0;
-      uint32_t ph = 0;
-      bool ok = true, any = false;
-      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
-        const int b = Cfg::ACC == 2 ? n & 1 : 0;
-        const uint32_t use = uint32_t(Cfg::ACC == 2 ? n >> 1 : n);
-        if (!(ok = mbar_wait(smem_addr(&sh->acc_empty[b]), (use & 1u) ^ 1u, abort, kMxWaitNs)))
-          break;
+    constexpr bool E8 = FMT == LUTQ_MXFP4;
+    int s = 0, it = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true, any = false;
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+      const int b = Cfg::ACC == 2 ? n & 1 : 0;
+      const uint32_t use = uint32_t(Cfg::ACC == 2 ? n >> 1 : n);
+      ok = mbar_wait(smem_addr(&sh->acc_empty[b]), (use & 1u) ^ 1u, abort, kMxWaitNs);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + uint32_t(b * ND * NT);
+      const int width = XQ ? NT : (valid + 15) / 16 * 16;
+      const uint32_t idesc = idesc_e2m1(128, width, E8, 0);
+      const uint32_t id2 = idesc_e2m1(0, 0, false, 2);  // the scale bytes 2 and 3
+      for (int c = c0; c < c1; ++c, ++it) {
+        ok = mbar_wait(full(s), ph, abort, kMxWaitNs);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const uint32_t d = tmem + uint32_t(b * ND * NT);
-        const int width = XQ ? NT : (valid + 15) / 16 * 16;
-        for (int c = c0; c < c1; ++c, ++it) {
-          if (!(ok = mbar_wait(full(s), ph, abort, kMxWaitNs))) break;
-          tc_fence_after();
-          const uint32_t st = sbase + s * Cfg::STAGE;
-          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
-          const uint32_t sf_tmem = tmem + uint32_t(Cfg::ACC * ND * NT + (it & 1) * (Cfg::SF_COLS / 2));
+        const uint32_t st = desc_lo(sbase + s * Cfg::STAGE);
+        const uint32_t bl = st + ((ND * Cfg::A_BYTES) >> 4);
+        const uint32_t sf = bl + (Cfg::B_BYTES >> 4);
+        const uint32_t sf_tmem =
+            tmem + uint32_t(Cfg::ACC * ND * NT + (it & 1) * (Cfg::SF_COLS / 2));
+        if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < (ND + 1) * BLOCKS; ++i)
-            tmem_cp_scales(sf_tmem + 4 * i, smem_desc_scales(sf + 512 * i));
+          for (int i = 0; i < (ND + 1) * BLOCKS; ++i) tmem_cp_scales(sf_tmem + 4 * i, sf + 32 * i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             // mxfp4: a block holds the scales of two MMAs, nvfp4: of one
-            const int blk = E8 ? j >> 1 : j, id = E8 ? (j & 1) * 2 : 0;
-            const uint32_t idesc = idesc_e2m1(128, width, E8, id);
-            const uint64_t bd = smem_desc_k_sw128(st + ND * Cfg::A_BYTES + 32 * j);
-            const uint32_t sb = sf_tmem + 4 * (ND * BLOCKS + blk);
+            const int blk = E8 ? j >> 1 : j;
 #pragma unroll
             for (int w = 0; w < ND; ++w)
-              mma_e2m1_ss<!E8>(d + w * NT, smem_desc_k_sw128(st + w * Cfg::A_BYTES + 32 * j), bd,
-                               idesc, sf_tmem + 4 * (w * BLOCKS + blk), sb,
-                               (c > c0 || j > 0) ? 1u : 0u);
+              mma_e2m1_ss<!E8>(d + w * NT, st + ((w * Cfg::A_BYTES) >> 4) + 2 * j, bl + 2 * j,
+                               E8 && (j & 1) ? idesc | id2 : idesc,
+                               sf_tmem + 4 * (w * BLOCKS + blk),
+                               sf_tmem + 4 * (ND * BLOCKS + blk), (c > c0 || j > 0) ? 1u : 0u);
           }
           mma_commit(empty(s));
-          any = true;
-          if (++s == ST) {
-            s = 0;
-            ph ^= 1;
-          }
         }
-        if (!ok) break;
-        mma_commit(smem_addr(&sh->acc_full[b]));
+        __syncwarp();
+        any = true;
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (*abort && any) {
-        mma_commit(smem_addr(&sh->drain));
-        mx_drain(smem_addr(&sh->drain), 0);
-      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(smem_addr(&sh->acc_full[b]));
+      __syncwarp();
+    }
+    if (__any_sync(0xffffffffu, *abort) && any) {
+      if (elect_one()) mma_commit(smem_addr(&sh->drain));
+      __syncwarp();
+      mx_drain(smem_addr(&sh->drain), 0);
     }
   } else if (warp < kMxQuantWarp) {
     // ------------------------------------------------------------ epilogue

@@ -156,7 +156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   PairShared* sh = reinterpret_cast<PairShared*>(staging + 4 * SLICE);
   int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);
   const uint32_t sbase = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp-uniform for the compiler, too
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   volatile int* abort = &sh->abort;
   auto full = [&](int s) { return smem_addr(&sh->full[s]); };
@@ -189,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const int64_t first = blockIdx.x >> 1, step = p.pairs;
   PairTiles<MODE> tiles(p, counts);
   int expert, mt, m0, valid;
@@ -249,47 +250,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (first block)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr bool E8 = FMT == LUTQ_MXFP4;
       int s = 0, it = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true, any = false;
       for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
         // the tile before must have left the shared columns
-        if (n > 0 && !(ok = mbar_wait_cluster(smem_addr(&sh->acc_free), uint32_t(n - 1) & 1u,
-                                              abort, kPairWaitNs)))
-          break;
+        if (n > 0) ok = mbar_wait_cluster(smem_addr(&sh->acc_free), uint32_t(n - 1) & 1u, abort,
+                                          kPairWaitNs);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t((n & 1) * Cfg::SECOND);
         const int width = pair_width(valid), sb_tiles = width > kMxRowTile ? 2 : 1;
+        const uint32_t idesc = idesc_e2m1(256, width, E8, 0);
+        const uint32_t id2 = idesc_e2m1(0, 0, false, 2);  // the scale bytes 2 and 3
         for (int c = 0; c < a.chunks; ++c, ++it) {
-          if (!(ok = mbar_wait(full(s), ph, abort, kPairWaitNs))) break;
+          ok = mbar_wait(full(s), ph, abort, kPairWaitNs);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          const uint32_t st = sbase + s * Cfg::STAGE;
-          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
+          const uint32_t st = desc_lo(sbase + s * Cfg::STAGE);
+          const uint32_t bl = st + ((ND * Cfg::A_BYTES) >> 4);
+          const uint32_t sf = bl + (Cfg::B_BYTES >> 4);
           const uint32_t sf_tmem = tmem + 512u - uint32_t(2 - (it & 1)) * Cfg::SF_COLS;
           const uint32_t sb_tmem = sf_tmem + ND * BLOCKS * 4;
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < ND * BLOCKS; ++i)
-            tmem_cp_scales_pair(sf_tmem + 4 * i, smem_desc_scales(sf + 512 * i));
-          // the tokens' blocks side by side: [block][row tile]
-          for (int h = 0; h < sb_tiles; ++h)
+            for (int i = 0; i < ND * BLOCKS; ++i) tmem_cp_scales_pair(sf_tmem + 4 * i, sf + 32 * i);
+            // the tokens' blocks side by side: [block][row tile]
 #pragma unroll
             for (int i = 0; i < BLOCKS; ++i)
-              tmem_cp_scales_pair(sb_tmem + 8 * i + 4 * h,
-                                  smem_desc_scales(sf + (ND + h) * CH + 512 * i));
+              tmem_cp_scales_pair(sb_tmem + 8 * i, sf + ((ND * CH) >> 4) + 32 * i);
+            if (sb_tiles == 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int blk = E8 ? j >> 1 : j, id = E8 ? (j & 1) * 2 : 0;
-            const uint32_t idesc = idesc_e2m1(256, width, E8, id);
-            const uint64_t bd = smem_desc_k_sw128(st + ND * Cfg::A_BYTES + 32 * j);
+              for (int i = 0; i < BLOCKS; ++i)
+                tmem_cp_scales_pair(sb_tmem + 8 * i + 4, sf + (((ND + 1) * CH) >> 4) + 32 * i);
+            }
 #pragma unroll
-            for (int w = 0; w < ND; ++w)
-              mma_e2m1_pair<!E8>(d + w * Cfg::NT, smem_desc_k_sw128(st + w * Cfg::A_BYTES + 32 * j),
-                                 bd, idesc, sf_tmem + 4 * (w * BLOCKS + blk),
-                                 sb_tmem + 8 * blk, (c > 0 || j > 0) ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {
+              // mxfp4: a block holds the scales of two MMAs, nvfp4: of one
+              const int blk = E8 ? j >> 1 : j;
+#pragma unroll
+              for (int w = 0; w < ND; ++w)
+                mma_e2m1_pair<!E8>(d + w * Cfg::NT, st + ((w * Cfg::A_BYTES) >> 4) + 2 * j,
+                                   bl + 2 * j, E8 && (j & 1) ? idesc | id2 : idesc,
+                                   sf_tmem + 4 * (w * BLOCKS + blk), sb_tmem + 8 * blk,
+                                   (c > 0 || j > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(empty(s));
           }
-          mma_commit_pair(empty(s));
+          __syncwarp();
           any = true;
           if (++s == ST) {
             s = 0;
@@ -297,10 +307,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           }
         }
         if (!ok) break;
-        mma_commit_pair(smem_addr(&sh->acc_full));
+        if (elect_one()) mma_commit_pair(smem_addr(&sh->acc_full));
+        __syncwarp();
       }
-      if (*abort && any) {
-        mma_commit_pair(smem_addr(&sh->drain));
+      if (__any_sync(0xffffffffu, *abort) && any) {
+        if (elect_one()) mma_commit_pair(smem_addr(&sh->drain));
+        __syncwarp();
         pair_drain(smem_addr(&sh->drain), 0);
       }
     }

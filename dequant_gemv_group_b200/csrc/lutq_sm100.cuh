@@ -178,6 +178,27 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
+// One thread of the (converged) warp, the same one every time.  Code under it
+// stays warp-uniform for the compiler, which keeps the operands of the
+// instructions below in uniform registers: issued by "lane 0" instead, a
+// stage's fourteen operand moves took longer than its MMAs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
+// Shared-memory descriptors in two words; the high ones are constants.
+//  128-byte rows, 128-byte swizzle (8-row groups 1024 bytes apart): version 1
+//  (bit 46), swizzle mode 2 (bits 61..63);
+//  scale blocks, no swizzle, 8-row groups 128 bytes apart.
+// Low words: the address / 16, and 1 in the (unused) leading offset.
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHiScales = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
 // ---- block pairs (cta_group::2) ----------------------------------------------
 // Two blocks of a cluster, ranks 2i and 2i + 1, share one MMA: each holds half
 // of the first operand's rows and half of the second operand's.
@@ -207,30 +228,37 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols)
 // As mma_e2m1_ss and tmem_cp_scales, for the pair: descriptors and columns
 // name the same places in both blocks.
 template <bool BLOCK16>
-__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
-                                              uint32_t accumulate) {
+__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t sa_tmem, uint32_t sb_tmem,
+                                            uint32_t accumulate) {
   if constexpr (BLOCK16) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
+        "n"(kDescHiSw128)
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
+        "n"(kDescHiSw128)
         : "memory");
   }
 }
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t d_tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(desc)
-               : "memory");
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t d_tmem, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(d_tmem),
+      "r"(lo), "n"(kDescHiScales)
+      : "memory");
 }
 // Arrive on `bar` in both blocks once this thread's tcgen05 work is done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
@@ -285,24 +313,28 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 // memory, scale bytes in tensor memory, fp32 accumulate.  Blocks of 32 with
 // E8M0 scales (two bytes a row) or of 16 with E4M3 scales (four).
 template <bool BLOCK16>
-__device__ __forceinline__ void mma_e2m1_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+__device__ __forceinline__ void mma_e2m1_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t sa_tmem, uint32_t sb_tmem,
                                             uint32_t accumulate) {
   if constexpr (BLOCK16) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
+        "n"(kDescHiSw128)
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
+        "n"(kDescHiSw128)
         : "memory");
   }
 }
@@ -310,17 +342,12 @@ __device__ __forceinline__ void mma_e2m1_ss(uint32_t d_tmem, uint64_t a_desc, ui
 // Copy a 512-byte scale block (32 rows of 16 bytes) from shared memory into
 // four columns of tensor memory, into the 32 lanes of each of the four warps.
 // It is ordered before the MMAs that this thread issues after it.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t d_tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(desc)
-               : "memory");
-}
-// Shared-memory descriptor of such a block: no swizzle, 8-row groups of 128 bytes.
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= uint64_t((saddr >> 4) & 0x3FFFu);
-  d |= uint64_t(128 >> 4) << 32;
-  d |= uint64_t(1) << 46;
-  return d;
+__device__ __forceinline__ void tmem_cp_scales(uint32_t d_tmem, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(d_tmem),
+      "r"(lo), "n"(kDescHiScales)
+      : "memory");
 }
 // Instruction descriptor of the E2M1 product: both operands K-major, scale
 // type (1: E8M0, 0: E4M3), and which two of a row's four scale bytes it takes
