@@ -187,57 +187,56 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 1;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
-        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-        const int width = (valid + 15) / 16 * 16;  // columns: in boxes of 16 tokens
-        const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
-        const uint8_t* bs = a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
-        for (int c = c0; c < c1; ++c) {
-          if (!(ok = mbar_wait(empty(s), ph, abort, kMxWaitNs))) break;
-          const uint32_t st = sbase + s * Cfg::STAGE;
-          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
-          mbar_expect_tx(full(s), ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : width * 128 + CH));
+    int s = 0;
+    uint32_t ph = 1;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
+      const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const int width = (valid + 15) / 16 * 16;  // columns: in boxes of 16 tokens
+      const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
+      const uint8_t* as = a.a_scales[0] + a_off;
+      const uint8_t* as2 = a.a_scales[1] + a_off;
+      const uint8_t* bs = XQ ? nullptr : a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
+      const uint32_t bytes = ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : width * 128 + CH);
+      for (int c = c0; c < c1; ++c) {
+        ok = mbar_wait(empty(s), ph, abort, kMxWaitNs);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const uint32_t st = sbase + s * Cfg::STAGE;
+        const uint32_t sb = st + ND * Cfg::A_BYTES, sf = sb + Cfg::B_BYTES;
+        if (elect_one()) {
+          mbar_expect_tx(full(s), bytes);
           tma_3d_g2s(st, &tmap_a, c * 128, mt * 128, expert, full(s));
-          bulk_g2s(sf, a.a_scales[0] + a_off + int64_t(c) * CH, CH, full(s));
-          if (ND == 2) {
-            tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, c * 128, mt * 128, expert, full(s));
-            bulk_g2s(sf + CH, a.a_scales[1] + a_off + int64_t(c) * CH, CH, full(s));
-          }
+          if (ND == 2) tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, c * 128, mt * 128, expert, full(s));
+          bulk_g2s(sf, as + int64_t(c) * CH, CH, full(s));
+          if (ND == 2) bulk_g2s(sf + CH, as2 + int64_t(c) * CH, CH, full(s));
           if (!XQ) {
             if (width == NT) {
-              tma_3d_g2s(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0, 0, full(s));
+              tma_3d_g2s(sb, &tmap_b, c * 128, row0, 0, full(s));
             } else {
               for (int i = 0; i < width; i += 16)
-                tma_3d_g2s(st + ND * Cfg::A_BYTES + i * 128, &tmap_b16, c * 128, row0 + i, 0,
-                           full(s));
+                tma_3d_g2s(sb + i * 128, &tmap_b16, c * 128, row0 + i, 0, full(s));
             }
             bulk_g2s(sf + ND * CH, bs + int64_t(c) * CH, CH, full(s));
           }
-          ++issued;
-          if (++s == ST) {
-            s = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      // given up: the copies in flight must land before the block may exit
-      if (*abort) {
-        const int64_t n = issued < ST ? issued : ST;
-        for (int64_t i = issued - n; i < issued; ++i)
-          if (!XQ) mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
-        if (XQ) {
-          // the quantizing warps may not arrive any more: arrive for them,
-          // so that the barrier follows the copies alone
-          for (int64_t i = issued - n; i < issued; ++i) {
-            for (int w = 0; w < 4; ++w) mbar_arrive(full(int(i % ST)));
-            mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
-          }
-        }
+    }
+    // given up: the copies in flight must land before the block may exit
+    if (__any_sync(0xffffffffu, *abort)) {
+      const int64_t n = issued < ST ? issued : ST;
+      for (int64_t i = issued - n; i < issued; ++i) {
+        // the quantizing warps may not arrive any more: arrive for them, so
+        // that the barrier follows the copies alone
+        if (XQ && lane < 4) mbar_arrive(full(int(i % ST)));
+        __syncwarp();
+        mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
       }
     }
   } else if (warp == 1) {

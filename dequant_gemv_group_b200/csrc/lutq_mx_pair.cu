@@ -192,61 +192,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const int64_t first = blockIdx.x >> 1, step = p.pairs;
+  const uint32_t full0 = cluster_map(full(0), 0);  // the first block's barriers
   PairTiles<MODE> tiles(p, counts);
   int expert, mt, m0, valid;
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies (both blocks)
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 1;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
-        const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-        const int arow = mt * 256 + int(rank) * 128;
-        const int half = pair_width(valid) / 2;
-        // the token scales of one or two tiles of 128 rows
-        const int sb_tiles = half > kMxRowTile / 2 ? 2 : 1;
-        const uint32_t bytes =
-            2u * uint32_t(ND * (Cfg::A_BYTES + CH) + half * 128 + sb_tiles * CH);
-        for (int c = 0; c < a.chunks; ++c) {
-          if (!(ok = mbar_wait(empty(s), ph, abort, kPairWaitNs))) break;
-          const uint32_t st = sbase + s * Cfg::STAGE;
-          const uint32_t sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES;
-          const uint32_t bar = cluster_map(full(s), 0);
+    int s = 0;
+    uint32_t ph = 1;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
+      const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const int arow = mt * 256 + int(rank) * 128;
+      const int half = pair_width(valid) / 2;
+      const int brow = row0 + int(rank) * half;
+      // the token scales of one or two tiles of 128 rows
+      const int sb_tiles = half > kMxRowTile / 2 ? 2 : 1;
+      const uint32_t bytes = 2u * uint32_t(ND * (Cfg::A_BYTES + CH) + half * 128 + sb_tiles * CH);
+      const int sa_row = (arow / 128) * a.chunks * (CH / 1024);
+      const int sb_row = (row0 / kMxRowTile) * a.chunks * (CH / 1024);
+      for (int c = 0; c < a.chunks; ++c) {
+        ok = mbar_wait(empty(s), ph, abort, kPairWaitNs);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const uint32_t st = sbase + s * Cfg::STAGE;
+        const uint32_t sb = st + ND * Cfg::A_BYTES, sf = sb + Cfg::B_BYTES;
+        const uint32_t bar = full0 + 8 * s;
+        const int sc = c * (CH / 1024);
+        if (elect_one()) {
           if (rank == 0) mbar_expect_tx(full(s), bytes);
           tma_3d_g2s_pair(st, &tmap_a, c * 128, arow, expert, bar);
-          tma_3d_g2s_pair(sf, &tmap_sa, 0, ((arow / 128) * a.chunks + c) * (CH / 1024), expert,
-                          bar);
-          if (ND == 2) {
-            tma_3d_g2s_pair(st + Cfg::A_BYTES, &tmap_a2, c * 128, arow, expert, bar);
-            tma_3d_g2s_pair(sf + CH, &tmap_sa2, 0, ((arow / 128) * a.chunks + c) * (CH / 1024),
-                            expert, bar);
-          }
+          if (ND == 2) tma_3d_g2s_pair(st + Cfg::A_BYTES, &tmap_a2, c * 128, arow, expert, bar);
           if (2 * half == Cfg::NT) {
-            tma_3d_g2s_pair(st + ND * Cfg::A_BYTES, &tmap_b, c * 128, row0 + int(rank) * half, 0,
-                            bar);
+            tma_3d_g2s_pair(sb, &tmap_b, c * 128, brow, 0, bar);
           } else {
             for (int i = 0; i < half; i += 16)
-              tma_3d_g2s_pair(st + ND * Cfg::A_BYTES + i * 128, &tmap_b16, c * 128,
-                              row0 + int(rank) * half + i, 0, bar);
+              tma_3d_g2s_pair(sb + i * 128, &tmap_b16, c * 128, brow + i, 0, bar);
           }
-          for (int i = 0; i < sb_tiles; ++i)
-            tma_3d_g2s_pair(sf + (ND + i) * CH, &tmap_sb, 0,
-                            ((row0 / kMxRowTile + i) * a.chunks + c) * (CH / 1024), 0, bar);
-          ++issued;
-          if (++s == ST) {
-            s = 0;
-            ph ^= 1;
-          }
+          tma_3d_g2s_pair(sf, &tmap_sa, 0, sa_row + sc, expert, bar);
+          if (ND == 2) tma_3d_g2s_pair(sf + CH, &tmap_sa2, 0, sa_row + sc, expert, bar);
+          tma_3d_g2s_pair(sf + ND * CH, &tmap_sb, 0, sb_row + sc, 0, bar);
+          if (sb_tiles == 2)
+            tma_3d_g2s_pair(sf + (ND + 1) * CH, &tmap_sb, 0,
+                            sb_row + a.chunks * (CH / 1024) + sc, 0, bar);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      if (*abort && rank == 0) {  // let both blocks' copies land before either leaves
-        const int64_t n = issued < ST ? issued : ST;
-        for (int64_t i = issued - n; i < issued; ++i)
-          pair_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
-      }
+    }
+    if (__any_sync(0xffffffffu, *abort) && rank == 0) {
+      // let both blocks' copies land before either leaves
+      const int64_t n = issued < ST ? issued : ST;
+      for (int64_t i = issued - n; i < issued; ++i)
+        pair_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (first block)
