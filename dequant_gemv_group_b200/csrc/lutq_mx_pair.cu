@@ -48,6 +48,7 @@ struct PairShared {
   uint64_t acc_full, acc_free, drain;
   uint32_t tmem;
   int abort;
+  alignas(16) float row_scales[8][128];  // nvfp4: per epilogue warp, its tokens' of a tile
 };
 
 struct PairArgs {
@@ -323,92 +324,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     const int quarter = warp & 3, group = (warp - 2) >> 2;  // four warps cover the 128 lanes
     const bool leader = (warp - 2) % 4 == 0 && lane == 0;
     uint8_t* stage0 = staging + group * 2 * SLICE;
+    float* gbs = sh->row_scales[warp - 2];  // nvfp4: the row scales of this warp's tokens
     int n = 0, slot = 0;
     bool ok = true;
     for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
+      const int row0 = mt * 256 + int(rank) * 128;
+      const int row = row0 + quarter * 32 + lane;
+      const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t((n & 1) * Cfg::SECOND);
+      // slices of 32 columns, this group's are order(group), order(group + 2),
+      // ...: those that the next tile's sums share come first, the last ones
+      // of an even tile (columns SECOND..255) and the first ones of an odd
+      // tile.  (With two sets the shared columns are the end of the second or
+      // the beginning of the first.)
+      constexpr int NS = Cfg::NT / 32, OWN = NS / 2;
+      auto column = [&](int i) {
+        const int sl = group + 2 * i;
+        return 32 * ((n & 1) == 0 ? NS - 1 - sl : sl);
+      };
+      float ga[2] = {1.f, 1.f};
+      if (FMT == LUTQ_NVFP4) {
+        if (row < a.N) {
+#pragma unroll
+          for (int w = 0; w < ND; ++w)
+            ga[w] = *reinterpret_cast<const float*>(
+                reinterpret_cast<const uint8_t*>(a.a_rows[w]) + int64_t(expert) * a.a_stride +
+                int64_t(row) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+          if (column(i) < valid) gbs[32 * i + lane] = a.b_rows[token0 + column(i) + lane];
+        __syncwarp();
+      }
       ok = mbar_wait(smem_addr(&sh->acc_full), uint32_t(n) & 1u, abort, kPairWaitNs);
       // the four warps of a group share the barriers below: they go on
       // together or not at all
       if (!group_all(1 + group, ok)) break;
       tc_fence_after();
-      const int row0 = mt * 256 + int(rank) * 128;
-      const int row = row0 + quarter * 32 + lane;
-      const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-      const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t((n & 1) * Cfg::SECOND);
-      float ga[2] = {1.f, 1.f};
-      if (FMT == LUTQ_NVFP4 && row < a.N) {
+
+      // one slice: scale, round, stage, store
+      auto finish = [&](int i, uint32_t (&v)[ND][32]) {
+        const int c = column(i);
+        uint8_t* stg = stage0 + slot * SLICE;
+        // the store that read this buffer last must be done
+        if (leader) bulk_wait_read<1>();
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+        const float4* gb = reinterpret_cast<const float4*>(gbs + 32 * i);
 #pragma unroll
-        for (int w = 0; w < ND; ++w)
-          ga[w] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.a_rows[w]) +
-                                                  int64_t(expert) * a.a_stride + int64_t(row) * 4);
-      }
-      // slices of 32 columns.  Those that the next tile's sums share come
-      // first: the last ones of an even tile (columns SECOND..255), the first
-      // ones of an odd tile.  With two sets the shared columns are the end of
-      // the second or the beginning of the first.
-      constexpr int NS = Cfg::NT / 32;
-      constexpr int SHARED = Cfg::SHARED_COLS / 32 < NS ? Cfg::SHARED_COLS / 32 : NS;
-      int left = SHARED;  // shared slices not yet read (by both groups of warps)
-#pragma unroll 1
-      for (int i = 0; i < NS; ++i) {
-        const int sl = (n & 1) == 0 ? NS - 1 - i : i;
-        const int c = sl * 32;
-        if ((i & 1) == group && c < valid) {
-          uint32_t v[ND][32];
+        for (int q = 0; q < 8; ++q) {
+          float4 s4 = make_float4(1.f, 1.f, 1.f, 1.f);
+          if (FMT == LUTQ_NVFP4) s4 = gb[q];
+          const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + c, v[w]);
-          tmem_wait_ld();
-          uint8_t* stg = stage0 + slot * SLICE;
-          // the store that read this buffer last must be done
-          if (leader) bulk_wait_read<1>();
+          for (int l = 0; l < 4; ++l) {
+            const int j = 4 * q + l;
+            float f = __uint_as_float(v[0][j]);
+            if (FMT == LUTQ_NVFP4) f = f * ga[0] * sc[l];
+            if (ND == 2) {
+              float u = __uint_as_float(v[ND - 1][j]);
+              if (FMT == LUTQ_NVFP4) u = u * ga[1] * sc[l];
+              f = pair_silu_mul(f, u);
+            }
+            store1<DT>(stg, j * 128 + quarter * 32 + lane, f);
+          }
+        }
+        if (p.tma_store) {
+          fence_async_shared();
           asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-          const float4* gb = reinterpret_cast<const float4*>(a.b_rows + token0 + c);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float4 s4 = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (FMT == LUTQ_NVFP4) s4 = gb[q];
-            const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-            for (int l = 0; l < 4; ++l) {
-              const int j = 4 * q + l;
-              float f = __uint_as_float(v[0][j]);
-              if (FMT == LUTQ_NVFP4) f = f * ga[0] * sc[l];
-              if (ND == 2) {
-                float u = __uint_as_float(v[ND - 1][j]);
-                if (FMT == LUTQ_NVFP4) u = u * ga[1] * sc[l];
-                f = pair_silu_mul(f, u);
-              }
-              store1<DT>(stg, j * 128 + quarter * 32 + lane, f);
-            }
+          if (leader) {
+            tma_2d_s2g(&tmap_y, row0, int(token0) + c, smem_addr(stg));
+            bulk_commit();
           }
-          if (p.tma_store) {
-            fence_async_shared();
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-            if (leader) {
-              tma_2d_s2g(&tmap_y, row0, int(token0) + c, smem_addr(stg));
-              bulk_commit();
-            }
-          } else {
-            // rows that no 16-byte copy can write: each warp its own lanes
-            __syncwarp();
-            if (row < a.N)
-              for (int j = 0; j < 32 && c + j < valid; ++j) {
-                const int64_t at = (token0 + c + j) * a.N + row;
-                if (ES == 4)
-                  static_cast<uint32_t*>(a.y)[at] =
-                      reinterpret_cast<const uint32_t*>(stg)[j * 128 + quarter * 32 + lane];
-                else
-                  static_cast<uint16_t*>(a.y)[at] =
-                      reinterpret_cast<const uint16_t*>(stg)[j * 128 + quarter * 32 + lane];
-              }
-          }
-          slot ^= 1;
-        }
-        if (--left == 0) {
-          tc_fence_before();
+        } else {
+          // rows that no 16-byte copy can write: each warp its own lanes
           __syncwarp();
-          if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), 0));
+          if (row < a.N)
+            for (int j = 0; j < 32 && c + j < valid; ++j) {
+              const int64_t at = (token0 + c + j) * a.N + row;
+              if (ES == 4)
+                static_cast<uint32_t*>(a.y)[at] =
+                    reinterpret_cast<const uint32_t*>(stg)[j * 128 + quarter * 32 + lane];
+              else
+                static_cast<uint16_t*>(a.y)[at] =
+                    reinterpret_cast<const uint16_t*>(stg)[j * 128 + quarter * 32 + lane];
+            }
         }
+        slot ^= 1;
+      };
+      auto load = [&](int i, uint32_t (&v)[ND][32]) {
+        if (column(i) < valid) {
+#pragma unroll
+          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + column(i), v[w]);
+        }
+      };
+      // two slices in registers; the shared columns are among the first two of
+      // each group, so the next tile's MMAs wait for no more than these loads
+      static_assert(Cfg::SHARED_COLS <= 128 && OWN >= 2, "");
+      uint32_t va[ND][32], vb[ND][32];
+      load(0, va);
+      load(1, vb);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), 0));
+#pragma unroll
+      for (int i = 0; i < OWN; i += 2) {
+        if (i > 0) {
+          load(i, va);
+          load(i + 1, vb);
+          tmem_wait_ld();
+        }
+        if (column(i) < valid) finish(i, va);
+        if (column(i + 1) < valid) finish(i + 1, vb);
       }
     }
     if (leader) bulk_wait<0>();
