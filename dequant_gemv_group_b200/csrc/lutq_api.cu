@@ -44,9 +44,10 @@ cudaError_t launch_rht(const void* in, int64_t rows, int64_t K, const int8_t* si
                        bool activations, void* out, int num_sms, cudaStream_t stream);
 cudaError_t launch_fit_histogram(const void* W, int64_t N, int64_t K, uint64_t* hist,
                                  int32_t* dev_status, int num_sms, cudaStream_t stream);
-cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t K,
-                               int fmt, const int32_t* gather, const int32_t* count, void* packed,
-                               int32_t* dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t items,
+                               int64_t rows, int64_t K, int fmt, const int32_t* from,
+                               const int32_t* to, int copies, void* packed, int32_t* dev_status,
+                               int num_sms, cudaStream_t stream);
 cudaError_t launch_mx_dequantize(const void* packed, int64_t batch, int64_t rows, int64_t K,
                                  int fmt, void* out, int dtype, int num_sms, cudaStream_t stream);
 cudaError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
@@ -559,8 +560,8 @@ lutq_status lutq_mx_quantize(const void* W, int dtype, int64_t batch, int64_t N,
   if (!aligned16(W) || !aligned16(packed)) return LUTQ_ERR_ALIGN;
   int sms = 0;
   if ((st = current_sms(&sms)) != LUTQ_OK) return st;
-  return from_cuda(lutq::launch_mx_quantize(W, dtype, batch, N, K, format, nullptr, nullptr,
-                                            packed, dev_status, sms,
+  return from_cuda(lutq::launch_mx_quantize(W, dtype, batch, N, N, K, format, nullptr, nullptr,
+                                            1, packed, dev_status, sms,
                                             static_cast<cudaStream_t>(stream)));
 }
 

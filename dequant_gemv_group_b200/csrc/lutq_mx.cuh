@@ -57,12 +57,23 @@ __device__ __forceinline__ uint32_t e2m1_x8(const float (&v)[8]) {
   return r;
 }
 
-// The value of E2M1 code c (0..15).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  // codes 2..7: exponent (m >> 1) - 1, one mantissa bit; code 1 is 0.5
-  const float a = m < 2u ? 0.5f * float(m) : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return (c & 8u) ? -a : a;
+// The values of eight codes, element 0 in the lowest nibble.
+__device__ __forceinline__ void e2m1_values8(uint32_t q, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
 }
 
 // One float >= 0 to E4M3 (round to nearest even, saturating at 448).
@@ -133,6 +144,79 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]
       }
     }
   }
+}
+
+// The same eight values as loaded: 16-bit pairs in four words, or fp32 in eight.
+template <int DT>
+struct Raw8 {
+  uint32_t w[DT == LUTQ_FP32 ? 8 : 4];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* base, int64_t i) {
+  Raw8<DT> r;
+  if constexpr (DT == LUTQ_FP32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
+    const uint4 a = p[0], b = p[1];
+    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < (DT == LUTQ_FP32 ? 8 : 4); ++j) {
+    if constexpr (DT == LUTQ_FP32) {
+      v[j] = __uint_as_float(r.w[j]);
+    } else if constexpr (DT == LUTQ_BF16) {
+      v[2 * j] = bf16_lo_to_f32(r.w[j]);
+      v[2 * j + 1] = bf16_hi_to_f32(r.w[j]);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[j]));
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+  }
+}
+// The largest magnitude as the type's own bits (16-bit types: two at a time,
+// by unsigned halfword maxima; infinities and NaN come out largest).
+template <int DT>
+__device__ __forceinline__ uint32_t max_raw8(const Raw8<DT>& r) {
+  if constexpr (DT == LUTQ_FP32) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, r.w[j] & 0x7fffffffu);
+    return m;
+  } else {
+    uint32_t m = __vmaxu2(__vmaxu2(r.w[0] & 0x7fff7fffu, r.w[1] & 0x7fff7fffu),
+                          __vmaxu2(r.w[2] & 0x7fff7fffu, r.w[3] & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+  }
+}
+// Those bits as fp32 bits (an infinity or NaN stays one), and their limit.
+template <int DT>
+__device__ __forceinline__ uint32_t max_bits_f32(uint32_t m) {
+  if constexpr (DT == LUTQ_FP32) return m;
+  if constexpr (DT == LUTQ_BF16) return m << 16;
+  return __float_as_uint(__half2float(__ushort_as_half(uint16_t(m))));
+}
+template <int DT>
+__host__ __device__ constexpr uint32_t raw_inf() {
+  return DT == LUTQ_FP32 ? 0x7f800000u : DT == LUTQ_BF16 ? 0x7f80u : 0x7c00u;
+}
+
+// x / s for the rounding to a level, s a scale of 4 significant bits times a
+// power of two.  For 16-bit x the quotient is either exactly halfway between
+// two levels or at least 2^-15 (relative) away from that: 11 + 4 + 3 bits.  So
+// x * (1 / s), off by 2^-23, rounded to 17 bits is halfway exactly when x / s
+// is, and otherwise on the same side; a division costs five times as much.
+template <int DT>
+__device__ __forceinline__ float level_quotient(float x, float s, float s_inv) {
+  if constexpr (DT == LUTQ_FP32) return __fdiv_rn(x, s);
+  return __uint_as_float((__float_as_uint(x * s_inv) + 0x40u) & 0xffffff80u);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }

@@ -23,67 +23,56 @@ constexpr int kPlanThreads = 512;
 struct MoePlan {
   int32_t* counts;  // [E] rows of an expert
   int32_t* bases;   // [E] its first row
-  int32_t* total;   // rows in use, padding included
   int32_t* slot;    // [pairs] a pair's row, or -1 (id outside 0..E-1)
-  int32_t* source;  // [cap] a row's token, or -1 (padding)
-  int32_t* self;    // [cap] the row itself, or -1
 };
 
 // Block e: counts every expert's pairs (shared-memory histogram), adds up the
-// rows before its own, then hands out its rows: each thread owns a run of
-// pairs, so a scan over the threads' counts keeps the pairs' order.
+// rows before its own, then hands out its rows: each warp owns a run of pairs
+// and reads it 32 at a time, so a scan over the warps' counts and the ballots
+// keeps the pairs' order.
 __global__ void __launch_bounds__(kPlanThreads)
-    moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int top_k, int E, MoePlan p) {
+    moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int E, MoePlan p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int W = kPlanThreads / 32;
   extern __shared__ int32_t hist[];
-  __shared__ int32_t warp_sum[kPlanThreads / 32];
+  __shared__ int32_t warp_count[W];
   __shared__ int32_t base_s;
   const int e = blockIdx.x, th = threadIdx.x, lane = th & 31, warp = th >> 5;
   for (int i = th; i < E; i += kPlanThreads) hist[i] = 0;
   if (th == 0) base_s = 0;
   __syncthreads();
-  for (int i = th; i < pairs; i += kPlanThreads) {
+  const int run = (pairs + kPlanThreads - 1) / kPlanThreads * 32;  // a multiple of 32
+  const int i0 = min(pairs, warp * run), i1 = min(pairs, i0 + run);
+  int mine = 0;
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 32) {
     const int id = ids[i];
+    mine += id == e;
     if (uint32_t(id) < uint32_t(E)) atomicAdd(&hist[id], 1);
     else if (e == 0) p.slot[i] = -1;
   }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) warp_count[warp] = mine;
   __syncthreads();
   int before = 0;
   for (int i = th; i < e; i += kPlanThreads) before += (hist[i] + 127) / 128 * 128;
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) atomicAdd(&base_s, before);
   __syncthreads();
-  const int base = base_s, count = hist[e], padded = (count + 127) / 128 * 128;
+  int row = base_s;
   if (th == 0) {
-    p.counts[e] = count;
-    p.bases[e] = base;
-    if (e == E - 1) *p.total = base + padded;
+    p.counts[e] = hist[e];
+    p.bases[e] = row;
   }
-  if (count == 0) return;
-  const int per = (pairs + kPlanThreads - 1) / kPlanThreads;
-  const int i0 = th * per, i1 = min(pairs, i0 + per);
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += ids[i] == e;
-  int scan = mine;
-  for (int x = 1; x < 32; x *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, scan, x);
-    if (lane >= x) scan += v;
-  }
-  if (lane == 31) warp_sum[warp] = scan;
-  __syncthreads();
-  int row = base + scan - mine;
-  for (int w = 0; w < warp; ++w) row += warp_sum[w];
-  for (int i = i0; i < i1; ++i)
-    if (ids[i] == e) {
-      p.slot[i] = row;
-      p.source[row] = i / top_k;
-      p.self[row] = row;
-      ++row;
-    }
-  for (int i = count + th; i < padded; i += kPlanThreads) {
-    p.source[base + i] = -1;
-    p.self[base + i] = -1;
+  if (mine == 0) return;
+  for (int w = 0; w < warp; ++w) row += warp_count[w];
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    const bool here = i + lane < i1 && ids[i + lane] == e;
+    const uint32_t who = __ballot_sync(0xffffffffu, here);
+    if (here) p.slot[i + lane] = row + __popc(who & ((1u << lane) - 1u));
+    row += __popc(who);
   }
 }
 
@@ -116,9 +105,10 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ host side
 
-cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t K,
-                               int fmt, const int32_t* gather, const int32_t* count, void* packed,
-                               int32_t* dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t items,
+                               int64_t rows, int64_t K, int fmt, const int32_t* from,
+                               const int32_t* to, int copies, void* packed, int32_t* dev_status,
+                               int num_sms, cudaStream_t stream);
 
 // Rows of all experts at most: every pair, and each expert in use padded to 128.
 static int64_t moe_rows(int64_t T, int top_k, int E) {
@@ -127,7 +117,7 @@ static int64_t moe_rows(int64_t T, int top_k, int E) {
 }
 
 struct MoeSpace {
-  int64_t counts, bases, total, slot, source, self, xq, h, hq, out, bytes;
+  int64_t counts, bases, slot, xq, h, hq, out, bytes;
 };
 static MoeSpace moe_space(int64_t T, int top_k, int E, int64_t D, int64_t F, int fmt) {
   const int64_t cap = moe_rows(T, top_k, E);
@@ -140,10 +130,7 @@ static MoeSpace moe_space(int64_t T, int top_k, int E, int64_t D, int64_t F, int
   };
   s.counts = take(4 * int64_t(E));
   s.bases = take(4 * int64_t(E));
-  s.total = take(4);
   s.slot = take(4 * T * top_k);
-  s.source = take(4 * cap);
-  s.self = take(4 * cap);
   s.xq = take(mx_bytes(cap, D, fmt));
   s.h = take(2 * cap * F);
   s.hq = take(mx_bytes(cap, F, fmt));
@@ -163,8 +150,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const MoeSpace s = moe_space(T, top_k, E, D, F, fmt);
   auto ints = [&](int64_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-  const MoePlan p = {ints(s.counts), ints(s.bases),  ints(s.total),
-                     ints(s.slot),   ints(s.source), ints(s.self)};
+  const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
   // an expert has at most T rows, T top_k / E on average
@@ -183,9 +169,9 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   };
 
   if ((err = launch_pdl(moe_plan_kernel, dim3(unsigned(E)), dim3(kPlanThreads), size_t(E) * 4,
-                        stream, ids, pairs, top_k, E, p)) != cudaSuccess)
+                        stream, ids, pairs, E, p)) != cudaSuccess)
     return err;
-  if ((err = launch_mx_quantize(x, dtype, 1, cap, D, fmt, p.source, p.total, ws + s.xq,
+  if ((err = launch_mx_quantize(x, dtype, 1, T, cap, D, fmt, nullptr, p.slot, top_k, ws + s.xq,
                                 dev_status, num_sms, stream)) != cudaSuccess)
     return err;
 
@@ -220,8 +206,8 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     err = launch_mx_gemm(maps, a, fmt, kMxGateUp, nt, split, clusters, false, stream);
   }
   if (err != cudaSuccess) return err;
-  if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, cap, F, fmt, p.self, p.total, ws + s.hq,
-                                dev_status, num_sms, stream)) != cudaSuccess)
+  if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, pairs, cap, F, fmt, p.slot, p.slot, 1,
+                                ws + s.hq, dev_status, num_sms, stream)) != cudaSuccess)
     return err;
 
   a.a_scales[0] = a.a_scales[1] = bytes(down, mx_scale_off(D, F));

@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
           } else {
             sc[h] = e4m3_byte(__uint_as_float(m) * g_inv / 6.0f);
             s4 = e4m3_value(sc[h]) * g;
+            mul = __frcp_rn(s4);
           }
           if (!nan) {
 #pragma unroll
@@ -475,7 +476,9 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
               for (int l = 0; l < 8; ++l) {
                 const float z = v[h * 16 + 8 * w + l];
                 u[l] = FMT == LUTQ_MXFP4 ? z * mul
-                                         : (s4 > 0.f ? __fdiv_rn(z, s4) : copysignf(0.f, z));
+                       : !(s4 > 0.f)     ? copysignf(0.f, z)
+                       : a.x_dtype == LUTQ_FP32 ? level_quotient<LUTQ_FP32>(z, s4, 0.f)
+                                                : level_quotient<LUTQ_BF16>(z, s4, mul);
               }
               codes[h * 2 + w] = e2m1_x8(u);
             }

@@ -1,15 +1,16 @@
 // Microscaled 4-bit floating point: quantize, dequantize, pack (layout in
 // lutq_mx.cuh).
 //
-// quantize is bound by memory: it reads 2 bytes a value (bf16) and writes
-// 0.53 (mxfp4) or 0.56 (nvfp4).  A warp takes 256 values of one row at a time,
-// 8 a lane, so that loads are 512 contiguous bytes, code stores 128 bytes, and
-// a block's largest magnitude takes two (32 values) or one (16) shuffles.  A
-// thread block takes rows p, p+1 and their partners 32, 64 and 96 below, whose
-// scales are neighbours in the layout: its eight warps write whole 32-byte
-// sectors of scales.  nvfp4 reads a row twice, first for the row's scale; the
-// second read comes from L2 (8 rows a block, at most some tens of megabytes in
-// flight).
+// Both directions are bound by memory: quantize reads 2 bytes a value (bf16)
+// and writes 0.53 (mxfp4) or 0.56 (nvfp4), dequantize the reverse.  A warp
+// takes 256 values of a row at a time, 8 a lane, so that value accesses are
+// 512 contiguous bytes, code accesses 128, and a block's largest magnitude
+// takes two (32 values) or one (16) shuffles; several such loads are issued
+// before the first is used.  Many rows: a warp takes a row; the eight warps of
+// a block take rows p, p+1 and their partners 32, 64 and 96 below, whose
+// scales are neighbours in the layout, and so write whole 32-byte sectors of
+// scales.  Few rows: the block's warps share a row.  nvfp4 reads a row twice,
+// first for the row's scale; the second read comes from L2.
 #include <algorithm>
 
 #include "lutq_mx.cuh"
@@ -17,6 +18,7 @@
 namespace lutq {
 
 constexpr int kMxWarps = 8;
+constexpr int kMxBatch = 4;  // loads of a lane in flight
 
 // The row that warp w of block b of a row tile handles.
 __device__ __forceinline__ int64_t mx_row_of(int b, int w) {
@@ -29,19 +31,20 @@ __device__ __forceinline__ int mx_scale_slot(int64_t r) {
 
 // Quantize one lane's 8 values; lanes 4i..4i+3 hold a block of 32 (mxfp4),
 // 2i..2i+1 one of 16 (nvfp4).  Returns the codes; *scale the block's byte.
-template <int FMT>
-__device__ __forceinline__ uint32_t mx_quantize8(float (&v)[8], float g, float g_inv,
+template <int FMT, int DT>
+__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<DT>& raw, float g, float g_inv,
                                                  uint32_t* scale, bool* bad) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  uint32_t m = max_raw8<DT>(raw);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   if (FMT == LUTQ_MXFP4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (m >= kInfBits) {  // a NaN or infinity: the block's scale is NaN
+  if (m >= raw_inf<DT>()) {  // a NaN or infinity: the block's scale is NaN
     *bad = true;
     *scale = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
     return 0u;
   }
+  m = max_bits_f32<DT>(m);
+  float v[8];
+  widen8<DT>(raw, v);
   if constexpr (FMT == LUTQ_MXFP4) {
     *scale = e8m0_byte(m);
     const float inv = e8m0_inverse(*scale);
@@ -50,78 +53,127 @@ __device__ __forceinline__ uint32_t mx_quantize8(float (&v)[8], float g, float g
   } else {
     *scale = e4m3_byte(__uint_as_float(m) * g_inv / 6.0f);
     const float s = e4m3_value(*scale) * g;
+    if (s > 0.f) {
+      const float s_inv = __frcp_rn(s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s > 0.f ? __fdiv_rn(v[j], s) : copysignf(0.f, v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = level_quotient<DT>(v[j], s, s_inv);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = copysignf(0.f, v[j]);
+    }
   }
   return e2m1_x8(v);
 }
 
-// gather == nullptr: destination row r is source row r.  Otherwise row r is
-// quantized from source row gather[r]; a negative entry leaves the row's
-// bytes as they are (and `count`, if given, bounds the rows in use).
-template <int FMT, int DT>
+// WPR warps share a row.  Without `from`, row r is source and destination row
+// r, and the zero padding below the last row of a tile is written too.  With
+// it, item r reads source row from[r] (or r, if from is null and to is not)
+// and goes to the `copies` rows to[copies * r ...]; a negative entry is
+// skipped, and nothing else is written.
+template <int FMT, int DT, int WPR>
 __global__ void __launch_bounds__(kMxWarps * 32)
-    mx_quantize_kernel(const void* __restrict__ x, int64_t rows, int64_t K,
-                       const int32_t* __restrict__ gather, const int32_t* __restrict__ count,
-                       uint8_t* __restrict__ packed, int64_t x_stride, int64_t packed_stride,
-                       int32_t* dev_status) {
+    mx_quantize_kernel(const void* __restrict__ x, int64_t items, int64_t rows, int64_t K,
+                       const int32_t* __restrict__ from, const int32_t* __restrict__ to,
+                       int copies, uint8_t* __restrict__ packed, int64_t x_stride,
+                       int64_t packed_stride, int32_t* dev_status) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t row_max[kMxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = mx_row_of(blockIdx.x, warp);
-  if (count != nullptr && int64_t(blockIdx.x >> 4) * kMxRowTile >= *count) return;
-  const int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
-  const uint8_t* xm = static_cast<const uint8_t*>(x) + int64_t(blockIdx.z) * x_stride * esize;
+  const bool listed = to != nullptr;
+  const int64_t item = WPR == kMxWarps ? blockIdx.x
+                       : listed        ? int64_t(blockIdx.x) * kMxWarps + warp
+                                       : mx_row_of(blockIdx.x, warp);
+  constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
+  int64_t src = item < items ? item : -1;
+  if (listed) {
+    if (item >= items) return;
+    if (from != nullptr) src = from[item];
+    if (src < 0) return;  // (the whole block, where its warps share the row)
+  }
+  const uint8_t* xr =
+      static_cast<const uint8_t*>(x) + (int64_t(blockIdx.z) * x_stride + src * K) * esize;
   uint8_t* pm = packed + int64_t(blockIdx.z) * packed_stride;
   const int64_t chunks = mx_ceil(K, kMxChunk);
-  // the zero padding below the last row of a tile is written too, except
-  // among gathered rows, where nothing reads it
-  int64_t src = r < rows ? r : -1;
-  if (gather != nullptr) {
-    src = r < rows ? gather[r] : -1;
-    if (src < 0) return;
-  }
-  const uint8_t* xr = xm + src * K * esize;
+  // this warp's chunks: first, first + step, ...
+  const int64_t first = WPR == kMxWarps ? blockIdx.y * kMxWarps + warp : blockIdx.y;
+  const int64_t step = int64_t(gridDim.y) * WPR;
+
   float g = 1.f, g_inv = 1.f;
   if (FMT == LUTQ_NVFP4 && src >= 0) {
+    // the row's largest finite magnitude (gridDim.y is 1)
     uint32_t m = 0;
-    for (int64_t k = lane * 8; k < K; k += 256) {
-      float v[8];
-      load8<DT>(xr, k, v);
+    for (int64_t c = first; c < chunks; c += step * kMxBatch) {
+      Raw8<DT> raw[kMxBatch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = abs_bits(v[j]);
-        m = max(m, b < kInfBits ? b : 0u);
+      for (int u = 0; u < kMxBatch; ++u) {
+        const int64_t k = (c + u * step) * kMxChunk + lane * 8;
+        raw[u] = Raw8<DT>{};
+        if (k < K) raw[u] = load_raw8<DT>(xr, k);
+      }
+#pragma unroll
+      for (int u = 0; u < kMxBatch; ++u) {
+        const uint32_t b = max_raw8<DT>(raw[u]);
+        if (b < raw_inf<DT>()) {
+          m = max(m, max_bits_f32<DT>(b));
+        } else {  // leave out what is not finite
+          float v[8];
+          widen8<DT>(raw[u], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
+        }
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
+    if (WPR == kMxWarps) {
+      if (lane == 0) row_max[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kMxWarps; ++w) m = max(m, row_max[w]);
+    }
     g = nv_row_scale(m);
     g_inv = nv_row_scale_inverse(g);
-    if (lane == 0 && blockIdx.y == 0)
-      reinterpret_cast<float*>(pm + mx_row_off(rows, K, FMT))[r] = g;
   }
   bool bad = false;
-  uint8_t* codes = pm + r * (K / 2);
-  uint8_t* sc = pm + mx_scale_off(rows, K) +
-                (r / kMxRowTile) * chunks * mx_chunk_bytes(FMT) + mx_scale_slot(r);
-#pragma unroll 4
-  for (int64_t c = blockIdx.y; c < chunks; c += gridDim.y) {
-    const int64_t k = c * kMxChunk + lane * 8;
-    uint32_t q = 0, s = 0;
-    if (src >= 0) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (k < K) load8<DT>(xr, k, v);
-      q = mx_quantize8<FMT>(v, g, g_inv, &s, &bad);
-      if (k < K) *reinterpret_cast<uint32_t*>(codes + k / 2) = q;
-      if (k >= K) s = 0;
+  const int64_t scale_off = mx_scale_off(rows, K), row_off = mx_row_off(rows, K, FMT);
+  for (int64_t c = first; c < chunks; c += step * kMxBatch) {
+    Raw8<DT> raw[kMxBatch];
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      const int64_t k = (c + u * step) * kMxChunk + lane * 8;
+      raw[u] = Raw8<DT>{};
+      if (src >= 0 && k < K) raw[u] = load_raw8<DT>(xr, k);
     }
-    // four scales of a block are one 32-bit word
-    constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;  // lanes per block
-    uint32_t w = s << (8 * ((lane / L) & 3));
-    w |= __shfl_xor_sync(0xffffffffu, w, L);
-    w |= __shfl_xor_sync(0xffffffffu, w, 2 * L);
-    if ((lane & (4 * L - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(sc + c * mx_chunk_bytes(FMT) + (lane / (4 * L)) * 512) = w;
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      const int64_t cu = c + u * step, k = cu * kMxChunk + lane * 8;
+      if (cu >= chunks) break;
+      uint32_t q = 0, s = 0;
+      if (src >= 0) {
+        q = mx_quantize8<FMT, DT>(raw[u], g, g_inv, &s, &bad);
+        if (k >= K) s = 0;
+      }
+      // four scales of a block are one 32-bit word
+      constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;  // lanes per block
+      uint32_t w = s << (8 * ((lane / L) & 3));
+      w |= __shfl_xor_sync(0xffffffffu, w, L);
+      w |= __shfl_xor_sync(0xffffffffu, w, 2 * L);
+      for (int i = 0; i < copies; ++i) {
+        const int64_t r = listed ? to[item * copies + i] : item;
+        if (r < 0) continue;
+        if (src >= 0 && k < K) *reinterpret_cast<uint32_t*>(pm + r * (K / 2) + k / 2) = q;
+        if ((lane & (4 * L - 1)) == 0)
+          *reinterpret_cast<uint32_t*>(pm + scale_off +
+                                       ((r / kMxRowTile) * chunks + cu) * mx_chunk_bytes(FMT) +
+                                       mx_scale_slot(r) + (lane / (4 * L)) * 512) = w;
+      }
+    }
+  }
+  if (FMT == LUTQ_NVFP4 && src >= 0 && (WPR == 1 || warp == 0) && lane == 0) {
+    for (int i = 0; i < copies; ++i) {
+      const int64_t r = listed ? to[item * copies + i] : item;
+      if (r >= 0) reinterpret_cast<float*>(pm + row_off)[r] = g;
+    }
   }
   if (bad) report(dev_status, LUTQ_ERR_NONFINITE);
 }
@@ -138,41 +190,54 @@ __global__ void __launch_bounds__(kMxWarps * 32)
   if (r >= rows) return;
   const uint8_t* pm = packed + int64_t(blockIdx.z) * packed_stride;
   const int64_t chunks = mx_ceil(K, kMxChunk);
-  const uint8_t* codes = pm + r * (K / 2);
+  constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;
+  const uint8_t* codes = pm + r * (K / 2) + lane * 4;
   const uint8_t* sc = pm + mx_scale_off(rows, K) +
-                      (r / kMxRowTile) * chunks * mx_chunk_bytes(FMT) + mx_scale_slot(r);
+                      (r / kMxRowTile) * chunks * mx_chunk_bytes(FMT) + mx_scale_slot(r) +
+                      (lane / (4 * L)) * 512 + ((lane / L) & 3);
   float g = 1.f;
   if (FMT == LUTQ_NVFP4) g = reinterpret_cast<const float*>(pm + mx_row_off(rows, K, FMT))[r];
   const int64_t base = (int64_t(blockIdx.z) * rows + r) * K;
-  constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;
-#pragma unroll 4
-  for (int64_t c = blockIdx.y; c < chunks; c += gridDim.y) {
-    const int64_t k = c * kMxChunk + lane * 8;
-    if (k >= K) continue;
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + k / 2);
-    const uint32_t b = sc[c * mx_chunk_bytes(FMT) + (lane / (4 * L)) * 512 + ((lane / L) & 3)];
-    const float s = FMT == LUTQ_MXFP4 ? e8m0_value(b) : e4m3_value(b);
-    float v[8];
+  constexpr int U = 2 * kMxBatch;
+  for (int64_t c = blockIdx.y; c < chunks; c += int64_t(gridDim.y) * U) {
+    uint32_t q[U], b[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e2m1_value((q >> (4 * j)) & 15u) * s * g;
-    if constexpr (DT == LUTQ_FP32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + base + k);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (DT == LUTQ_BF16) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int64_t cu = c + u * int64_t(gridDim.y);
+      q[u] = b[u] = 0;
+      if (cu * kMxChunk + lane * 8 < K) {
+        q[u] = *reinterpret_cast<const uint32_t*>(codes + cu * (kMxChunk / 2));
+        b[u] = sc[cu * mx_chunk_bytes(FMT)];
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + base + k) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (c + u * int64_t(gridDim.y)) * kMxChunk + lane * 8;
+      if (k >= K) break;
+      const float s = FMT == LUTQ_MXFP4 ? e8m0_value(b[u]) : e4m3_value(b[u]);
+      float v[8];
+      e2m1_values8(q[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
+      if constexpr (DT == LUTQ_FP32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + base + k);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (DT == LUTQ_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + base + k) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
 }
@@ -223,24 +288,47 @@ static unsigned k_split(int64_t rows, int64_t K, int64_t batch, int num_sms) {
   return unsigned(std::max<int64_t>(1, std::min<int64_t>(want, mx_ceil(K, kMxChunk))));
 }
 
-cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t K,
-                               int fmt, const int32_t* gather, const int32_t* count, void* packed,
-                               int32_t* dev_status, int num_sms, cudaStream_t stream) {
-  const dim3 grid(unsigned(mx_ceil(rows, kMxRowTile) * 16),
-                  fmt == LUTQ_MXFP4 ? k_split(rows, K, batch, num_sms) : 1u, unsigned(batch));
-  const int64_t xs = rows * K, ps = mx_bytes(rows, K, fmt);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kMxWarps * 32), 0, stream, x, rows, K, gather, count,
-                      static_cast<uint8_t*>(packed), xs, ps, dev_status);
+template <int FMT, int DT>
+static cudaError_t launch_quantize_t(const void* x, int64_t batch, int64_t items, int64_t rows,
+                                     int64_t K, const int32_t* from, const int32_t* to,
+                                     int copies, void* packed, int32_t* dev_status, int num_sms,
+                                     cudaStream_t stream) {
+  // below one row for each of the warps that an eighth of the blocks hold, a
+  // block takes a row (a whole matrix too, but for the padding rows' zeros)
+  const bool shared_row = items <= int64_t(num_sms) * kMxWarps;
+  const int64_t padded = to != nullptr ? items : mx_ceil(rows, kMxRowTile) * kMxRowTile;
+  const int64_t xs = rows * K, ps = mx_bytes(rows, K, FMT);
+  uint8_t* out = static_cast<uint8_t*>(packed);
+  if (shared_row) {
+    // mxfp4 blocks along K as well, until every warp has a chunk or two
+    const int64_t chunks = mx_ceil(K, kMxChunk);
+    const unsigned gy = FMT == LUTQ_MXFP4 ? unsigned(mx_ceil(chunks, 2 * kMxWarps)) : 1u;
+    return launch_pdl(mx_quantize_kernel<FMT, DT, kMxWarps>,
+                      dim3(unsigned(padded), gy, unsigned(batch)), dim3(kMxWarps * 32), 0, stream,
+                      x, items, rows, K, from, to, copies, out, xs, ps, dev_status);
+  }
+  return launch_pdl(mx_quantize_kernel<FMT, DT, 1>,
+                    dim3(unsigned(mx_ceil(padded, kMxWarps)), 1u, unsigned(batch)),
+                    dim3(kMxWarps * 32), 0, stream, x, items, rows, K, from, to, copies, out, xs,
+                    ps, dev_status);
+}
+
+// `items` source rows into a packed buffer of `rows` rows (see the kernel).
+cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t items,
+                               int64_t rows, int64_t K, int fmt, const int32_t* from,
+                               const int32_t* to, int copies, void* packed, int32_t* dev_status,
+                               int num_sms, cudaStream_t stream) {
+  auto go = [&](auto f) {
+    return f(x, batch, items, rows, K, from, to, copies, packed, dev_status, num_sms, stream);
   };
   if (fmt == LUTQ_MXFP4) {
-    if (dtype == LUTQ_BF16) return go(mx_quantize_kernel<LUTQ_MXFP4, LUTQ_BF16>);
-    if (dtype == LUTQ_FP16) return go(mx_quantize_kernel<LUTQ_MXFP4, LUTQ_FP16>);
-    return go(mx_quantize_kernel<LUTQ_MXFP4, LUTQ_FP32>);
+    if (dtype == LUTQ_BF16) return go(launch_quantize_t<LUTQ_MXFP4, LUTQ_BF16>);
+    if (dtype == LUTQ_FP16) return go(launch_quantize_t<LUTQ_MXFP4, LUTQ_FP16>);
+    return go(launch_quantize_t<LUTQ_MXFP4, LUTQ_FP32>);
   }
-  if (dtype == LUTQ_BF16) return go(mx_quantize_kernel<LUTQ_NVFP4, LUTQ_BF16>);
-  if (dtype == LUTQ_FP16) return go(mx_quantize_kernel<LUTQ_NVFP4, LUTQ_FP16>);
-  return go(mx_quantize_kernel<LUTQ_NVFP4, LUTQ_FP32>);
+  if (dtype == LUTQ_BF16) return go(launch_quantize_t<LUTQ_NVFP4, LUTQ_BF16>);
+  if (dtype == LUTQ_FP16) return go(launch_quantize_t<LUTQ_NVFP4, LUTQ_FP16>);
+  return go(launch_quantize_t<LUTQ_NVFP4, LUTQ_FP32>);
 }
 
 cudaError_t launch_mx_dequantize(const void* packed, int64_t batch, int64_t rows, int64_t K,
