@@ -38,8 +38,8 @@ PER_FILE = {
 }
 SOURCES = ["lutq_api.cu", "lutq_quantize.cu", "lutq_pack.cu", "lutq_gemv.cu", "lutq_gemm.cu",
            "lutq_noalloc.cu", "lutq_selftest.cu", "lutq_rht.cu", "lutq_fit.cu",
-           "lutq_mx_quantize.cu", "lutq_mx_gemm.cu",
-           "lutq_mx_pair.cu", "lutq_mx_experts.cu", "lutq_route.cu"]
+           "lutq_mx_quantize.cu", "lutq_mx_gemm.cu", "lutq_mx_pair.cu", "lutq_mx_small.cu",
+           "lutq_mx_experts.cu", "lutq_route.cu"]
 HOST_SOURCES = ["lutq_codebook.cpp"]
 VARIANTS = {None: [], "nvtx": ["-DLUTQ_NVTX"], "bounds": ["-DLUTQ_BOUNDS"]}
 

@@ -208,15 +208,60 @@ __host__ __device__ constexpr uint32_t raw_inf() {
   return DT == LUTQ_FP32 ? 0x7f800000u : DT == LUTQ_BF16 ? 0x7f80u : 0x7c00u;
 }
 
-// x / s for the rounding to a level, s a scale of 4 significant bits times a
-// power of two.  For 16-bit x the quotient is either exactly halfway between
-// two levels or at least 2^-15 (relative) away from that: 11 + 4 + 3 bits.  So
-// x * (1 / s), off by 2^-23, rounded to 17 bits is halfway exactly when x / s
-// is, and otherwise on the same side; a division costs five times as much.
+// Quotients for a rounding decision, without a division.  Where x and s have
+// few bits, x / s is either exactly halfway between two neighbouring results
+// or at least 2^-15 (relative) away from that: fp16 x (11 bits), s of 4 bits,
+// halfway points of 3 for the levels; x / 6 and halfway points of 5 bits for
+// E4M3.  A product with the approximate reciprocal is off by less than 2^-22;
+// rounded to 17 bits it is halfway exactly when the quotient is, and otherwise
+// on the same side.  (A division costs five times as much.  fp32 inputs have
+// no such gap and are divided.)
+__device__ __forceinline__ float snap17(float v) {
+  return __uint_as_float((__float_as_uint(v) + 0x40u) & 0xffffff80u);
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// nvfp4: the scale byte of a block with largest magnitude m (fp32 bits).
 template <int DT>
-__device__ __forceinline__ float level_quotient(float x, float s, float s_inv) {
-  if constexpr (DT == LUTQ_FP32) return __fdiv_rn(x, s);
-  return __uint_as_float((__float_as_uint(x * s_inv) + 0x40u) & 0xffffff80u);
+__device__ __forceinline__ uint32_t nv_scale_byte(uint32_t m, float g_inv) {
+  const float t = __uint_as_float(m) * g_inv;
+  return e4m3_byte(DT == LUTQ_FP32 ? t / 6.0f : snap17(t * (1.0f / 6.0f)));
+}
+// Multipliers that take x to x / (s g): the reciprocal of s > 0 times 1 / g,
+// which only passes fp32's range for rows below 2^-100 (then in two steps).
+__device__ __forceinline__ bool nv_one_step(float g_inv) { return g_inv < 0x1p110f; }
+
+// Eight values to their codes, s the block's scale (nvfp4) or unused.
+template <int FMT, int DT>
+__device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, float g,
+                                              float g_inv) {
+  if constexpr (FMT == LUTQ_MXFP4) {
+    const float inv = e8m0_inverse(scale);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= inv;  // exact: a power of two
+  } else {
+    const float s = e4m3_value(scale);
+    if (!(s > 0.f)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = copysignf(0.f, v[j]);
+    } else if constexpr (DT == LUTQ_FP32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], s * g);
+    } else if (nv_one_step(g_inv)) {
+      const float m = rcp_approx(s) * g_inv;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = snap17(v[j] * m);
+    } else {
+      const float m = rcp_approx(s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = snap17(v[j] * g_inv * m);
+    }
+  }
+  return e2m1_x8(v);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }

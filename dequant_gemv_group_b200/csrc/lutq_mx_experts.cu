@@ -18,6 +18,7 @@
 namespace lutq {
 
 constexpr int kPlanThreads = 512;
+constexpr int64_t kSmallPairs = 8;  // pairs an expert, at most, for the kernel of few tokens
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {
@@ -76,11 +77,13 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// y[t] = sum_j weights[t, j] * out[slot[t, j]] in fp32, rounded once.
+// y[t] = sum_j weights[t, j] * out[slot[t, j]] in fp32, rounded once.  Without
+// slots, a pair's row is its own number (and counts if its id is an expert).
 template <int DT>
 __global__ void __launch_bounds__(256)
     moe_combine_kernel(const float* __restrict__ out, const int32_t* __restrict__ slot,
-                       const float* __restrict__ weights, int top_k, int64_t D, void* y) {
+                       const int32_t* __restrict__ ids, int E, const float* __restrict__ weights,
+                       int top_k, int64_t D, void* y) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t t = blockIdx.x;
@@ -88,10 +91,11 @@ __global__ void __launch_bounds__(256)
   if (d >= D) return;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < top_k; ++j) {
-    const int r = slot[t * top_k + j];
+    const int64_t p = t * top_k + j;
+    const int64_t r = slot != nullptr ? slot[p] : uint32_t(ids[p]) < uint32_t(E) ? p : -1;
     if (r < 0) continue;
-    const float w = weights[t * top_k + j];
-    const float4 v = *reinterpret_cast<const float4*>(out + int64_t(r) * D + d);
+    const float w = weights[p];
+    const float4 v = *reinterpret_cast<const float4*>(out + r * D + d);
     s.x += w * v.x;
     s.y += w * v.y;
     s.z += w * v.z;
@@ -153,6 +157,37 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
+  auto combine = [&](const int32_t* slot) {
+    auto go = [&](auto kernel) {
+      return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 1024))), dim3(256), 0,
+                        stream, reinterpret_cast<const float*>(ws + s.out), slot, ids, E, weights,
+                        top_k, D, y);
+    };
+    return dtype == LUTQ_BF16   ? go(moe_combine_kernel<LUTQ_BF16>)
+           : dtype == LUTQ_FP16 ? go(moe_combine_kernel<LUTQ_FP16>)
+                                : go(moe_combine_kernel<LUTQ_FP32>);
+  };
+  if (mx_small_fits(pairs, E) && pairs <= kSmallPairs * std::min(E, pairs)) {
+    // a handful of pairs an expert: quantized inside the products, three launches
+    MxGemmArgs a = {};
+    a.dev_status = dev_status;
+    a.experts = E;
+    a.x = x;
+    a.x_dtype = dtype;
+    a.y = ws + s.h;
+    a.N = F;
+    a.K = D;
+    cudaError_t err = launch_mx_small(a, gate, up, fmt, kMxGateUp, ids, pairs, top_k, num_sms,
+                                      stream);
+    if (err != cudaSuccess) return err;
+    a.x = ws + s.h;
+    a.x_dtype = LUTQ_BF16;
+    a.y = ws + s.out;
+    a.N = D;
+    a.K = F;
+    err = launch_mx_small(a, down, nullptr, fmt, kMxDown, ids, pairs, top_k, num_sms, stream);
+    return err != cudaSuccess ? err : combine(nullptr);
+  }
   // an expert has at most T rows, T top_k / E on average
   const int nt = mx_tile_tokens(T);
   const bool wide = mx_ceil(pairs, E) > 32 && T > 64;
@@ -194,7 +229,6 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.K = D;
   a.chunks = int(mx_ceil(D, kMxChunk));
   a.mtiles = int(mx_ceil(F, 128));
-  int split, clusters;
   if (wide) {
     err = launch_mx_pair(a, gate, up, w1, ws + s.xq, cap, fmt, kMxGateUp,
                          (used + pairs / 128) * mx_ceil(F, 256), num_sms, stream);
@@ -202,8 +236,8 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     if ((err = make_mx_map(&maps[0], gate, F, D, E, w1, 128)) != cudaSuccess) return err;
     if ((err = make_mx_map(&maps[1], up, F, D, E, w1, 128)) != cudaSuccess) return err;
     if ((err = token_maps(ws + s.xq, D)) != cudaSuccess) return err;
-    mx_split((used + pairs / nt) * a.mtiles, a.chunks, nt, true, num_sms, &split, &clusters);
-    err = launch_mx_gemm(maps, a, fmt, kMxGateUp, nt, split, clusters, false, stream);
+    err = launch_mx_gemm(maps, a, fmt, kMxGateUp, nt, (used + pairs / nt) * a.mtiles, num_sms,
+                         stream);
   }
   if (err != cudaSuccess) return err;
   if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, pairs, cap, F, fmt, p.slot, p.slot, 1,
@@ -227,17 +261,11 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     if ((err = make_mx_map(&maps[0], down, D, F, E, w2, 128)) != cudaSuccess) return err;
     maps[1] = maps[0];
     if ((err = token_maps(ws + s.hq, F)) != cudaSuccess) return err;
-    mx_split((used + pairs / nt) * a.mtiles, a.chunks, nt, false, num_sms, &split, &clusters);
-    err = launch_mx_gemm(maps, a, fmt, kMxDown, nt, split, clusters, false, stream);
+    err = launch_mx_gemm(maps, a, fmt, kMxDown, nt, (used + pairs / nt) * a.mtiles, num_sms,
+                         stream);
   }
   if (err != cudaSuccess) return err;
-  auto combine = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 1024))), dim3(256), 0, stream,
-                      reinterpret_cast<const float*>(ws + s.out), p.slot, weights, top_k, D, y);
-  };
-  return dtype == LUTQ_BF16   ? combine(moe_combine_kernel<LUTQ_BF16>)
-         : dtype == LUTQ_FP16 ? combine(moe_combine_kernel<LUTQ_FP16>)
-                              : combine(moe_combine_kernel<LUTQ_FP32>);
+  return combine(p.slot);
 }
 
 }  // namespace lutq

@@ -16,8 +16,7 @@
 // over the cluster through distributed shared memory, in rank order, so that
 // results do not depend on timing and no workspace is needed.
 //
-// Warps: 0 copies, 1 issues, 2..5 read tensor memory and write y, 6..9 (token
-// values quantized in the kernel) turn x into the second operand's codes.
+// Warps: 0 copies, 1 issues, 2..5 read tensor memory and write y.
 #include "lutq_mx_gemm.cuh"
 
 #include <algorithm>
@@ -32,7 +31,6 @@ using namespace sm100;
 constexpr uint64_t kMxWaitNs = 2000000000ull;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxMaxExperts = 1024;
-constexpr int kMxEpiWarp = 2, kMxQuantWarp = 6;
 
 template <int FMT, int NT, int MODE>
 struct MxCfg {
@@ -53,11 +51,9 @@ struct MxCfg {
 struct MxShared {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t part_full, part_empty, max_full, drain;
+  uint64_t part_full, part_empty, drain;
   uint32_t tmem;
   int abort;
-  uint32_t row_max[8][16];   // the cluster's largest magnitudes per token (nvfp4)
-  float row_scale[16];       // tokens quantized here: their row scales
 };
 
 // A tile begins at a multiple of 128 tokens, the height of a scale block
@@ -123,8 +119,8 @@ __device__ __forceinline__ void mx_drain(uint32_t bar, uint32_t parity) {
     if (global_ns() - t0 > kMxWaitNs) return;
 }
 
-template <int FMT, int NT, int MODE, bool XQ>
-__global__ void __launch_bounds__(XQ ? 320 : 192)
+template <int FMT, int NT, int MODE>
+__global__ void __launch_bounds__(192)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a2,
                    const __grid_constant__ CUtensorMap tmap_b,
@@ -147,7 +143,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(full(s), XQ ? 5 : 1);
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -156,7 +152,6 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
     }
     mbar_init(smem_addr(&sh->part_full), 4 * split);
     mbar_init(smem_addr(&sh->part_empty), 4 * split);
-    mbar_init(smem_addr(&sh->max_full), 4 * split);
     mbar_init(smem_addr(&sh->drain), 1);
     sh->abort = 0;
     mbar_fence_init();
@@ -197,8 +192,8 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
       const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
       const uint8_t* as = a.a_scales[0] + a_off;
       const uint8_t* as2 = a.a_scales[1] + a_off;
-      const uint8_t* bs = XQ ? nullptr : a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
-      const uint32_t bytes = ND * (Cfg::A_BYTES + CH) + (XQ ? 0 : width * 128 + CH);
+      const uint8_t* bs = a.b_scales + int64_t(row0 / kMxRowTile) * a.chunks * CH;
+      const uint32_t bytes = ND * (Cfg::A_BYTES + CH) + width * 128 + CH;
       for (int c = c0; c < c1; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kMxWaitNs);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -210,15 +205,13 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
           if (ND == 2) tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, c * 128, mt * 128, expert, full(s));
           bulk_g2s(sf, as + int64_t(c) * CH, CH, full(s));
           if (ND == 2) bulk_g2s(sf + CH, as2 + int64_t(c) * CH, CH, full(s));
-          if (!XQ) {
-            if (width == NT) {
-              tma_3d_g2s(sb, &tmap_b, c * 128, row0, 0, full(s));
-            } else {
-              for (int i = 0; i < width; i += 16)
-                tma_3d_g2s(sb + i * 128, &tmap_b16, c * 128, row0 + i, 0, full(s));
-            }
-            bulk_g2s(sf + ND * CH, bs + int64_t(c) * CH, CH, full(s));
+          if (width == NT) {
+            tma_3d_g2s(sb, &tmap_b, c * 128, row0, 0, full(s));
+          } else {
+            for (int i = 0; i < width; i += 16)
+              tma_3d_g2s(sb + i * 128, &tmap_b16, c * 128, row0 + i, 0, full(s));
           }
+          bulk_g2s(sf + ND * CH, bs + int64_t(c) * CH, CH, full(s));
         }
         __syncwarp();
         ++issued;
@@ -231,13 +224,8 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
     // given up: the copies in flight must land before the block may exit
     if (__any_sync(0xffffffffu, *abort)) {
       const int64_t n = issued < ST ? issued : ST;
-      for (int64_t i = issued - n; i < issued; ++i) {
-        // the quantizing warps may not arrive any more: arrive for them, so
-        // that the barrier follows the copies alone
-        if (XQ && lane < 4) mbar_arrive(full(int(i % ST)));
-        __syncwarp();
+      for (int64_t i = issued - n; i < issued; ++i)
         mx_drain(full(int(i % ST)), uint32_t(i / ST) & 1u);
-      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -252,7 +240,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
       const uint32_t d = tmem + uint32_t(b * ND * NT);
-      const int width = XQ ? NT : (valid + 15) / 16 * 16;
+      const int width = (valid + 15) / 16 * 16;
       const uint32_t idesc = idesc_e2m1(128, width, E8, 0);
       const uint32_t id2 = idesc_e2m1(0, 0, false, 2);  // the scale bytes 2 and 3
       for (int c = c0; c < c1; ++c, ++it) {
@@ -296,7 +284,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
       __syncwarp();
       mx_drain(smem_addr(&sh->drain), 0);
     }
-  } else if (warp < kMxQuantWarp) {
+  } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
     int n = 0;
@@ -321,7 +309,7 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
       }
       auto put = [&](int m, float v0, float v1) {
         if (FMT == LUTQ_NVFP4) {
-          const float gb = XQ ? sh->row_scale[m] : a.b_rows[token0 + m];
+          const float gb = a.b_rows[token0 + m];
           v0 = v0 * ga[0] * gb;
           if (ND == 2) v1 = v1 * ga[1] * gb;
         }
@@ -391,125 +379,6 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
         if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_empty), lane));
       }
     }
-  } else if (XQ) {
-    // ------------------------------------------------------------ x into codes
-    // thread: token i, block of 32 elements q of each chunk
-    const int th = threadIdx.x - kMxQuantWarp * 32, i = th >> 3, q = th & 7;
-    int s = 0;
-    uint32_t ph = 1;
-    bool ok = true, bad = false;
-    const int64_t esize = a.x_dtype == LUTQ_FP32 ? 4 : 2;
-    auto load32 = [&](int64_t k, float (&v)[32]) {
-      const bool in = i < a.M && k < a.K;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in) {
-          const void* p = static_cast<const uint8_t*>(a.x) + (int64_t(i) * a.K + k + 8 * j) * esize;
-          if (a.x_dtype == LUTQ_BF16) load8<LUTQ_BF16>(p, 0, u);
-          else if (a.x_dtype == LUTQ_FP16) load8<LUTQ_FP16>(p, 0, u);
-          else load8<LUTQ_FP32>(p, 0, u);
-        }
-#pragma unroll
-        for (int l = 0; l < 8; ++l) v[8 * j + l] = u[l];
-      }
-    };
-    float g = 1.f, g_inv = 1.f;
-    if (FMT == LUTQ_NVFP4) {
-      // the token's largest finite magnitude: this block's chunks, then the cluster's
-      uint32_t m = 0;
-      for (int c = c0; c < c1; ++c) {
-        float v[32];
-        load32(int64_t(c) * kMxChunk + q * 32, v);
-#pragma unroll
-        for (int l = 0; l < 32; ++l) {
-          const uint32_t u = abs_bits(v[l]);
-          m = max(m, u < kInfBits ? u : 0u);
-        }
-      }
-#pragma unroll
-      for (int x = 1; x < 8; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
-      if (split > 1) {
-        const uint32_t slot = smem_addr(&sh->row_max[rank][i]);
-        if (q < split) cluster_st_u32(cluster_map(slot, q), m);
-        __syncwarp();
-        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->max_full), lane));
-        ok = mbar_wait_cluster(smem_addr(&sh->max_full), 0, abort, kMxWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok)
-          for (int r = 0; r < split; ++r) m = max(m, sh->row_max[r][i]);
-      }
-      g = nv_row_scale(m);
-      g_inv = nv_row_scale_inverse(g);
-      if (q == 0) sh->row_scale[i] = g;
-    }
-    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
-      for (int c = c0; c < c1; ++c) {
-        float v[32];
-        const int64_t k = int64_t(c) * kMxChunk + q * 32;
-        load32(k, v);
-        uint32_t codes[4] = {0u, 0u, 0u, 0u}, sc[2] = {0u, 0u};
-        constexpr int H = FMT == LUTQ_MXFP4 ? 1 : 2;  // blocks per 32 elements
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int l = 0; l < 32 / H; ++l) m = max(m, abs_bits(v[h * 16 + l]));
-          float mul = 0.f, s4 = 0.f;
-          const bool nan = m >= kInfBits;
-          if (nan) {
-            bad = true;
-            sc[h] = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
-          } else if (FMT == LUTQ_MXFP4) {
-            sc[h] = e8m0_byte(m);
-            mul = e8m0_inverse(sc[h]);
-          } else {
-            sc[h] = e4m3_byte(__uint_as_float(m) * g_inv / 6.0f);
-            s4 = e4m3_value(sc[h]) * g;
-            mul = __frcp_rn(s4);
-          }
-          if (!nan) {
-#pragma unroll
-            for (int w = 0; w < 4 / H; ++w) {
-              float u[8];
-#pragma unroll
-              for (int l = 0; l < 8; ++l) {
-                const float z = v[h * 16 + 8 * w + l];
-                u[l] = FMT == LUTQ_MXFP4 ? z * mul
-                       : !(s4 > 0.f)     ? copysignf(0.f, z)
-                       : a.x_dtype == LUTQ_FP32 ? level_quotient<LUTQ_FP32>(z, s4, 0.f)
-                                                : level_quotient<LUTQ_BF16>(z, s4, mul);
-              }
-              codes[h * 2 + w] = e2m1_x8(u);
-            }
-          }
-        }
-        if (k >= a.K) sc[0] = sc[1] = 0u;
-        ok = mbar_wait(empty(s), ph, abort, kMxWaitNs);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        uint8_t* st = smem + s * Cfg::STAGE;
-        *reinterpret_cast<uint4*>(st + ND * Cfg::A_BYTES + i * 128 + ((q ^ (i & 7)) * 16)) =
-            make_uint4(codes[0], codes[1], codes[2], codes[3]);
-        uint8_t* sf = st + ND * Cfg::A_BYTES + Cfg::B_BYTES + ND * CH;
-        if (FMT == LUTQ_MXFP4) {
-          sf[(q >> 2) * 512 + i * 16 + (q & 3)] = uint8_t(sc[0]);
-        } else {
-          *reinterpret_cast<uint16_t*>(sf + (q >> 1) * 512 + i * 16 + (q & 1) * 2) =
-              uint16_t(sc[0] | (sc[1] << 8));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(s));
-        if (++s == ST) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
   }
 
   __syncwarp();
@@ -525,20 +394,21 @@ __global__ void __launch_bounds__(XQ ? 320 : 192)
 
 // ------------------------------------------------------------------ host side
 
-// A block that holds c of an SM's 512 columns of tensor memory asks for at
-// least c / 512 of its 228 KB of shared memory (1 KB of which a block always
-// takes), so that no two blocks of these kernels on one SM can want more
-// columns than it has: an allocation then never waits, and clusters cannot
-// wait for one another.
-static int mx_smem_floor(int cols) { return 228 * 1024 / 512 * cols - 1024; }
 constexpr int kMxSmemMax = 227 * 1024;
 
-template <int FMT, int NT, int MODE, bool XQ>
-static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int clusters,
+template <int FMT, int NT, int MODE>
+static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int64_t tiles, int num_sms,
                               cudaStream_t stream) {
   using Cfg = MxCfg<FMT, NT, MODE>;
-  // narrow plain tiles leave room for a second block on the SM
-  constexpr int budget = Cfg::TMEM <= 256 && Cfg::STAGE * 4 <= 104 * 1024 ? 113 * 1024 : kMxSmemMax;
+  // narrow tiles of one matrix leave room for a second block on the SM; the
+  // partial sums of a wide gate-and-up tile would leave none for stages
+  constexpr bool two = NT <= 32 && Cfg::ND == 1;
+  constexpr int budget = two ? 113 * 1024 : kMxSmemMax;
+  int split;
+  mx_split(tiles, a.chunks, int64_t(num_sms) * (two ? 2 : 1), Cfg::ND == 2 && NT > 32 ? 1 : 8,
+           &split);
+  const int clusters =
+      int(std::max<int64_t>(1, std::min<int64_t>(tiles, int64_t(num_sms) * (two ? 2 : 1) / split)));
   const int fixed = 1024 + (split > 1 ? Cfg::RECV : 0) + int(sizeof(MxShared)) +
                     (MODE != kMxPlain ? 8 * a.experts : 0);
   a.stages = std::min(kMxMaxStages, (budget - fixed) / Cfg::STAGE);
@@ -549,7 +419,7 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = mx_gemm_kernel<FMT, NT, MODE, XQ>;
+  auto kernel = mx_gemm_kernel<FMT, NT, MODE>;
   if (!granted[dev]) {
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemMax);
     if (err != cudaSuccess) return err;
@@ -557,7 +427,7 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(clusters * split));
-  cfg.blockDim = dim3(XQ ? 320 : 192);
+  cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -570,33 +440,29 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int split, int
   return cudaLaunchKernelEx(&cfg, kernel, t[0], t[1], t[2], t[3], a, split);
 }
 
+template <int FMT, int MODE>
+static cudaError_t launch_nt(const CUtensorMap* t, const MxGemmArgs& a, int nt, int64_t tiles,
+                             int num_sms, cudaStream_t stream) {
+  switch (nt) {
+    case 16: return launch_one<FMT, 16, MODE>(t, a, tiles, num_sms, stream);
+    case 32: return launch_one<FMT, 32, MODE>(t, a, tiles, num_sms, stream);
+    case 64: return launch_one<FMT, 64, MODE>(t, a, tiles, num_sms, stream);
+    default: return launch_one<FMT, 128, MODE>(t, a, tiles, num_sms, stream);
+  }
+}
+
 template <int FMT>
-static cudaError_t launch_fmt(const CUtensorMap* t, const MxGemmArgs& a, int mode, int nt,
-                              int split, int clusters, bool xq, cudaStream_t stream) {
-#define LUTQ_MX_CASE(NT, MODE, XQ) \
-  if (nt == NT && mode == MODE && xq == XQ) \
-    return launch_one<FMT, NT, MODE, XQ>(t, a, split, clusters, stream);
-  LUTQ_MX_CASE(16, kMxPlain, true)
-  LUTQ_MX_CASE(16, kMxPlain, false)
-  LUTQ_MX_CASE(32, kMxPlain, false)
-  LUTQ_MX_CASE(64, kMxPlain, false)
-  LUTQ_MX_CASE(128, kMxPlain, false)
-  LUTQ_MX_CASE(16, kMxGateUp, false)
-  LUTQ_MX_CASE(32, kMxGateUp, false)
-  LUTQ_MX_CASE(64, kMxGateUp, false)
-  LUTQ_MX_CASE(128, kMxGateUp, false)
-  LUTQ_MX_CASE(16, kMxDown, false)
-  LUTQ_MX_CASE(32, kMxDown, false)
-  LUTQ_MX_CASE(64, kMxDown, false)
-  LUTQ_MX_CASE(128, kMxDown, false)
-#undef LUTQ_MX_CASE
-  return cudaErrorInvalidValue;
+static cudaError_t launch_mode(const CUtensorMap* t, const MxGemmArgs& a, int mode, int nt,
+                               int64_t tiles, int num_sms, cudaStream_t stream) {
+  if (mode == kMxGateUp) return launch_nt<FMT, kMxGateUp>(t, a, nt, tiles, num_sms, stream);
+  if (mode == kMxDown) return launch_nt<FMT, kMxDown>(t, a, nt, tiles, num_sms, stream);
+  return launch_nt<FMT, kMxPlain>(t, a, nt, tiles, num_sms, stream);
 }
 
 cudaError_t launch_mx_gemm(const CUtensorMap* t, const MxGemmArgs& a, int fmt, int mode, int nt,
-                           int split, int clusters, bool xq, cudaStream_t stream) {
-  return fmt == LUTQ_MXFP4 ? launch_fmt<LUTQ_MXFP4>(t, a, mode, nt, split, clusters, xq, stream)
-                           : launch_fmt<LUTQ_NVFP4>(t, a, mode, nt, split, clusters, xq, stream);
+                           int64_t tiles, int num_sms, cudaStream_t stream) {
+  return fmt == LUTQ_MXFP4 ? launch_mode<LUTQ_MXFP4>(t, a, mode, nt, tiles, num_sms, stream)
+                           : launch_mode<LUTQ_NVFP4>(t, a, mode, nt, tiles, num_sms, stream);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -662,79 +528,49 @@ cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Split a tile's K over a cluster while that gives idle multiprocessors work
-// (two blocks fit a multiprocessor for narrow plain tiles).
-void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
-              int* clusters) {
-  const int64_t slots = int64_t(num_sms) * (nt <= 32 && !gate_up ? 2 : 1);
-  // (the partial sums of a wide gate-and-up tile leave no room for stages)
-  const int most = gate_up && nt > 32 ? 1 : 8;
-  int s = 1;
-  while (s < most && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
-  *split = s;
-  *clusters = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / s)));
-}
-
 constexpr int64_t kPairMinTokens = 64;
 
 int mx_tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// y[M, N] = x w^T.  x: the packed tokens, or (xq) M <= 16 rows of values.
-cudaError_t launch_mx_product(const void* x, int x_dtype, bool xq, int64_t M, const void* packed,
-                              int fmt, int64_t N, int64_t K, void* y, int y_dtype,
-                              int32_t* dev_status, int num_sms, cudaStream_t stream) {
+// y[M, N] = x w^T.  x: the packed tokens, or (values) M <= 16 rows of values.
+cudaError_t launch_mx_product(const void* x, int x_dtype, bool values, int64_t M,
+                              const void* packed, int fmt, int64_t N, int64_t K, void* y,
+                              int y_dtype, int32_t* dev_status, int num_sms,
+                              cudaStream_t stream) {
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   const uint8_t* xp = static_cast<const uint8_t*>(x);
-  if (M > kPairMinTokens) {
-    const int64_t tiles = mx_ceil(N, 256) * mx_ceil(M, 256);
-    if (tiles * 4 >= num_sms) {
-      MxGemmArgs g = {};
-      g.a_rows[0] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));
-      g.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
-      g.y = y;
-      g.y_dtype = y_dtype;
-      g.dev_status = dev_status;
-      g.N = N;
-      g.M = M;
-      g.K = K;
-      g.chunks = int(mx_ceil(K, kMxChunk));
-      return launch_mx_pair(g, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain, tiles,
-                            num_sms, stream);
-    }
-  }
-  const int nt = mx_tile_tokens(M);
-  CUtensorMap t[4];
-  std::memset(t, 0, sizeof(t));
-  cudaError_t err = make_mx_map(&t[0], w, N, K, 1, mx_bytes(N, K, fmt), 128);
-  if (err != cudaSuccess) return err;
-  t[1] = t[0];
-  if (!xq) {
-    if ((err = make_mx_map(&t[2], xp, M, K, 1, mx_bytes(M, K, fmt), nt)) != cudaSuccess) return err;
-    if ((err = make_mx_map(&t[3], xp, M, K, 1, mx_bytes(M, K, fmt), 16)) != cudaSuccess) return err;
-  }
   MxGemmArgs a = {};
-  a.a_scales[0] = a.a_scales[1] = w + mx_scale_off(N, K);
-  a.a_rows[0] = a.a_rows[1] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));
-  a.a_stride = 0;
-  if (xq) {
-    a.x = x;
-    a.x_dtype = x_dtype;
-  } else {
-    a.b_scales = xp + mx_scale_off(M, K);
-    a.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
-  }
   a.y = y;
   a.y_dtype = y_dtype;
   a.dev_status = dev_status;
   a.N = N;
   a.M = M;
   a.K = K;
+  if (values) {
+    a.x = x;
+    a.x_dtype = x_dtype;
+    return launch_mx_small(a, packed, nullptr, fmt, kMxPlain, nullptr, 0, 1, num_sms, stream);
+  }
+  a.a_scales[0] = a.a_scales[1] = w + mx_scale_off(N, K);
+  a.a_rows[0] = a.a_rows[1] = reinterpret_cast<const float*>(w + mx_row_off(N, K, fmt));
+  a.b_scales = xp + mx_scale_off(M, K);
+  a.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
   a.chunks = int(mx_ceil(K, kMxChunk));
+  const int64_t pair_tiles = mx_ceil(N, 256) * mx_ceil(M, 256);
+  if (M > kPairMinTokens && pair_tiles * 4 >= num_sms)
+    return launch_mx_pair(a, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain, pair_tiles,
+                          num_sms, stream);
+  const int nt = mx_tile_tokens(M);
   a.mtiles = int(mx_ceil(N, 128));
-  const int64_t tiles = a.mtiles * mx_ceil(M, nt);
-  int split, clusters;
-  mx_split(tiles, a.chunks, nt, false, num_sms, &split, &clusters);
-  return launch_mx_gemm(t, a, fmt, kMxPlain, nt, split, clusters, xq, stream);
+  CUtensorMap t[4];
+  std::memset(t, 0, sizeof(t));
+  cudaError_t err;
+  const int64_t xb = mx_bytes(M, K, fmt);
+  if ((err = make_mx_map(&t[0], w, N, K, 1, mx_bytes(N, K, fmt), 128)) != cudaSuccess) return err;
+  if ((err = make_mx_map(&t[2], xp, M, K, 1, xb, nt)) != cudaSuccess) return err;
+  if ((err = make_mx_map(&t[3], xp, M, K, 1, xb, 16)) != cudaSuccess) return err;
+  t[1] = t[0];
+  return launch_mx_gemm(t, a, fmt, kMxPlain, nt, a.mtiles * mx_ceil(M, nt), num_sms, stream);
 }
 
 }  // namespace lutq

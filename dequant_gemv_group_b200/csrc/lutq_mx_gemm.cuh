@@ -21,7 +21,7 @@ struct MxGemmArgs {
   int64_t a_stride;            // bytes from one expert's matrix to the next
   const uint8_t* b_scales;     // tokens: scale chunks and row scales
   const float* b_rows;
-  const void* x;               // tokens quantized in the kernel: the values
+  const void* x;               // tokens quantized in the kernel: their values
   int x_dtype;
   void* y;
   int y_dtype;
@@ -36,8 +36,17 @@ struct MxGemmArgs {
   int experts;
 };
 
+// The kernel for packed tokens (lutq_mx_gemm.cu).  tmaps: weights (two for
+// gate and up), tokens in boxes of nt and of 16 rows; tiles: of the launch.
 cudaError_t launch_mx_gemm(const CUtensorMap* tmaps, const MxGemmArgs& a, int fmt, int mode,
-                           int nt, int split, int clusters, bool xq, cudaStream_t stream);
+                           int nt, int64_t tiles, int num_sms, cudaStream_t stream);
+
+// The kernel for few tokens given as values (lutq_mx_small.cu): g.x, M <= 16
+// rows; or experts, with the pairs' ids.
+bool mx_small_fits(int64_t pairs, int experts);
+cudaError_t launch_mx_small(MxGemmArgs g, const void* weights, const void* weights2, int fmt,
+                            int mode, const int32_t* ids, int pairs, int top_k, int num_sms,
+                            cudaStream_t stream);
 
 // Tensor map of `batch` matrices of packed codes, `stride` bytes apart.
 cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K,
@@ -60,8 +69,19 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
 // Tokens per tile of mx_gemm_kernel: one tile for up to 128.
 int mx_tile_tokens(int64_t M);
 
-// Blocks of a launch: how many share a tile by K, and how many tiles run at once.
-void mx_split(int64_t tiles, int chunks, int nt, bool gate_up, int num_sms, int* split,
-              int* clusters);
+// Split a tile's K over a cluster while that gives idle block slots work and
+// every block two chunks.
+inline void mx_split(int64_t tiles, int chunks, int64_t slots, int most, int* split) {
+  int s = 1;
+  while (s < most && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
+  *split = s;
+}
+
+// A block that holds c of an SM's 512 columns of tensor memory asks for at
+// least c / 512 of its 228 KB of shared memory (1 KB of which a block always
+// takes), so that no two blocks of these kernels on one SM can want more
+// columns than it has: an allocation then never waits, and clusters cannot
+// wait for one another.
+constexpr int mx_smem_floor(int cols) { return 228 * 1024 / 512 * cols - 1024; }
 
 }  // namespace lutq

@@ -72,20 +72,6 @@ __device__ __forceinline__ void pair_drain(uint32_t bar, uint32_t parity) {
     if (global_ns() - t0 > kPairWaitNs) return;
 }
 
-// Whether `ok` holds in all 128 threads that meet at named barrier `id`.
-__device__ __forceinline__ bool group_all(int id, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(ok)), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
 // Tile t of a launch: token tiles vary fastest (in groups), so that a weight
 // tile is read from memory once per group and then from L2.
 // Tiles begin at multiples of 128 tokens (the height of a scale block), a last

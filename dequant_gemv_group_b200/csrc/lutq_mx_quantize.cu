@@ -45,24 +45,8 @@ __device__ __forceinline__ uint32_t mx_quantize8(const Raw8<DT>& raw, float g, f
   m = max_bits_f32<DT>(m);
   float v[8];
   widen8<DT>(raw, v);
-  if constexpr (FMT == LUTQ_MXFP4) {
-    *scale = e8m0_byte(m);
-    const float inv = e8m0_inverse(*scale);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= inv;  // exact: a power of two
-  } else {
-    *scale = e4m3_byte(__uint_as_float(m) * g_inv / 6.0f);
-    const float s = e4m3_value(*scale) * g;
-    if (s > 0.f) {
-      const float s_inv = __frcp_rn(s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = level_quotient<DT>(v[j], s, s_inv);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = copysignf(0.f, v[j]);
-    }
-  }
-  return e2m1_x8(v);
+  *scale = FMT == LUTQ_MXFP4 ? e8m0_byte(m) : nv_scale_byte<DT>(m, g_inv);
+  return mx_codes8<FMT, DT>(v, *scale, g, g_inv);
 }
 
 // WPR warps share a row.  Without `from`, row r is source and destination row

@@ -93,17 +93,26 @@ def test_quantize_types(lq, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_quantize_every_bf16(lq, fmt):
-    """All finite bf16 values, alone in their blocks and beside 1.0."""
+@pytest.mark.parametrize("beside", [1.0, 0.0])
+def test_quantize_every_bf16(lq, fmt, beside):
+    """All finite bf16 values, alone in their blocks and beside 1.0, in rows with and without it;
+    then the same rows through the product that quantizes inside the kernel."""
     bits = torch.arange(0, 65536, dtype=torch.int32).to(torch.int16)
     v = bits.view(torch.bfloat16)
     v = v[torch.isfinite(v)]
     x = torch.zeros(v.numel(), 64, dtype=torch.bfloat16)
     x[:, 0] = v
     x[:, 32] = v
-    x[:, 33] = 1.0
+    x[:, 33] = beside
+    x[:, 34] = -v                        # another value of the block on its levels
     got = lq.lutq_mx_quantize(x.cuda(), fmt)
     _same_packed(got, *O.quantize(_f64(x), fmt), fmt)
+    w = lq.lutq_mx_quantize(torch.eye(64, dtype=torch.bfloat16, device="cuda") * 2.0 ** -20, fmt)
+    xs = torch.cat([x[:16], x[5:21], x[200:216], x[-16:]]).cuda()
+    for i in range(0, 64, 16):
+        part = xs[i:i + 16].contiguous()
+        y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(part, fmt), 16, w, 64, 64, fmt)
+        assert torch.equal(lq.lutq_mx_gemv(part, w, 64, 64, fmt), y)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -165,6 +174,7 @@ SHAPES = [(1, 1, 32), (1, 128, 256), (2, 7, 96), (3, 256, 512), (8, 1000, 2048),
           (16, 64, 14336), (17, 33, 288), (31, 513, 1024), (33, 128, 4096), (64, 640, 800),
           (65, 96, 2080), (127, 257, 544), (128, 384, 4096), (129, 1024, 256), (200, 200, 3232),
           (300, 2049, 96), (513, 300, 1056),
+          (1, 20000, 512), (4, 1024, 28672), (13, 64, 8224),
           # enough tiles for the kernel of block pairs: 1 and 2 token tiles, row pitches that no
           # 16-byte copy can write, tokens beyond one pass over the weights
           (77, 9601, 288), (160, 9480, 64), (300, 8200, 96), (600, 4096, 544), (1000, 2564, 1312),
