@@ -18,7 +18,7 @@
 namespace lutq {
 
 constexpr int kPlanThreads = 512;
-constexpr int64_t kSmallPairs = 8;  // pairs an expert, at most, for the kernel of few tokens
+constexpr int64_t kSmallPairs = 16;  // pairs an expert, at most, for the kernel of few tokens
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {

@@ -345,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       ok = mbar_wait(smem_addr(&sh->acc_full), uint32_t(n) & 1u, abort, kPairWaitNs);
       // the four warps of a group share the barriers below: they go on
       // together or not at all
-      if (!group_all(1 + group, ok)) break;
+      if (!group_all(1 + group, 128, ok)) break;
       tc_fence_after();
 
       // one slice: scale, round, stage, store

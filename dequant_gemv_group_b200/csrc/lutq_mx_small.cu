@@ -78,6 +78,11 @@ __device__ __forceinline__ void small_drain(uint32_t bar, uint32_t parity) {
     if (global_ns() - t0 > kSmallWaitNs) return;
 }
 
+// Wait for the work before this launch in the stream.
+__device__ __forceinline__ void wait_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // DT: the type of the values; OT: of a plain product's output.
 template <int FMT, int MODE, int DT>
 __global__ void __launch_bounds__(kSmallThreads)
@@ -136,10 +141,27 @@ __global__ void __launch_bounds__(kSmallThreads)
   }
   if (MODE != kMxPlain)
     for (int e = threadIdx.x; e < a.experts; e += kSmallThreads) cursor[e] = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The down product follows the gate and up product of the same call, which
+  // waited for all work before it: the ids and the weights are there, and
+  // only the hidden values must be waited for.
+  if (MODE != kMxDown) wait_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
+  const int first = blockIdx.x / split, step = gridDim.x / split;
+  const int c0 = int(int64_t(a.chunks) * rank / split);
+  const int nch = int(int64_t(a.chunks) * (rank + 1) / split) - c0;
+  auto load_stage = [&](int s, int expert, int mt, int c) {
+    const int64_t off = int64_t(expert) * a.a_stride + (int64_t(mt) * a.chunks + c0 + c) * CH;
+    const uint32_t st = sbase + s * Cfg::STAGE, sf = st + ND * Cfg::A_BYTES;
+    mbar_expect_tx(full(s), Cfg::STAGE);
+    tma_3d_g2s(st, &tmap_a, (c0 + c) * 128, mt * 128, expert, full(s));
+    if (ND == 2) tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, (c0 + c) * 128, mt * 128, expert, full(s));
+    bulk_g2s(sf, a.a_scales[0] + off, CH, full(s));
+    if (ND == 2) bulk_g2s(sf + CH, a.a_scales[1] + off, CH, full(s));
+  };
   tc_fence_before();
   __syncthreads();
+  if (split > 1) cluster_arrive_all();  // this block's barriers are set up
   if (MODE != kMxPlain) {
     for (int i = threadIdx.x; i < p.pairs; i += kSmallThreads) {
       const int id = p.ids[i];
@@ -191,13 +213,8 @@ __global__ void __launch_bounds__(kSmallThreads)
     }
     __syncthreads();
   }
-  if (split > 1) cluster_sync_all();  // every block's barriers are set up
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
-  const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
-  const int first = blockIdx.x / split, step = gridDim.x / split;
-  const int c0 = int(int64_t(a.chunks) * rank / split);
-  const int nch = int(int64_t(a.chunks) * (rank + 1) / split) - c0;
   const int ntiles = (MODE == kMxPlain ? 1 : sh->entries) * a.mtiles;
   // a plain product's tokens are quantized once if they fit
   const bool resident = MODE == kMxPlain && nch <= slots;
@@ -221,22 +238,10 @@ __global__ void __launch_bounds__(kSmallThreads)
     bool ok = true;
     for (int t = first; ok && t < ntiles; t += step) {
       const Tile r = tile(t);
-      const int64_t off = int64_t(r.expert) * a.a_stride +
-                          (int64_t(r.mt) * a.chunks + c0) * CH;
-      const uint8_t* as = a.a_scales[0] + off;
-      const uint8_t* as2 = a.a_scales[1] + off;
       for (int c = 0; c < nch; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kSmallWaitNs);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const uint32_t st = sbase + s * Cfg::STAGE, sf = st + ND * Cfg::A_BYTES;
-        if (elect_one()) {
-          mbar_expect_tx(full(s), Cfg::STAGE);
-          tma_3d_g2s(st, &tmap_a, (c0 + c) * 128, r.mt * 128, r.expert, full(s));
-          if (ND == 2)
-            tma_3d_g2s(st + Cfg::A_BYTES, &tmap_a2, (c0 + c) * 128, r.mt * 128, r.expert, full(s));
-          bulk_g2s(sf, as + c * CH, CH, full(s));
-          if (ND == 2) bulk_g2s(sf + CH, as2 + c * CH, CH, full(s));
-        }
+        if (elect_one()) load_stage(s, r.expert, r.mt, c);
         __syncwarp();
         ++issued;
         if (++s == ST) {
@@ -313,234 +318,245 @@ __global__ void __launch_bounds__(kSmallThreads)
       __syncwarp();
       small_drain(smem_addr(&sh->drain), 0);
     }
-  } else if (warp < kSmallQuantWarp) {
-    // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;
-    int n = 0;
-    bool ok = true;
-    const int own = NT / split;  // columns of a split tile that this block sums
-    for (int t = first; ok && t < ntiles; t += step, ++n) {
-      const Tile r = tile(t);
-      const int acc = n & 1;
-      const int64_t row = int64_t(r.mt) * 128 + quarter * 32 + lane;
-      float ga[2] = {1.f, 1.f};
-      if (FMT == LUTQ_NVFP4 && row < a.N) {
-#pragma unroll
-        for (int w = 0; w < ND; ++w)
-          ga[w] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.a_rows[w]) +
-                                                  int64_t(r.expert) * a.a_stride + row * 4);
-      }
-      ok = mbar_wait(smem_addr(&sh->acc_full[acc]), uint32_t(n >> 1) & 1u, abort, kSmallWaitNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      auto put = [&](int m, float v0, float v1) {
-        if (FMT == LUTQ_NVFP4) {
-          const float gb = sh->row_scale[MODE == kMxPlain ? 0 : n & 1][m];
-          v0 = v0 * ga[0] * gb;
-          if (ND == 2) v1 = v1 * ga[1] * gb;
-        }
-        if (row >= a.N) return;
-        const int64_t at = int64_t(MODE == kMxPlain ? m : list[r.at + m]) * a.N + row;
-        if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, at, v0 / (1.f + __expf(-v0)) * v1);
-        else if (MODE == kMxDown) store1<LUTQ_FP32>(a.y, at, v0);
-        else if (a.y_dtype == LUTQ_FP32) store1<LUTQ_FP32>(a.y, at, v0);
-        else if (a.y_dtype == LUTQ_BF16) store1<LUTQ_BF16>(a.y, at, v0);
-        else store1<LUTQ_FP16>(a.y, at, v0);
-      };
-      const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * ND * NT);
-      uint32_t v[ND][16];
-#pragma unroll
-      for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x16(d + w * NT, v[w]);
-      tmem_wait_ld();
-      if (split == 1) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j < r.valid) put(j, __uint_as_float(v[0][j]), __uint_as_float(v[ND - 1][j]));
-        // (behind the reads of row_scale, which a later tile's quantizing
-        // warps write once this set of sums is free)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));
-      } else {
-        // send every column to the block that sums it: recv[rank][w][column][lane]
-        ok = n == 0 || mbar_wait_cluster(smem_addr(&sh->part_empty), uint32_t(n - 1) & 1u, abort,
-                                         kSmallWaitNs);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t slot = smem_addr(recv) + (rank * ND * own * 128 + quarter * 32 + lane) * 4;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j < r.valid) {
-            const uint32_t to = cluster_map(slot, uint32_t(j / own));
-#pragma unroll
-            for (int w = 0; w < ND; ++w)
-              cluster_st_f32(to + (w * own + j % own) * 512, __uint_as_float(v[w][j]));
-          }
-        __syncwarp();
-        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_full), lane));
-        ok = mbar_wait_cluster(smem_addr(&sh->part_full), uint32_t(n) & 1u, abort, kSmallWaitNs);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        for (int j = 0; j < own; ++j) {
-          const int col = int(rank) * own + j;
-          if (col >= r.valid) break;
-          float sum[2] = {0.f, 0.f};
-          for (int q = 0; q < split; ++q)
-#pragma unroll
-            for (int w = 0; w < ND; ++w)
-              sum[w] += recv[((q * ND + w) * own + j) * 128 + quarter * 32 + lane];
-          put(col, sum[0], sum[ND - 1]);
-        }
-        __syncwarp();
-        if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_empty), lane));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));
-      }
-    }
   } else {
-    // ------------------------------------------------------------ values into codes
-    const int th = threadIdx.x - kSmallQuantWarp * 32;
-    constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
-    const uint8_t* x = static_cast<const uint8_t*>(a.x);
-    bool ok = true, bad = false;
-    float g = 1.f, g_inv = 1.f;
-    int fill = 0;  // chunks quantized so far (slot and phase of the next)
-    int n = 0;
-    for (int t = first; t < ntiles; t += step, ++n) {
-      // (the warps share barriers: they go on together or not at all)
-      if ((resident && n > 0) || !group_all(1, ok)) break;
-      const Tile r = tile(t);
-      // 8 threads take a token's chunk (a block of 32 elements each); as many
-      // chunks at a time as the tokens leave threads for
-      int rows = 1;
-      while (rows < r.valid) rows *= 2;
-      // (no more than there are slots: a warp's threads wait for their slots
-      // together, so none may need another's chunk of the same round)
-      int per = 128 / (8 * rows);
-      while (per > slots) per /= 2;
-      const int q = th & 7, i = (th >> 3) & (rows - 1), lead = (th >> 3) / rows;
-      const bool live = i < r.valid;
-      int64_t src = 0;
-      if (live) {
-        src = i;
-        if (MODE == kMxGateUp) src = list[r.at + i] / p.top_k;
-        if (MODE == kMxDown) src = list[r.at + i];
-      }
-      const uint8_t* xr = x + src * a.K * esize;
-      auto load32 = [&](int c, Raw8<DT> (&raw)[4]) {
-        const int64_t k = int64_t(c) * kMxChunk + q * 32;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          raw[j] = Raw8<DT>{};
-          if (live && k < a.K) raw[j] = load_raw8<DT>(xr, k + 8 * j);
+    bool met = split == 1;  // the other blocks' barriers are known to be set up
+    // Values into codes, by warps 6..9; where that is done once, by the
+    // epilogue's warps as well, which have nothing else to do yet.
+    if (warp >= kSmallQuantWarp || resident) {
+      if (MODE == kMxDown) wait_before();  // the hidden values
+      const int th = int(threadIdx.x) - (resident ? 64 : kSmallQuantWarp * 32);
+      const int nq = resident ? 256 : 128;
+      constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
+      const uint8_t* x = static_cast<const uint8_t*>(a.x);
+      bool ok = true, bad = false;
+      float g = 1.f, g_inv = 1.f;
+      int fill = 0;  // chunks quantized so far (slot and phase of the next)
+      int n = 0;
+      for (int t = first; t < ntiles; t += step, ++n) {
+        // (the warps share barriers: they go on together or not at all)
+        if ((resident && n > 0) || !group_all(1, nq, ok)) break;
+        const Tile r = tile(t);
+        // 8 threads take a token's chunk (a block of 32 elements each); as many
+        // chunks at a time as the tokens leave threads for
+        int rows = 1;
+        while (rows < r.valid) rows *= 2;
+        // (no more than there are slots: a warp's threads wait for their slots
+        // together, so none may need another's chunk of the same round)
+        int per = nq / (8 * rows);
+        while (per > slots) per /= 2;
+        const int q = th & 7, i = (th >> 3) & (rows - 1), lead = (th >> 3) / rows;
+        const bool live = i < r.valid;
+        int64_t src = 0;
+        if (live) {
+          src = i;
+          if (MODE == kMxGateUp) src = list[r.at + i] / p.top_k;
+          if (MODE == kMxDown) src = list[r.at + i];
         }
-      };
-      if (FMT == LUTQ_NVFP4 && (MODE != kMxPlain || n == 0)) {
-        // the token's largest finite magnitude.  Plain: of this block's
-        // chunks, then the cluster's; experts: of the whole row
-        const int m0 = MODE == kMxPlain ? c0 : 0, m1 = MODE == kMxPlain ? c0 + nch : a.chunks;
-        const int pc = MODE == kMxPlain ? 0 : n & 1;
-        uint32_t m = 0;
-#pragma unroll 2
-        for (int c = lead < per ? m0 + lead : m1; c < m1; c += per) {
-          Raw8<DT> raw[4];
-          load32(c, raw);
+        const uint8_t* xr = x + src * a.K * esize;
+        auto load32 = [&](int c, Raw8<DT> (&raw)[4]) {
+          const int64_t k = int64_t(c) * kMxChunk + q * 32;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t b = max_raw8<DT>(raw[j]);
-            if (b < raw_inf<DT>()) {
-              m = max(m, max_bits_f32<DT>(b));
-            } else {
-              float v[8];
-              widen8<DT>(raw[j], v);
-#pragma unroll
-              for (int l = 0; l < 8; ++l)
-                m = max(m, abs_bits(v[l]) < kInfBits ? abs_bits(v[l]) : 0u);
-            }
+            raw[j] = Raw8<DT>{};
+            if (live && k < a.K) raw[j] = load_raw8<DT>(xr, k + 8 * j);
           }
-        }
-        if (live && lead < per) atomicMax(&sh->my_max[pc][i], m);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (MODE == kMxPlain && split > 1) {
-          if (th < NT)
-            for (int k = 0; k < split; ++k)
-              cluster_st_u32(cluster_map(smem_addr(&sh->row_max[rank][th]), k), sh->my_max[0][th]);
-          __syncwarp();
-          if (th < split) cluster_arrive(cluster_map(smem_addr(&sh->max_full), th));
-          ok = mbar_wait_cluster(smem_addr(&sh->max_full), 0, abort, kSmallWaitNs);
-          if (!(ok = group_all(1, ok))) break;
-          m = 0;
-          for (int k = 0; k < split; ++k) m = max(m, sh->row_max[k][i]);
-        } else {
-          m = sh->my_max[pc][i];
-        }
-        g = nv_row_scale(m);
-        g_inv = nv_row_scale_inverse(g);
-        if (MODE != kMxPlain && n > 1) {
-          // the epilogue must have used what tile n - 2 left here
-          ok = mbar_wait(smem_addr(&sh->acc_empty[n & 1]), (uint32_t(n >> 1) & 1u) ^ 1u, abort,
-                         kSmallWaitNs);
-          if (!(ok = group_all(1, ok))) break;
-        }
-        if (live && q == 0 && lead == 0) sh->row_scale[pc][i] = g;
-        if (MODE != kMxPlain) {
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read my_max
-          if (th < NT) sh->my_max[pc][th] = 0u;
-        }
-      }
-      Raw8<DT> raw[4];
-      if (lead < per && lead < nch) load32(c0 + lead, raw);
-      for (int c = lead < per ? lead : nch; c < nch; c += per) {
-        const int f = fill + c, slot = f % slots;
-        uint32_t sc[2] = {0u, 0u}, codes[4] = {0u, 0u, 0u, 0u};
-        constexpr int H = FMT == LUTQ_MXFP4 ? 1 : 2;  // blocks per 32 elements
-        if (live) {
+        };
+        if (FMT == LUTQ_NVFP4 && (MODE != kMxPlain || n == 0)) {
+          // the token's largest finite magnitude.  Plain: of this block's
+          // chunks, then the cluster's; experts: of the whole row
+          const int m0 = MODE == kMxPlain ? c0 : 0, m1 = MODE == kMxPlain ? c0 + nch : a.chunks;
+          const int pc = MODE == kMxPlain ? 0 : n & 1;
+          uint32_t m = 0;
+#pragma unroll 2
+          for (int c = lead < per ? m0 + lead : m1; c < m1; c += per) {
+            Raw8<DT> raw[4];
+            load32(c, raw);
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int w = 0; w < 4 / H; ++w) m = max(m, max_raw8<DT>(raw[h * 2 + w]));
-            if (m >= raw_inf<DT>()) {
-              bad = true;
-              sc[h] = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
-            } else {
-              m = max_bits_f32<DT>(m);
-              sc[h] = FMT == LUTQ_MXFP4 ? e8m0_byte(m) : nv_scale_byte<DT>(m, g_inv);
-#pragma unroll
-              for (int w = 0; w < 4 / H; ++w) {
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b = max_raw8<DT>(raw[j]);
+              if (b < raw_inf<DT>()) {
+                m = max(m, max_bits_f32<DT>(b));
+              } else {
                 float v[8];
-                widen8<DT>(raw[h * 2 + w], v);
-                codes[h * 2 + w] = mx_codes8<FMT, DT>(v, sc[h], g, g_inv);
+                widen8<DT>(raw[j], v);
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                  m = max(m, abs_bits(v[l]) < kInfBits ? abs_bits(v[l]) : 0u);
               }
             }
           }
-          if (int64_t(c0 + c) * kMxChunk + q * 32 >= a.K) sc[0] = sc[1] = 0u;
+          if (live && lead < per) atomicMax(&sh->my_max[pc][i], m);
+          asm volatile("bar.sync 1, %0;" ::"r"(nq) : "memory");
+          if (MODE == kMxPlain && split > 1) {
+            cluster_wait_all();
+            met = true;
+            if (th < NT)
+              for (int k = 0; k < split; ++k)
+                cluster_st_u32(cluster_map(smem_addr(&sh->row_max[rank][th]), k), sh->my_max[0][th]);
+            __syncwarp();
+            if (th < split) cluster_arrive(cluster_map(smem_addr(&sh->max_full), th));
+            ok = mbar_wait_cluster(smem_addr(&sh->max_full), 0, abort, kSmallWaitNs);
+            if (!(ok = group_all(1, nq, ok))) break;
+            m = 0;
+            for (int k = 0; k < split; ++k) m = max(m, sh->row_max[k][i]);
+          } else {
+            m = sh->my_max[pc][i];
+          }
+          g = nv_row_scale(m);
+          g_inv = nv_row_scale_inverse(g);
+          if (MODE != kMxPlain && n > 1) {
+            // the epilogue must have used what tile n - 2 left here
+            ok = mbar_wait(smem_addr(&sh->acc_empty[n & 1]), (uint32_t(n >> 1) & 1u) ^ 1u, abort,
+                           kSmallWaitNs);
+            if (!(ok = group_all(1, nq, ok))) break;
+          }
+          if (live && q == 0 && lead == 0) sh->row_scale[pc][i] = g;
+          if (MODE != kMxPlain) {
+            asm volatile("bar.sync 1, %0;" ::"r"(nq) : "memory");  // all have read my_max
+            if (th < NT) sh->my_max[pc][th] = 0u;
+          }
         }
-        if (c + per < nch) load32(c0 + c + per, raw);  // a round ahead
-        if (!resident) {
-          ok = mbar_wait(bempty(slot), (uint32_t(f / slots) & 1u) ^ 1u, abort, kSmallWaitNs);
-          if (!ok) break;
+        Raw8<DT> raw[4];
+        if (lead < per && lead < nch) load32(c0 + lead, raw);
+        for (int c = lead < per ? lead : nch; c < nch; c += per) {
+          const int f = fill + c, slot = f % slots;
+          uint32_t sc[2] = {0u, 0u}, codes[4] = {0u, 0u, 0u, 0u};
+          constexpr int H = FMT == LUTQ_MXFP4 ? 1 : 2;  // blocks per 32 elements
+          if (live) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              uint32_t m = 0;
+#pragma unroll
+              for (int w = 0; w < 4 / H; ++w) m = max(m, max_raw8<DT>(raw[h * 2 + w]));
+              if (m >= raw_inf<DT>()) {
+                bad = true;
+                sc[h] = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
+              } else {
+                m = max_bits_f32<DT>(m);
+                sc[h] = FMT == LUTQ_MXFP4 ? e8m0_byte(m) : nv_scale_byte<DT>(m, g_inv);
+#pragma unroll
+                for (int w = 0; w < 4 / H; ++w) {
+                  float v[8];
+                  widen8<DT>(raw[h * 2 + w], v);
+                  codes[h * 2 + w] = mx_codes8<FMT, DT>(v, sc[h], g, g_inv);
+                }
+              }
+            }
+            if (int64_t(c0 + c) * kMxChunk + q * 32 >= a.K) sc[0] = sc[1] = 0u;
+          }
+          if (c + per < nch) load32(c0 + c + per, raw);  // a round ahead
+          if (!resident) {
+            ok = mbar_wait(bempty(slot), (uint32_t(f / slots) & 1u) ^ 1u, abort, kSmallWaitNs);
+            if (!ok) break;
+          }
+          uint8_t* bp = tokens + slot * Cfg::SLOT;
+          if (live) {
+            *reinterpret_cast<uint4*>(bp + i * 128 + ((q ^ (i & 7)) * 16)) =
+                make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            uint8_t* sf = bp + Cfg::B_BYTES + i * 16;
+            if (FMT == LUTQ_MXFP4)
+              sf[(q >> 2) * 512 + (q & 3)] = uint8_t(sc[0]);
+            else
+              *reinterpret_cast<uint16_t*>(sf + (q >> 1) * 512 + (q & 1) * 2) =
+                  uint16_t(sc[0] | (sc[1] << 8));
+          }
+          fence_async_shared();
+          // 8 * rows threads have this chunk; the barrier counts 128 arrivals
+          mbar_arrive_n(bfull(slot), uint32_t(NT / rows));
         }
-        uint8_t* bp = tokens + slot * Cfg::SLOT;
-        if (live) {
-          *reinterpret_cast<uint4*>(bp + i * 128 + ((q ^ (i & 7)) * 16)) =
-              make_uint4(codes[0], codes[1], codes[2], codes[3]);
-          uint8_t* sf = bp + Cfg::B_BYTES + i * 16;
-          if (FMT == LUTQ_MXFP4)
-            sf[(q >> 2) * 512 + (q & 3)] = uint8_t(sc[0]);
-          else
-            *reinterpret_cast<uint16_t*>(sf + (q >> 1) * 512 + (q & 1) * 2) =
-                uint16_t(sc[0] | (sc[1] << 8));
-        }
-        fence_async_shared();
-        // 8 * rows threads have this chunk; the barrier counts 128 arrivals
-        mbar_arrive_n(bfull(slot), uint32_t(NT / rows));
+        fill += nch;
       }
-      fill += nch;
+      if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
     }
-    if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
+    if (!met) cluster_wait_all();
+    if (warp < kSmallQuantWarp) {
+      const int quarter = warp & 3;
+      int n = 0;
+      bool ok = true;
+      const int own = NT / split;  // columns of a split tile that this block sums
+      for (int t = first; ok && t < ntiles; t += step, ++n) {
+        const Tile r = tile(t);
+        const int acc = n & 1;
+        const int64_t row = int64_t(r.mt) * 128 + quarter * 32 + lane;
+        float ga[2] = {1.f, 1.f};
+        if (FMT == LUTQ_NVFP4 && row < a.N) {
+#pragma unroll
+          for (int w = 0; w < ND; ++w)
+            ga[w] = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.a_rows[w]) +
+                                                    int64_t(r.expert) * a.a_stride + row * 4);
+        }
+        ok = mbar_wait(smem_addr(&sh->acc_full[acc]), uint32_t(n >> 1) & 1u, abort, kSmallWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        auto put = [&](int m, float v0, float v1) {
+          if (FMT == LUTQ_NVFP4) {
+            const float gb = sh->row_scale[MODE == kMxPlain ? 0 : n & 1][m];
+            v0 = v0 * ga[0] * gb;
+            if (ND == 2) v1 = v1 * ga[1] * gb;
+          }
+          if (row >= a.N) return;
+          const int64_t at = int64_t(MODE == kMxPlain ? m : list[r.at + m]) * a.N + row;
+          if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, at, v0 / (1.f + __expf(-v0)) * v1);
+          else if (MODE == kMxDown) store1<LUTQ_FP32>(a.y, at, v0);
+          else if (a.y_dtype == LUTQ_FP32) store1<LUTQ_FP32>(a.y, at, v0);
+          else if (a.y_dtype == LUTQ_BF16) store1<LUTQ_BF16>(a.y, at, v0);
+          else store1<LUTQ_FP16>(a.y, at, v0);
+        };
+        const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * ND * NT);
+        uint32_t v[ND][16];
+#pragma unroll
+        for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x16(d + w * NT, v[w]);
+        tmem_wait_ld();
+        if (split == 1) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (j < r.valid) put(j, __uint_as_float(v[0][j]), __uint_as_float(v[ND - 1][j]));
+          // (behind the reads of row_scale, which a later tile's quantizing
+          // warps write once this set of sums is free)
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));
+        } else {
+          // send every column to the block that sums it: recv[rank][w][column][lane]
+          ok = n == 0 || mbar_wait_cluster(smem_addr(&sh->part_empty), uint32_t(n - 1) & 1u, abort,
+                                           kSmallWaitNs);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const uint32_t slot = smem_addr(recv) + (rank * ND * own * 128 + quarter * 32 + lane) * 4;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (j < r.valid) {
+              const uint32_t to = cluster_map(slot, uint32_t(j / own));
+#pragma unroll
+              for (int w = 0; w < ND; ++w)
+                cluster_st_f32(to + (w * own + j % own) * 512, __uint_as_float(v[w][j]));
+            }
+          __syncwarp();
+          if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_full), lane));
+          ok = mbar_wait_cluster(smem_addr(&sh->part_full), uint32_t(n) & 1u, abort, kSmallWaitNs);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          for (int j = 0; j < own; ++j) {
+            const int col = int(rank) * own + j;
+            if (col >= r.valid) break;
+            float sum[2] = {0.f, 0.f};
+            for (int q = 0; q < split; ++q)
+#pragma unroll
+              for (int w = 0; w < ND; ++w)
+                sum[w] += recv[((q * ND + w) * own + j) * 128 + quarter * 32 + lane];
+            put(col, sum[0], sum[ND - 1]);
+          }
+          __syncwarp();
+          if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_empty), lane));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));
+        }
+      }
+    }
   }
 
   __syncwarp();
+  if (split > 1 && warp < 2) cluster_wait_all();  // (the other warps have)
+  if (MODE == kMxDown) wait_before();  // no thread is done before the work it follows
   tc_fence_before();
   __syncthreads();
   if (split > 1) cluster_sync_all();  // no block leaves while another may write to it
