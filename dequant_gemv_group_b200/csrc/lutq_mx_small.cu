@@ -7,8 +7,9 @@
 // 128 weight rows by 16 tokens; a stage holds 256 elements of K of one tile
 // (of two matrices for gate and up).  Meanwhile four warps turn the tokens'
 // values into codes and scale bytes in shared memory, in the order of the
-// tensor core's 128-byte swizzle; they are loaded a round ahead, and in a plain product
-// stay for all of a block's tiles.  A cluster of `split` blocks shares a tile
+// tensor core's 128-byte swizzle; they are loaded a round ahead, and stay as
+// long as a block's tiles have the same tokens (a block takes neighbouring
+// tiles).  A cluster of `split` blocks shares a tile
 // by K, as in lutq_mx_gemm.cu; so neither a workspace nor another launch is
 // needed, and results do not depend on timing.
 //
@@ -61,7 +62,10 @@ struct SmallShared {
   int entries;
   uint32_t row_max[8][kSmallNT];   // the cluster's largest magnitudes per token (nvfp4)
   uint32_t my_max[2][kSmallNT];
-  float row_scale[2][kSmallNT];    // nvfp4: tokens' row scales, by parity of the tile
+  // nvfp4: the tokens' row scales of the last four fills.  A fill is written
+  // once the MMAs of the fill before have begun its last tile, so the epilogue
+  // is at most two fills behind.
+  float row_scale[4][kSmallNT];
 };
 
 struct SmallArgs {
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   if (MODE != kMxDown) wait_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
-  const int first = blockIdx.x / split, step = gridDim.x / split;
+  const int cluster = blockIdx.x / split, clusters = gridDim.x / split;
   const int c0 = int(int64_t(a.chunks) * rank / split);
   const int nch = int(int64_t(a.chunks) * (rank + 1) / split) - c0;
   auto load_stage = [&](int s, int expert, int mt, int c) {
@@ -216,8 +220,15 @@ __global__ void __launch_bounds__(kSmallThreads)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const int ntiles = (MODE == kMxPlain ? 1 : sh->entries) * a.mtiles;
-  // a plain product's tokens are quantized once if they fit
-  const bool resident = MODE == kMxPlain && nch <= slots;
+  const int t0 = int(int64_t(ntiles) * cluster / clusters);
+  const int t1 = int(int64_t(ntiles) * (cluster + 1) / clusters);
+  // Tokens in shared memory: all chunks of a tile's, kept for the tiles of the
+  // same tokens that follow (a fill), or a ring, filled for every tile.
+  const bool keep = nch <= slots;
+  auto entry_of = [&](int t) { return MODE == kMxPlain ? 0 : t / a.mtiles; };
+  auto opens = [&](int t) { return !keep || t == t0 || entry_of(t) != entry_of(t - 1); };
+  auto closes = [&](int t) { return !keep || t + 1 == t1 || entry_of(t) != entry_of(t + 1); };
+  const bool once = MODE == kMxPlain && keep;
   struct Tile {
     int expert, mt, at, valid;
   };
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     uint32_t ph = 1;
     int issued = 0;
     bool ok = true;
-    for (int t = first; ok && t < ntiles; t += step) {
+    for (int t = t0; ok && t < t1; ++t) {
       const Tile r = tile(t);
       for (int c = 0; c < nch; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kSmallWaitNs);
@@ -259,15 +270,19 @@ __global__ void __launch_bounds__(kSmallThreads)
     constexpr bool E8 = FMT == LUTQ_MXFP4;
     constexpr uint32_t idesc = idesc_e2m1(128, NT, E8, 0), id2 = idesc_e2m1(0, 0, false, 2);
     int s = 0, it = 0, n = 0, b = 0;
-    uint32_t ph = 0, bph = 0;
+    uint32_t ph = 0, bph = keep ? 1 : 0;
     bool ok = true, any = false;
-    for (int t = first; ok && t < ntiles; t += step, ++n) {
+    for (int t = t0; ok && t < t1; ++t, ++n) {
       const int acc = n & 1;
       ok = mbar_wait(smem_addr(&sh->acc_empty[acc]), (uint32_t(n >> 1) & 1u) ^ 1u, abort,
                      kSmallWaitNs);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const uint32_t d = tmem + uint32_t(acc * ND * NT);
-      if (resident) b = 0;
+      if (keep) {
+        b = 0;
+        if (opens(t)) bph ^= 1;
+      }
+      const bool release = closes(t);
       for (int c = 0; c < nch; ++c, ++it) {
         ok = mbar_wait(bfull(b), bph, abort, kSmallWaitNs) &&
              mbar_wait(full(s), ph, abort, kSmallWaitNs);
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kSmallThreads)
                                (c > 0 || j > 0) ? 1u : 0u);
           }
           mma_commit(empty(s));
-          if (!resident) mma_commit(bempty(b));
+          if (release) mma_commit(bempty(b));
         }
         __syncwarp();
         any = true;
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kSmallThreads)
           s = 0;
           ph ^= 1;
         }
-        if (++b == slots && !resident) {
+        if (++b == slots && !keep) {
           b = 0;
           bph ^= 1;
         }
@@ -322,19 +337,21 @@ __global__ void __launch_bounds__(kSmallThreads)
     bool met = split == 1;  // the other blocks' barriers are known to be set up
     // Values into codes, by warps 6..9; where that is done once, by the
     // epilogue's warps as well, which have nothing else to do yet.
-    if (warp >= kSmallQuantWarp || resident) {
+    if (warp >= kSmallQuantWarp || once) {
       if (MODE == kMxDown) wait_before();  // the hidden values
-      const int th = int(threadIdx.x) - (resident ? 64 : kSmallQuantWarp * 32);
-      const int nq = resident ? 256 : 128;
+      const int th = int(threadIdx.x) - (once ? 64 : kSmallQuantWarp * 32);
+      const int nq = once ? 256 : 128;
       constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
       const uint8_t* x = static_cast<const uint8_t*>(a.x);
       bool ok = true, bad = false;
       float g = 1.f, g_inv = 1.f;
-      int fill = 0;  // chunks quantized so far (slot and phase of the next)
-      int n = 0;
-      for (int t = first; t < ntiles; t += step, ++n) {
+      int ring = 0;   // chunks quantized so far (slot and phase of the next)
+      int fill = -1;  // fills
+      for (int t = t0; t < t1; ++t) {
+        if (!opens(t)) continue;
+        ++fill;
         // (the warps share barriers: they go on together or not at all)
-        if ((resident && n > 0) || !group_all(1, nq, ok)) break;
+        if (!group_all(1, nq, ok)) break;
         const Tile r = tile(t);
         // 8 threads take a token's chunk (a block of 32 elements each); as many
         // chunks at a time as the tokens leave threads for
@@ -361,11 +378,11 @@ __global__ void __launch_bounds__(kSmallThreads)
             if (live && k < a.K) raw[j] = load_raw8<DT>(xr, k + 8 * j);
           }
         };
-        if (FMT == LUTQ_NVFP4 && (MODE != kMxPlain || n == 0)) {
+        if (FMT == LUTQ_NVFP4 && (MODE != kMxPlain || fill == 0)) {
           // the token's largest finite magnitude.  Plain: of this block's
           // chunks, then the cluster's; experts: of the whole row
           const int m0 = MODE == kMxPlain ? c0 : 0, m1 = MODE == kMxPlain ? c0 + nch : a.chunks;
-          const int pc = MODE == kMxPlain ? 0 : n & 1;
+          const int pc = MODE == kMxPlain ? 0 : fill & 1;
           uint32_t m = 0;
 #pragma unroll 2
           for (int c = lead < per ? m0 + lead : m1; c < m1; c += per) {
@@ -404,13 +421,6 @@ __global__ void __launch_bounds__(kSmallThreads)
           }
           g = nv_row_scale(m);
           g_inv = nv_row_scale_inverse(g);
-          if (MODE != kMxPlain && n > 1) {
-            // the epilogue must have used what tile n - 2 left here
-            ok = mbar_wait(smem_addr(&sh->acc_empty[n & 1]), (uint32_t(n >> 1) & 1u) ^ 1u, abort,
-                           kSmallWaitNs);
-            if (!(ok = group_all(1, nq, ok))) break;
-          }
-          if (live && q == 0 && lead == 0) sh->row_scale[pc][i] = g;
           if (MODE != kMxPlain) {
             asm volatile("bar.sync 1, %0;" ::"r"(nq) : "memory");  // all have read my_max
             if (th < NT) sh->my_max[pc][th] = 0u;
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         Raw8<DT> raw[4];
         if (lead < per && lead < nch) load32(c0 + lead, raw);
         for (int c = lead < per ? lead : nch; c < nch; c += per) {
-          const int f = fill + c, slot = f % slots;
+          const int f = keep ? fill * slots + c : ring + c, slot = f % slots;
           uint32_t sc[2] = {0u, 0u}, codes[4] = {0u, 0u, 0u, 0u};
           constexpr int H = FMT == LUTQ_MXFP4 ? 1 : 2;  // blocks per 32 elements
           if (live) {
@@ -445,10 +455,9 @@ __global__ void __launch_bounds__(kSmallThreads)
             if (int64_t(c0 + c) * kMxChunk + q * 32 >= a.K) sc[0] = sc[1] = 0u;
           }
           if (c + per < nch) load32(c0 + c + per, raw);  // a round ahead
-          if (!resident) {
-            ok = mbar_wait(bempty(slot), (uint32_t(f / slots) & 1u) ^ 1u, abort, kSmallWaitNs);
-            if (!ok) break;
-          }
+          ok = mbar_wait(bempty(slot), (uint32_t(f / slots) & 1u) ^ 1u, abort, kSmallWaitNs);
+          if (!ok) break;
+          if (FMT == LUTQ_NVFP4 && c == 0 && q == 0 && live) sh->row_scale[fill & 3][i] = g;
           uint8_t* bp = tokens + slot * Cfg::SLOT;
           if (live) {
             *reinterpret_cast<uint4*>(bp + i * 128 + ((q ^ (i & 7)) * 16)) =
@@ -464,18 +473,19 @@ __global__ void __launch_bounds__(kSmallThreads)
           // 8 * rows threads have this chunk; the barrier counts 128 arrivals
           mbar_arrive_n(bfull(slot), uint32_t(NT / rows));
         }
-        fill += nch;
+        ring += nch;
       }
       if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
     }
     if (!met) cluster_wait_all();
     if (warp < kSmallQuantWarp) {
       const int quarter = warp & 3;
-      int n = 0;
+      int n = 0, fill = -1;
       bool ok = true;
       const int own = NT / split;  // columns of a split tile that this block sums
-      for (int t = first; ok && t < ntiles; t += step, ++n) {
+      for (int t = t0; ok && t < t1; ++t, ++n) {
         const Tile r = tile(t);
+        if (opens(t)) ++fill;
         const int acc = n & 1;
         const int64_t row = int64_t(r.mt) * 128 + quarter * 32 + lane;
         float ga[2] = {1.f, 1.f};
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         tc_fence_after();
         auto put = [&](int m, float v0, float v1) {
           if (FMT == LUTQ_NVFP4) {
-            const float gb = sh->row_scale[MODE == kMxPlain ? 0 : n & 1][m];
+            const float gb = sh->row_scale[fill & 3][m];
             v0 = v0 * ga[0] * gb;
             if (ND == 2) v1 = v1 * ga[1] * gb;
           }
@@ -511,8 +521,7 @@ __global__ void __launch_bounds__(kSmallThreads)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (j < r.valid) put(j, __uint_as_float(v[0][j]), __uint_as_float(v[ND - 1][j]));
-          // (behind the reads of row_scale, which a later tile's quantizing
-          // warps write once this set of sums is free)
+          // (behind the reads of row_scale: see there)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));

@@ -1,12 +1,19 @@
 // Routing to experts: scores, selection and weights, one warp per token.
 //
-// The scores and every comparison are in 64 bits: which of two nearly equal
-// experts wins is a discrete outcome, and 32-bit scores would decide it by the
-// rounding of exp.  The arithmetic is small (E exponentials a token; a
-// multiprocessor has half as many 64-bit as 32-bit lanes).  A lane keeps E / 32 scores as
-// order-preserving 64-bit keys; the largest key of the warp takes three warp
-// reductions (high word, low word, lowest expert), so ties go to the lowest
-// expert whatever the order of arrival.
+// The order of the scores is that of 64 bits: which of two nearly equal
+// experts wins is a discrete outcome, and 32-bit scores alone would decide it
+// by the rounding of exp.  64-bit exponentials of all scores are what this
+// operator costs, so they are avoided where 32 bits suffice: the scores are
+// selected in 32 bits first, and if every comparison that decided something
+// was clear by more than both scores can be off, the outcome is that of 64
+// bits; then only the top_k weights are computed in 64.  Otherwise (a tie, a
+// close call, fewer experts available than asked for) the token is routed
+// again with 64-bit scores.  A softmax whose weights are not renormalised
+// needs the 64-bit sum over all experts, and takes that path at once.
+//
+// A lane holds every 32nd expert's score.  The largest score of the warp, and
+// the lowest expert that has it, take two warp reductions of 32-bit keys
+// (three for 64-bit ones), so ties go to the lowest expert.
 #include <algorithm>
 #include <cmath>
 
@@ -25,7 +32,14 @@ struct RouteArgs {
   int64_t T;
   int dtype, E, score, groups, top_groups, group_best, top_k, renormalize;
   float scale;
+  int per;             // experts of a group
+  uint32_t per_magic;  // ceil(2^20 / per): e / per = e * magic >> 20 for e < 1024, per <= 512
+  int group_lanes;     // log2 of the lanes that share a group
 };
+
+__device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
+  return int(uint32_t(e) * a.per_magic >> 20);
+}
 
 // Doubles to unsigned keys in the same order, all above 1.
 __device__ __forceinline__ uint64_t order_key(double v) {
@@ -48,38 +62,151 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// P: scores a lane holds (E <= 32 P)
+// Floats to unsigned keys in the same order; 0 stands for "taken".  The lowest
+// bits, log2 P of them, are given up for the number of the score in its lane.
+__device__ __forceinline__ uint32_t order_key32(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value32(uint32_t k) {
+  // (below the key of the lowest float: -infinity, whatever its low bits)
+  return k < 0x00800000u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+}
+// Whether 32-bit values (sums of `scores` scores) tell the order of the exact
+// ones.  A score p <= 1 is off by less than 2^-20 (exp, a sum, a division),
+// p + bias by another 2^-24 of its magnitude, a key of P scores by P 2^-23 of
+// it (P <= 32).
+__device__ __forceinline__ bool clearly_above(float a, float b, float scores) {
+  if (b == -INFINITY) return a > -INFINITY;  // nothing available there
+  return a - b > scores * 1.2e-5f * (1.f + fabsf(a) + fabsf(b));
+}
+
+// The selection in 32 bits; false if some decision was not clear.  Lane j
+// receives the j-th choice.
 template <int P>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ double route_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
-  if (t >= a.T) return;
-  double* ps = route_smem + warp * a.E;  // the token's scores; -1: not available
+__device__ __forceinline__ bool route_select32(const RouteArgs& a, const float (&z)[P], float top,
+                                               float* cs, int lane, int* mine) {
   const int E = a.E;
+  float c[P], bias[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    bias[i] = a.bias != nullptr && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
+  if (a.score == LUTQ_SCORE_SOFTMAX) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      c[i] = z[i] > -INFINITY ? __expf(z[i] - top) : 0.f;
+      sum += c[i];
+    }
+    if (a.bias != nullptr) {  // (without one the exponentials have the order)
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      sum = 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < P; ++i) c[i] *= sum;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) c[i] = __fdividef(1.f, 1.f + __expf(-z[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) c[i] = z[i] > -INFINITY ? c[i] + bias[i] : -INFINITY;
+  bool clear = true;
+  if (a.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane + 32 * i < E) cs[lane + 32 * i] = c[i];
+    __syncwarp();
+    const int L = 1 << a.group_lanes, gr = lane >> a.group_lanes;
+    float b0 = -INFINITY, b1 = -INFINITY;  // the two best
+    if (gr < a.groups) {
+      const float* cg = cs + gr * a.per;
+      for (int j = lane & (L - 1); j < a.per; j += L) {
+        const float v = cg[j];
+        b1 = fmaxf(b1, fminf(b0, v));
+        b0 = fmaxf(b0, v);
+      }
+    }
+    for (int x = 1; x < L; x *= 2) {
+      const float o0 = __shfl_xor_sync(0xffffffffu, b0, x);
+      const float o1 = __shfl_xor_sync(0xffffffffu, b1, x);
+      b1 = fmaxf(fmaxf(b1, o1), fminf(b0, o0));
+      b0 = fmaxf(b0, o0);
+    }
+    const float best = a.group_best == 2 && b1 > -INFINITY ? b0 + b1 : b0;
+    uint32_t gk = gr < a.groups && (lane & (L - 1)) == 0 ? order_key32(best) : 0u;
+    uint32_t kept = 0, last = 0;
+    for (int i = 0; i < a.top_groups; ++i) {
+      last = __reduce_max_sync(0xffffffffu, gk);
+      // (equal ones leave together; then the order is not clear below)
+      const uint32_t who = __ballot_sync(0xffffffffu, gk == last);
+      clear = clear && (who & (who - 1u)) == 0u;
+      kept |= 1u << ((__ffs(who) - 1) >> a.group_lanes);
+      if (gk == last) gk = 0u;
+    }
+    const uint32_t next = __reduce_max_sync(0xffffffffu, gk);
+    if (next != 0u) clear = clear && clearly_above(key_value32(last), key_value32(next), 2.f);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (!((kept >> group_of(a, lane + 32 * i)) & 1u)) c[i] = -INFINITY;
+  }
+  uint32_t key[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    key[i] = lane + 32 * i < E ? (order_key32(c[i]) & ~uint32_t(P - 1)) | uint32_t(i) : 0u;
+  uint32_t chosen = 0, who_j = 1;
+  for (int j = 0; j <= a.top_k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) m = max(m, key[i]);
+    const uint32_t k = __reduce_max_sync(0xffffffffu, m);
+    const uint32_t who = __ballot_sync(0xffffffffu, m == k);
+    if (lane == (j & 31)) {  // (the last of 33 passes lane 0 by below)
+      if (j < 32) {
+        chosen = k;
+        who_j = who;
+      }
+    }
+    if (j == 32) clear = clear && clearly_above(key_value32(__shfl_sync(0xffffffffu, chosen, 31)),
+                                                key_value32(k), 1.f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = key[i] == k ? 0u : key[i];
+  }
+  // lane j: the j-th largest key.  Clear if it is one score's, available, and
+  // clearly below the one before (the lane behind the last choice: only that)
+  const float v = key_value32(chosen), before = __shfl_up_sync(0xffffffffu, v, 1);
+  bool fine = true;
+  if (lane < a.top_k) fine = (who_j & (who_j - 1u)) == 0u && chosen != 0u && v > -INFINITY;
+  if (lane >= 1 && lane <= a.top_k && chosen != 0u) fine = fine && clearly_above(before, v, 1.f);
+  *mine = __ffs(who_j) - 1 + 32 * int(chosen & uint32_t(P - 1));
+  return __all_sync(0xffffffffu, clear && fine);
+}
+
+__device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
+  if (a.dtype == LUTQ_FP32) return static_cast<const float*>(a.logits)[at];
+  if (a.dtype == LUTQ_BF16) return bf16_lo_to_f32(static_cast<const uint16_t*>(a.logits)[at]);
+  return __half2float(static_cast<const __half*>(a.logits)[at]);
+}
+
+// The selection in 64 bits: lane j receives the j-th choice and its score.
+struct Choice {
+  double w;
+  int mine;
+};
+template <int P>
+__device__ __noinline__ Choice route_select64(const RouteArgs& a, int64_t t, float topf,
+                                              double* ps, int lane) {
+  const int E = a.E;
+  Choice out = {0.0, 0};
   double p[P];
-  bool bad = false;
-  double top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = lane + 32 * i;
     float z = -INFINITY;
-    if (e < E) {
-      const int64_t at = t * E + e;
-      if (a.dtype == LUTQ_FP32) z = static_cast<const float*>(a.logits)[at];
-      else if (a.dtype == LUTQ_BF16) z = bf16_lo_to_f32(static_cast<const uint16_t*>(a.logits)[at]);
-      else z = __half2float(static_cast<const __half*>(a.logits)[at]);
-      bad |= isnan(z) || z == INFINITY;
-      if (isnan(z)) z = -INFINITY;
-    }
-    p[i] = double(z);
-    top = fmax(top, p[i]);
+    if (lane + 32 * i < E) z = load_logit(a, t * E + lane + 32 * i);
+    p[i] = isnan(z) ? -INFINITY : double(z);
   }
   if (a.score == LUTQ_SCORE_SOFTMAX) {
-#pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const double top = double(topf);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -104,12 +231,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   __syncwarp();
 
   // groups: the sum of a group's best scores; the best groups stay
-  const int per = E / a.groups;
+  const int per = a.per;
   uint32_t kept = 0xffffffffu;
   if (a.groups > 1) {
-    int pow2 = 2;
-    while (pow2 < a.groups) pow2 *= 2;
-    const int L = 32 / pow2, gr = lane / L;
+    const int L = 1 << a.group_lanes, gr = lane >> a.group_lanes;
     double b0 = -INFINITY, b1 = -INFINITY;  // the two best
     if (gr < a.groups) {
       for (int j = lane % L; j < per; j += L) {
@@ -143,12 +268,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     const int e = lane + 32 * i;
     key[i] = kTaken;
     if (e < E) {
-      const bool in = p[i] >= 0.0 && (a.groups == 1 || ((kept >> (e / per)) & 1u));
+      const bool in = p[i] >= 0.0 && (a.groups == 1 || ((kept >> group_of(a, e)) & 1u));
       key[i] = in ? order_key(a.bias != nullptr ? p[i] + double(a.bias[e]) : p[i]) : kUnavailable;
     }
   }
-  int mine = 0;          // lane j: the j-th choice
-  double w = 0.0;
   for (int j = 0; j < a.top_k; ++j) {
     uint64_t k = kTaken;
     int e = E;
@@ -159,12 +282,72 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
         e = lane + 32 * i;
       }
     const int won = warp_argmax(k, e);
-    if (lane == j) mine = won;
+    if (lane == j) out.mine = won;
     const bool served = __any_sync(0xffffffffu, e == won && k > kUnavailable);
-    if (lane == j) w = served ? ps[won] : 0.0;
+    if (lane == j) out.w = served ? ps[won] : 0.0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 32 * i == won) key[i] = kTaken;
+  }
+  return out;
+}
+
+// P: scores a lane holds (E <= 32 P)
+template <int P>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ double route_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  double* ps = route_smem + warp * a.E;  // the token's scores; -1: not available
+  const int E = a.E;
+  float z[P];
+  bool bad = false;
+  float topf = -INFINITY;
+  const int64_t first = t * E + lane;
+#pragma unroll
+  for (int i = 0; i < P; ++i) z[i] = -INFINITY;
+  if (a.dtype == LUTQ_FP32) {
+    const float* p = static_cast<const float*>(a.logits) + first;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane + 32 * i < E) z[i] = p[32 * i];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + first;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane + 32 * i < E)
+        z[i] = a.dtype == LUTQ_BF16 ? bf16_lo_to_f32(p[32 * i])
+                                    : __half2float(__ushort_as_half(p[32 * i]));
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    bad |= !(z[i] < INFINITY);  // NaN, too
+    if (isnan(z[i])) z[i] = -INFINITY;
+    topf = fmaxf(topf, z[i]);
+  }
+  if (a.score == LUTQ_SCORE_SOFTMAX) {
+#pragma unroll
+    for (int x = 16; x; x >>= 1) topf = fmaxf(topf, __shfl_xor_sync(0xffffffffu, topf, x));
+  }
+  if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
+  int mine = 0;    // lane j: the j-th choice and its weight
+  double w = 0.0;
+  bool done = false;
+  if ((a.score == LUTQ_SCORE_SIGMOID || a.renormalize) && !__any_sync(0xffffffffu, bad)) {
+    done = route_select32<P>(a, z, topf, reinterpret_cast<float*>(ps), lane, &mine);
+    if (done && lane < a.top_k) {
+      const double v = double(load_logit(a, t * E + mine));
+      w = a.score == LUTQ_SCORE_SOFTMAX ? exp(v - double(topf)) : 1.0 / (1.0 + exp(-v));
+    }
+    __syncwarp();
+  }
+  if (!done) {
+    const Choice c = route_select64<P>(a, t, topf, ps, lane);
+    mine = c.mine;
+    w = c.w;
   }
   if (a.renormalize) {
     const double sum = warp_sum(lane < a.top_k ? w : 0.0);
@@ -174,7 +357,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     a.ids[t * a.top_k + lane] = mine;
     a.weights[t * a.top_k + lane] = float(w * double(a.scale));
   }
-  if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
 }
 
 cudaError_t launch_route(const void* logits, int dtype, int64_t T, int E, const float* bias,
@@ -182,7 +364,9 @@ cudaError_t launch_route(const void* logits, int dtype, int64_t T, int E, const 
                          int renormalize, float scale, int32_t* ids, float* weights,
                          int32_t* dev_status, cudaStream_t stream) {
   RouteArgs a = {logits, bias,  ids,    weights,    dev_status, T,     dtype, E,
-                 score,  groups, top_groups, group_best, top_k, renormalize, scale};
+                 score,  groups, top_groups, group_best, top_k, renormalize, scale, E / groups, 0, 5};
+  a.per_magic = uint32_t(mx_ceil(int64_t(1) << 20, a.per));
+  while ((32 >> a.group_lanes) < groups) --a.group_lanes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(mx_ceil(T, kRouteWarps)));
   cfg.blockDim = dim3(kRouteWarps * 32);

@@ -101,6 +101,19 @@ def test_near_ties_need_64_bits(lq):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gap", [2.0 ** -23, 3e-7, 1e-6, 4e-6, 1.7e-5, 1e-4])
+def test_close_calls(lq, score, gap):
+    """Logits, biases and group sums about as far apart as 32-bit scores can tell, and closer."""
+    g = torch.Generator().manual_seed(int(1 / gap))
+    base = torch.randn(200, 8, generator=g).repeat_interleave(8, 1)
+    z = base + gap * torch.randint(-3, 4, (200, 64), generator=g)
+    bias = (gap * torch.randint(-2, 3, (64,), generator=g)).float()
+    for b in (None, bias):
+        for kw in (dict(), dict(groups=8, top_groups=3, group_best=2), dict(groups=4, top_groups=1)):
+            _check(lq, z, 8, bias=b, score=score, renormalize=True, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_nonfinite_reported(lq, score):
     z = torch.randn(3, 40, generator=torch.Generator().manual_seed(1))
     z[1, 7] = np.nan
