@@ -4,12 +4,11 @@
 // experts wins is a discrete outcome, and 32-bit scores alone would decide it
 // by the rounding of exp.  64-bit exponentials of all scores are what this
 // operator costs, so they are avoided where 32 bits suffice: the scores are
-// selected in 32 bits first, and if every comparison that decided something
-// was clear by more than both scores can be off, the outcome is that of 64
-// bits; then only the top_k weights are computed in 64.  Otherwise (a tie, a
-// close call, fewer experts available than asked for) the token is routed
-// again with 64-bit scores.  A softmax whose weights are not renormalised
-// needs the 64-bit sum over all experts, and takes that path at once.
+// selected in 32 bits first: the top_k, and those that are below by no more than
+// both scores can be off.  Only these few get 64-bit scores, which give the
+// weights, and the order where it is close.  Where 32 bits do not settle that
+// much (a close call between groups, fewer experts available than asked for)
+// the token is routed again with 64-bit scores.
 //
 // A lane holds every 32nd expert's score.  The largest score of the warp, and
 // the lowest expert that has it, take two warp reductions of 32-bit keys
@@ -72,21 +71,31 @@ __device__ __forceinline__ float key_value32(uint32_t k) {
   // (below the key of the lowest float: -infinity, whatever its low bits)
   return k < 0x00800000u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
-// Whether 32-bit values (sums of `scores` scores) tell the order of the exact
-// ones.  A score p <= 1 is off by less than 2^-20 (exp, a sum, a division),
-// p + bias by another 2^-24 of its magnitude, a key of P scores by P 2^-23 of
-// it (P <= 32).
-__device__ __forceinline__ bool clearly_above(float a, float b, float scores) {
+// Whether 32-bit scores tell the order of the exact ones.  `base` bounds the
+// error of p: sigmoid, 1 / (1 + e) with e off by (2 + 1.2 |z|) ulp and a
+// division by 2 ulp, in all below 4e-7; softmax, by the same with a sum and
+// two multiplications, below 1.2e-6.  `rel` times the score bounds that of the
+// addition of the bias and of a key's lost bits.
+struct Error32 {
+  float base, rel;
+};
+__device__ __forceinline__ bool clearly_above(float a, float b, Error32 e) {
   if (b == -INFINITY) return a > -INFINITY;  // nothing available there
-  return a - b > scores * 1.2e-5f * (1.f + fabsf(a) + fabsf(b));
+  return a - b > 2.f * e.base + e.rel * (fabsf(a) + fabsf(b));
 }
 
-// The selection in 32 bits; false if some decision was not clear.  Lane j
-// receives the j-th choice.
+// The selection in 32 bits.  Lane j < n receives the expert with the j-th
+// largest 32-bit score (j alone where the order is clear); the top_k largest
+// exact scores are certainly among these n.  Returns n, or 0 if 32 bits do not
+// tell: which groups stay, fewer available than asked for, too many close.
 template <int P>
-__device__ __forceinline__ bool route_select32(const RouteArgs& a, const float (&z)[P], float top,
-                                               float* cs, int lane, int* mine) {
+__device__ __forceinline__ int route_select32(const RouteArgs& a, const float (&z)[P], float top,
+                                               float* cs, int lane, int* mine,
+                                              bool* ordered) {
   const int E = a.E;
+  const float base = a.score == LUTQ_SCORE_SOFTMAX ? 1.2e-6f : 4e-7f;
+  const Error32 score_error = {base, float(P + 1) * 0x1p-23f};
+  const Error32 group_error = {2.f * base, 0x1p-22f};
   float c[P], bias[P];
 #pragma unroll
   for (int i = 0; i < P; ++i)
@@ -111,8 +120,8 @@ __device__ __forceinline__ bool route_select32(const RouteArgs& a, const float (
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) c[i] = z[i] > -INFINITY ? c[i] + bias[i] : -INFINITY;
-  bool clear = true;
   if (a.groups > 1) {
+    bool clear = true;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 32 * i < E) cs[lane + 32 * i] = c[i];
@@ -145,7 +154,9 @@ __device__ __forceinline__ bool route_select32(const RouteArgs& a, const float (
       if (gk == last) gk = 0u;
     }
     const uint32_t next = __reduce_max_sync(0xffffffffu, gk);
-    if (next != 0u) clear = clear && clearly_above(key_value32(last), key_value32(next), 2.f);
+    if (next != 0u)
+      clear = clear && clearly_above(key_value32(last), key_value32(next), group_error);
+    if (!clear) return 0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (!((kept >> group_of(a, lane + 32 * i)) & 1u)) c[i] = -INFINITY;
@@ -154,32 +165,33 @@ __device__ __forceinline__ bool route_select32(const RouteArgs& a, const float (
 #pragma unroll
   for (int i = 0; i < P; ++i)
     key[i] = lane + 32 * i < E ? (order_key32(c[i]) & ~uint32_t(P - 1)) | uint32_t(i) : 0u;
-  uint32_t chosen = 0, who_j = 1;
-  for (int j = 0; j <= a.top_k; ++j) {
+  float mine_v = 0.f, kth = 0.f;  // lane j: the j-th score; the top_k-th
+  int n = 0;
+  for (;; ++n) {
     uint32_t m = key[0];
 #pragma unroll
     for (int i = 1; i < P; ++i) m = max(m, key[i]);
     const uint32_t k = __reduce_max_sync(0xffffffffu, m);
-    const uint32_t who = __ballot_sync(0xffffffffu, m == k);
-    if (lane == (j & 31)) {  // (the last of 33 passes lane 0 by below)
-      if (j < 32) {
-        chosen = k;
-        who_j = who;
-      }
+    const float v = key_value32(k);
+    if (n < a.top_k) {
+      if (v == -INFINITY) return 0;
+      kth = v;
+    } else {
+      if (clearly_above(kth, v, score_error)) break;
+      if (n == 32) return 0;
     }
-    if (j == 32) clear = clear && clearly_above(key_value32(__shfl_sync(0xffffffffu, chosen, 31)),
-                                                key_value32(k), 1.f);
+    const int w = __ffs(__ballot_sync(0xffffffffu, m == k)) - 1;
+    if (lane == n) {
+      mine_v = v;
+      *mine = w + 32 * int(k & uint32_t(P - 1));
+    }
 #pragma unroll
-    for (int i = 0; i < P; ++i) key[i] = key[i] == k ? 0u : key[i];
+    for (int i = 0; i < P; ++i) key[i] = key[i] == k && lane == w ? 0u : key[i];
   }
-  // lane j: the j-th largest key.  Clear if it is one score's, available, and
-  // clearly below the one before (the lane behind the last choice: only that)
-  const float v = key_value32(chosen), before = __shfl_up_sync(0xffffffffu, v, 1);
-  bool fine = true;
-  if (lane < a.top_k) fine = (who_j & (who_j - 1u)) == 0u && chosen != 0u && v > -INFINITY;
-  if (lane >= 1 && lane <= a.top_k && chosen != 0u) fine = fine && clearly_above(before, v, 1.f);
-  *mine = __ffs(who_j) - 1 + 32 * int(chosen & uint32_t(P - 1));
-  return __all_sync(0xffffffffu, clear && fine);
+  const float before = __shfl_up_sync(0xffffffffu, mine_v, 1);
+  *ordered = __all_sync(0xffffffffu, lane == 0 || lane >= n ||
+                                         clearly_above(before, mine_v, score_error));
+  return n;  // the same in all lanes
 }
 
 __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
@@ -333,29 +345,51 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     for (int x = 16; x; x >>= 1) topf = fmaxf(topf, __shfl_xor_sync(0xffffffffu, topf, x));
   }
   if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
-  int mine = 0;    // lane j: the j-th choice and its weight
+  int mine = 0, rank = lane;  // an expert, its place among the chosen, its score
   double w = 0.0;
-  bool done = false;
-  if ((a.score == LUTQ_SCORE_SIGMOID || a.renormalize) && !__any_sync(0xffffffffu, bad)) {
-    done = route_select32<P>(a, z, topf, reinterpret_cast<float*>(ps), lane, &mine);
-    if (done && lane < a.top_k) {
+  int n = 0;
+  if (!__any_sync(0xffffffffu, bad)) {
+    bool ordered = true;
+    n = route_select32<P>(a, z, topf, reinterpret_cast<float*>(ps), lane, &mine, &ordered);
+    if (lane < n) {
       const double v = double(load_logit(a, t * E + mine));
       w = a.score == LUTQ_SCORE_SOFTMAX ? exp(v - double(topf)) : 1.0 / (1.0 + exp(-v));
     }
+    // a softmax's sum, unless it cancels (renormalised, and no bias to add to p)
+    if (n > 0 && a.score == LUTQ_SCORE_SOFTMAX &&
+        (!a.renormalize || (!ordered && a.bias != nullptr))) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (z[i] > -INFINITY) sum += exp(double(z[i]) - double(topf));
+      w /= warp_sum(sum);
+    }
+    if (n > 0 && !ordered) {
+      // the exact order of the few: how many come before this one
+      const double c = w + (a.bias != nullptr && lane < n ? double(a.bias[mine]) : 0.0);
+      rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const double cj = __shfl_sync(0xffffffffu, c, j);
+        const int ej = __shfl_sync(0xffffffffu, mine, j);
+        rank += cj > c || (cj == c && ej < mine);
+      }
+      if (lane >= n) rank = 32;
+    }
     __syncwarp();
   }
-  if (!done) {
+  if (n == 0) {
     const Choice c = route_select64<P>(a, t, topf, ps, lane);
     mine = c.mine;
     w = c.w;
   }
+  const bool in = rank < a.top_k;
   if (a.renormalize) {
-    const double sum = warp_sum(lane < a.top_k ? w : 0.0);
+    const double sum = warp_sum(in ? w : 0.0);
     w = sum > 0.0 ? w / sum : 0.0;
   }
-  if (lane < a.top_k) {
-    a.ids[t * a.top_k + lane] = mine;
-    a.weights[t * a.top_k + lane] = float(w * double(a.scale));
+  if (in) {
+    a.ids[t * a.top_k + rank] = mine;
+    a.weights[t * a.top_k + rank] = float(w * double(a.scale));
   }
 }
 
