@@ -278,6 +278,30 @@ __device__ __forceinline__ void store1(void* y, int64_t i, float v) {
   }
 }
 
+// Eight values rounded once to the output type, from element i (a multiple of
+// 8, in a 16-byte aligned y).
+template <int DT>
+__device__ __forceinline__ void store8(void* y, int64_t i, const float (&v)[8]) {
+  if constexpr (DT == LUTQ_FP32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + i);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == LUTQ_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // Launch with the next kernel of the stream allowed to start early: every
 // kernel of this family waits for the one before it (griddepcontrol.wait)
 // before it reads or writes anything.

@@ -18,7 +18,9 @@
 namespace lutq {
 
 constexpr int kPlanThreads = 512;
-constexpr int64_t kSmallPairs = 16;  // pairs an expert, at most, for the kernel of few tokens
+// Pairs an expert, at most, for the kernel of few tokens.  Measured (64 experts
+// of 4096 x 2048, 60 of 2048 x 1440): SMALL_PAIRS_FIGURES
+constexpr int64_t kSmallPairsMx = 8, kSmallPairsNv = 4;
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {
@@ -27,84 +29,104 @@ struct MoePlan {
   int32_t* slot;    // [pairs] a pair's row, or -1 (id outside 0..E-1)
 };
 
-// Block e: counts every expert's pairs (shared-memory histogram), adds up the
-// rows before its own, then hands out its rows: each warp owns a run of pairs
-// and reads it 32 at a time, so a scan over the warps' counts and the ballots
-// keeps the pairs' order.
+// Four ids from place i on, -1 behind the end.
+__device__ __forceinline__ int4 load_ids(const int32_t* ids, int i, int end, bool aligned) {
+  if (aligned && i + 4 <= end) return *reinterpret_cast<const int4*>(ids + i);
+  return make_int4(i < end ? ids[i] : -1, i + 1 < end ? ids[i + 1] : -1,
+                   i + 2 < end ? ids[i + 2] : -1, i + 3 < end ? ids[i + 3] : -1);
+}
+
+// Two launches of a block for each expert e.  The first counts its pairs.  The
+// second adds up the rows before its own from all counts and hands its rows
+// out: each warp owns a run of pairs, 128 at a time, and a scan over the
+// warps' and the lanes' counts keeps the pairs' order.
+template <bool PLACE>
 __global__ void __launch_bounds__(kPlanThreads)
     moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int E, MoePlan p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int W = kPlanThreads / 32;
-  extern __shared__ int32_t hist[];
   __shared__ int32_t warp_count[W];
   __shared__ int32_t base_s;
   const int e = blockIdx.x, th = threadIdx.x, lane = th & 31, warp = th >> 5;
-  for (int i = th; i < E; i += kPlanThreads) hist[i] = 0;
+  const bool aligned = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
   if (th == 0) base_s = 0;
-  __syncthreads();
-  const int run = (pairs + kPlanThreads - 1) / kPlanThreads * 32;  // a multiple of 32
+  const int run = (pairs + W * 128 - 1) / (W * 128) * 128;
   const int i0 = min(pairs, warp * run), i1 = min(pairs, i0 + run);
   int mine = 0;
 #pragma unroll 4
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const int id = ids[i];
-    mine += id == e;
-    if (uint32_t(id) < uint32_t(E)) atomicAdd(&hist[id], 1);
-    else if (e == 0) p.slot[i] = -1;
+  for (int i = i0 + 4 * lane; i < i1; i += 128) {
+    const int4 d = load_ids(ids, i, i1, aligned);
+    mine += (d.x == e) + (d.y == e) + (d.z == e) + (d.w == e);
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) warp_count[warp] = mine;
   __syncthreads();
+  if (!PLACE) {
+    if (warp == 0) {
+      const int c = __reduce_add_sync(0xffffffffu, lane < W ? warp_count[lane] : 0);
+      if (lane == 0) p.counts[e] = c;
+    }
+    return;
+  }
   int before = 0;
-  for (int i = th; i < e; i += kPlanThreads) before += (hist[i] + 127) / 128 * 128;
+  for (int i = th; i < e; i += kPlanThreads) before += (p.counts[i] + 127) / 128 * 128;
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) atomicAdd(&base_s, before);
   __syncthreads();
   int row = base_s;
-  if (th == 0) {
-    p.counts[e] = hist[e];
-    p.bases[e] = row;
+  if (th == 0) p.bases[e] = row;
+  if (e == 0) {  // pairs of no expert
+    for (int i = i0 + lane; i < i1; i += 32)
+      if (uint32_t(ids[i]) >= uint32_t(E)) p.slot[i] = -1;
   }
   if (mine == 0) return;
   for (int w = 0; w < warp; ++w) row += warp_count[w];
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const bool here = i + lane < i1 && ids[i + lane] == e;
-    const uint32_t who = __ballot_sync(0xffffffffu, here);
-    if (here) p.slot[i + lane] = row + __popc(who & ((1u << lane) - 1u));
-    row += __popc(who);
+  for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
+    const int4 d = load_ids(ids, i, i1, aligned);
+    const int n = (d.x == e) + (d.y == e) + (d.z == e) + (d.w == e);
+    if (!__any_sync(0xffffffffu, n)) continue;
+    int scan = n;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, x);
+      if (lane >= x) scan += v;
+    }
+    int r = row + scan - n;
+    if (d.x == e) p.slot[i] = r++;
+    if (d.y == e) p.slot[i + 1] = r++;
+    if (d.z == e) p.slot[i + 2] = r++;
+    if (d.w == e) p.slot[i + 3] = r++;
+    row += __shfl_sync(0xffffffffu, scan, 31);
   }
 }
 
 // y[t] = sum_j weights[t, j] * out[slot[t, j]] in fp32, rounded once.  Without
 // slots, a pair's row is its own number (and counts if its id is an expert).
-template <int DT>
+// PT: the type of the rows (see launch_mx_experts).
+template <int DT, int PT>
 __global__ void __launch_bounds__(256)
-    moe_combine_kernel(const float* __restrict__ out, const int32_t* __restrict__ slot,
+    moe_combine_kernel(const void* __restrict__ out, const int32_t* __restrict__ slot,
                        const int32_t* __restrict__ ids, int E, const float* __restrict__ weights,
                        int top_k, int64_t D, void* y) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t t = blockIdx.x;
-  const int64_t d = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  const int64_t d = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 8;
   if (d >= D) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int j = 0; j < top_k; ++j) {
     const int64_t p = t * top_k + j;
     const int64_t r = slot != nullptr ? slot[p] : uint32_t(ids[p]) < uint32_t(E) ? p : -1;
     if (r < 0) continue;
     const float w = weights[p];
-    const float4 v = *reinterpret_cast<const float4*>(out + r * D + d);
-    s.x += w * v.x;
-    s.y += w * v.y;
-    s.z += w * v.z;
-    s.w += w * v.w;
+    float v[8];
+    widen8<PT>(load_raw8<PT>(out, r * D + d), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += w * v[i];
   }
-  store1<DT>(y, t * D + d, s.x);
-  store1<DT>(y, t * D + d + 1, s.y);
-  store1<DT>(y, t * D + d + 2, s.z);
-  store1<DT>(y, t * D + d + 3, s.w);
+  store8<DT>(y, t * D + d, s);
 }
 
 // ------------------------------------------------------------------ host side
@@ -157,17 +179,27 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
-  auto combine = [&](const int32_t* slot) {
+  // A pair's output row is fp32, except for bf16 tokens in batches whose rows
+  // would go through memory: there it is rounded to bf16 first.
+  // That costs the result one more rounding of its own size (each of the top_k
+  // rows is off by at most 2^-8 of itself, the sum's own rounding is another
+  // 2^-8), and halves the largest traffic of the layer: 4096 tokens x 8 x 4096
+  // are 537 MB in fp32, written and read once.
+  auto combine = [&](const int32_t* slot, bool bf16_rows) {
+    const unsigned threads = unsigned(std::min<int64_t>(256, mx_ceil(D / 8, 32) * 32));
     auto go = [&](auto kernel) {
-      return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 1024))), dim3(256), 0,
-                        stream, reinterpret_cast<const float*>(ws + s.out), slot, ids, E, weights,
+      return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 2048))), dim3(threads), 0,
+                        stream, static_cast<const void*>(ws + s.out), slot, ids, E, weights,
                         top_k, D, y);
     };
-    return dtype == LUTQ_BF16   ? go(moe_combine_kernel<LUTQ_BF16>)
-           : dtype == LUTQ_FP16 ? go(moe_combine_kernel<LUTQ_FP16>)
-                                : go(moe_combine_kernel<LUTQ_FP32>);
+    if (dtype == LUTQ_BF16)
+      return bf16_rows ? go(moe_combine_kernel<LUTQ_BF16, LUTQ_BF16>)
+                       : go(moe_combine_kernel<LUTQ_BF16, LUTQ_FP32>);
+    if (dtype == LUTQ_FP16) return go(moe_combine_kernel<LUTQ_FP16, LUTQ_FP32>);
+    return go(moe_combine_kernel<LUTQ_FP32, LUTQ_FP32>);
   };
-  if (mx_small_fits(pairs, E) && pairs <= kSmallPairs * std::min(E, pairs)) {
+  const int64_t small = fmt == LUTQ_MXFP4 ? kSmallPairsMx : kSmallPairsNv;
+  if (mx_small_fits(pairs, E) && pairs <= small * std::min(E, pairs)) {
     // a handful of pairs an expert: quantized inside the products, three launches
     MxGemmArgs a = {};
     a.dev_status = dev_status;
@@ -186,7 +218,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     a.N = D;
     a.K = F;
     err = launch_mx_small(a, down, nullptr, fmt, kMxDown, ids, pairs, top_k, num_sms, stream);
-    return err != cudaSuccess ? err : combine(nullptr);
+    return err != cudaSuccess ? err : combine(nullptr, false);
   }
   // an expert has at most T rows, T top_k / E on average
   const int nt = mx_tile_tokens(T);
@@ -203,8 +235,11 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                : make_mx_map(&maps[3], rows, cap, width, 1, mx_bytes(cap, width, fmt), 16);
   };
 
-  if ((err = launch_pdl(moe_plan_kernel, dim3(unsigned(E)), dim3(kPlanThreads), size_t(E) * 4,
-                        stream, ids, pairs, E, p)) != cudaSuccess)
+  if ((err = launch_pdl(moe_plan_kernel<false>, dim3(unsigned(E)), dim3(kPlanThreads), 0, stream,
+                        ids, pairs, E, p)) != cudaSuccess)
+    return err;
+  if ((err = launch_pdl(moe_plan_kernel<true>, dim3(unsigned(E)), dim3(kPlanThreads), 0, stream,
+                        ids, pairs, E, p)) != cudaSuccess)
     return err;
   if ((err = launch_mx_quantize(x, dtype, 1, T, cap, D, fmt, nullptr, p.slot, top_k, ws + s.xq,
                                 dev_status, num_sms, stream)) != cudaSuccess)
@@ -249,7 +284,9 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.a_stride = w2;
   a.b_scales = ws + s.hq + mx_scale_off(cap, F);
   a.b_rows = reinterpret_cast<const float*>(ws + s.hq + mx_row_off(cap, F, fmt));
+  const bool bf16_rows = wide && dtype == LUTQ_BF16;
   a.y = ws + s.out;
+  a.y_dtype = bf16_rows ? LUTQ_BF16 : LUTQ_FP32;
   a.N = D;
   a.K = F;
   a.chunks = int(mx_ceil(F, kMxChunk));
@@ -265,7 +302,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                          stream);
   }
   if (err != cudaSuccess) return err;
-  return combine(p.slot);
+  return combine(p.slot, bf16_rows);
 }
 
 }  // namespace lutq

@@ -467,7 +467,9 @@ template <int FMT>
 static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode, int num_sms,
                               cudaStream_t stream) {
   if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16>(m, p, num_sms, stream);
-  if (mode == kMxDown) return launch_one<FMT, kMxDown, LUTQ_FP32>(m, p, num_sms, stream);
+  if (mode == kMxDown)
+    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16>(m, p, num_sms, stream)
+                                    : launch_one<FMT, kMxDown, LUTQ_FP32>(m, p, num_sms, stream);
   if (p.g.y_dtype == LUTQ_BF16) return launch_one<FMT, kMxPlain, LUTQ_BF16>(m, p, num_sms, stream);
   if (p.g.y_dtype == LUTQ_FP16) return launch_one<FMT, kMxPlain, LUTQ_FP16>(m, p, num_sms, stream);
   return launch_one<FMT, kMxPlain, LUTQ_FP32>(m, p, num_sms, stream);
@@ -496,7 +498,7 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
     return err;
   if ((err = make_mx_scale_map(&m.sb, tokens, token_rows, g.K, 1, t_bytes, fmt)) != cudaSuccess)
     return err;
-  const int dt = mode == kMxGateUp ? int(LUTQ_BF16) : mode == kMxDown ? int(LUTQ_FP32) : g.y_dtype;
+  const int dt = mode == kMxGateUp ? int(LUTQ_BF16) : g.y_dtype;
   PairArgs p = {};
   p.g = g;
   p.token_tiles = int(mx_ceil(g.M, nt));

@@ -49,13 +49,13 @@ __device__ __forceinline__ uint32_t mx_quantize8(const Raw8<DT>& raw, float g, f
   return mx_codes8<FMT, DT>(v, *scale, g, g_inv);
 }
 
-// WPR warps share a row.  Without `from`, row r is source and destination row
-// r, and the zero padding below the last row of a tile is written too.  With
-// it, item r reads source row from[r] (or r, if from is null and to is not)
-// and goes to the `copies` rows to[copies * r ...]; a negative entry is
-// skipped, and nothing else is written.
-template <int FMT, int DT, int WPR>
-__global__ void __launch_bounds__(kMxWarps * 32)
+// WPR warps share a row.  Not LISTED: row r is source and destination row r,
+// and the zero padding below the last row of a tile is written too.  LISTED:
+// item r reads source row from[r] (or r, if from is null) and goes to the
+// `copies` rows to[copies * r ...]; a negative entry is skipped, and nothing
+// else is written.
+template <int FMT, int DT, int WPR, bool LISTED>
+__global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4 : 1)
     mx_quantize_kernel(const void* __restrict__ x, int64_t items, int64_t rows, int64_t K,
                        const int32_t* __restrict__ from, const int32_t* __restrict__ to,
                        int copies, uint8_t* __restrict__ packed, int64_t x_stride,
@@ -64,49 +64,57 @@ __global__ void __launch_bounds__(kMxWarps * 32)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint32_t row_max[kMxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool listed = to != nullptr;
   const int64_t item = WPR == kMxWarps ? blockIdx.x
-                       : listed        ? int64_t(blockIdx.x) * kMxWarps + warp
+                       : LISTED        ? int64_t(blockIdx.x) * kMxWarps + warp
                                        : mx_row_of(blockIdx.x, warp);
   constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
   int64_t src = item < items ? item : -1;
-  if (listed) {
+  if (LISTED) {
     if (item >= items) return;
     if (from != nullptr) src = from[item];
     if (src < 0) return;  // (the whole block, where its warps share the row)
   }
-  const uint8_t* xr =
-      static_cast<const uint8_t*>(x) + (int64_t(blockIdx.z) * x_stride + src * K) * esize;
+  const uint8_t* xr = static_cast<const uint8_t*>(x) +
+                      (int64_t(blockIdx.z) * x_stride + src * K + lane * 8) * esize;
   uint8_t* pm = packed + int64_t(blockIdx.z) * packed_stride;
-  const int64_t chunks = mx_ceil(K, kMxChunk);
+  const int chunks = int(mx_ceil(K, kMxChunk));
+  const int last = int(K - int64_t(chunks - 1) * kMxChunk) / 8;  // lanes of the last chunk
   // this warp's chunks: first, first + step, ...
-  const int64_t first = WPR == kMxWarps ? blockIdx.y * kMxWarps + warp : blockIdx.y;
-  const int64_t step = int64_t(gridDim.y) * WPR;
+  const int first = WPR == kMxWarps ? blockIdx.y * kMxWarps + warp : blockIdx.y;
+  const int step = int(gridDim.y) * WPR;
+  auto inside = [&](int c) { return c < chunks - 1 || (c == chunks - 1 && lane < last); };
+  auto load = [&](int c) {
+    return load_raw8<DT>(xr, int64_t(c) * kMxChunk);
+  };
 
   float g = 1.f, g_inv = 1.f;
   if (FMT == LUTQ_NVFP4 && src >= 0) {
     // the row's largest finite magnitude (gridDim.y is 1)
     uint32_t m = 0;
-    for (int64_t c = first; c < chunks; c += step * kMxBatch) {
-      Raw8<DT> raw[kMxBatch];
+    for (int c = first; c < chunks; c += step * 2 * kMxBatch) {
+      Raw8<DT> raw[2 * kMxBatch];
 #pragma unroll
-      for (int u = 0; u < kMxBatch; ++u) {
-        const int64_t k = (c + u * step) * kMxChunk + lane * 8;
+      for (int u = 0; u < 2 * kMxBatch; ++u) {
         raw[u] = Raw8<DT>{};
-        if (k < K) raw[u] = load_raw8<DT>(xr, k);
+        if (inside(c + u * step)) raw[u] = load(c + u * step);
       }
+      uint32_t b[2 * kMxBatch], most = 0;
 #pragma unroll
-      for (int u = 0; u < kMxBatch; ++u) {
-        const uint32_t b = max_raw8<DT>(raw[u]);
-        if (b < raw_inf<DT>()) {
-          m = max(m, max_bits_f32<DT>(b));
-        } else {  // leave out what is not finite
+      for (int u = 0; u < 2 * kMxBatch; ++u) {
+        b[u] = max_raw8<DT>(raw[u]);
+        most = max(most, b[u]);
+      }
+      if (most >= raw_inf<DT>()) {  // leave out what is not finite
+        most = 0;
+#pragma unroll
+        for (int u = 0; u < 2 * kMxBatch; ++u) {
           float v[8];
           widen8<DT>(raw[u], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
         }
       }
+      m = max(m, max_bits_f32<DT>(most));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (WPR == kMxWarps) {
@@ -119,44 +127,57 @@ __global__ void __launch_bounds__(kMxWarps * 32)
     g_inv = nv_row_scale_inverse(g);
   }
   bool bad = false;
-  const int64_t scale_off = mx_scale_off(rows, K), row_off = mx_row_off(rows, K, FMT);
-  for (int64_t c = first; c < chunks; c += step * kMxBatch) {
+  constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;  // lanes per block
+  uint8_t* codes = pm + lane * 4;
+  uint8_t* scales = pm + mx_scale_off(rows, K) + (lane / (4 * L)) * 512;
+  auto code_row = [&](int64_t r) { return codes + r * (K / 2); };
+  auto scale_row = [&](int64_t r) {
+    return scales + (r / kMxRowTile) * chunks * mx_chunk_bytes(FMT) + mx_scale_slot(r);
+  };
+  uint8_t* own_codes = code_row(item);
+  uint8_t* own_scales = scale_row(item);
+  for (int c = first; c < chunks; c += step * kMxBatch) {
     Raw8<DT> raw[kMxBatch];
 #pragma unroll
     for (int u = 0; u < kMxBatch; ++u) {
-      const int64_t k = (c + u * step) * kMxChunk + lane * 8;
       raw[u] = Raw8<DT>{};
-      if (src >= 0 && k < K) raw[u] = load_raw8<DT>(xr, k);
+      if (src >= 0 && inside(c + u * step)) raw[u] = load(c + u * step);
     }
+    uint32_t q[kMxBatch], w[kMxBatch];
 #pragma unroll
     for (int u = 0; u < kMxBatch; ++u) {
-      const int64_t cu = c + u * step, k = cu * kMxChunk + lane * 8;
-      if (cu >= chunks) break;
-      uint32_t q = 0, s = 0;
-      if (src >= 0) {
-        q = mx_quantize8<FMT, DT>(raw[u], g, g_inv, &s, &bad);
-        if (k >= K) s = 0;
-      }
+      uint32_t s = 0;
+      q[u] = src >= 0 ? mx_quantize8<FMT, DT>(raw[u], g, g_inv, &s, &bad) : 0u;
+      // (zeros behind the row's end have the scale byte of zeros: 0)
       // four scales of a block are one 32-bit word
-      constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;  // lanes per block
-      uint32_t w = s << (8 * ((lane / L) & 3));
-      w |= __shfl_xor_sync(0xffffffffu, w, L);
-      w |= __shfl_xor_sync(0xffffffffu, w, 2 * L);
+      w[u] = s << (8 * ((lane / L) & 3));
+      w[u] |= __shfl_xor_sync(0xffffffffu, w[u], L);
+      w[u] |= __shfl_xor_sync(0xffffffffu, w[u], 2 * L);
+    }
+    auto store = [&](uint8_t* cr, uint8_t* sr) {
+#pragma unroll
+      for (int u = 0; u < kMxBatch; ++u) {
+        const int cu = c + u * step;
+        if (src >= 0 && inside(cu))
+          *reinterpret_cast<uint32_t*>(cr + int64_t(cu) * (kMxChunk / 2)) = q[u];
+        if ((lane & (4 * L - 1)) == 0 && cu < chunks)
+          *reinterpret_cast<uint32_t*>(sr + int64_t(cu) * mx_chunk_bytes(FMT)) = w[u];
+      }
+    };
+    if (!LISTED) {
+      store(own_codes, own_scales);
+    } else {
       for (int i = 0; i < copies; ++i) {
-        const int64_t r = listed ? to[item * copies + i] : item;
-        if (r < 0) continue;
-        if (src >= 0 && k < K) *reinterpret_cast<uint32_t*>(pm + r * (K / 2) + k / 2) = q;
-        if ((lane & (4 * L - 1)) == 0)
-          *reinterpret_cast<uint32_t*>(pm + scale_off +
-                                       ((r / kMxRowTile) * chunks + cu) * mx_chunk_bytes(FMT) +
-                                       mx_scale_slot(r) + (lane / (4 * L)) * 512) = w;
+        const int r = to[item * copies + i];
+        if (r >= 0) store(code_row(r), scale_row(r));
       }
     }
   }
   if (FMT == LUTQ_NVFP4 && src >= 0 && (WPR == 1 || warp == 0) && lane == 0) {
-    for (int i = 0; i < copies; ++i) {
-      const int64_t r = listed ? to[item * copies + i] : item;
-      if (r >= 0) reinterpret_cast<float*>(pm + row_off)[r] = g;
+    float* row_scales = reinterpret_cast<float*>(pm + mx_row_off(rows, K, FMT));
+    for (int i = 0; i < (LISTED ? copies : 1); ++i) {
+      const int64_t r = LISTED ? to[item * copies + i] : item;
+      if (r >= 0) row_scales[r] = g;
     }
   }
   if (bad) report(dev_status, LUTQ_ERR_NONFINITE);
@@ -203,25 +224,7 @@ __global__ void __launch_bounds__(kMxWarps * 32)
       e2m1_values8(q[u], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
-      if constexpr (DT == LUTQ_FP32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + base + k);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (DT == LUTQ_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + base + k) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      store8<DT>(out, base + k, v);
     }
   }
 }
@@ -272,29 +275,41 @@ static unsigned k_split(int64_t rows, int64_t K, int64_t batch, int num_sms) {
   return unsigned(std::max<int64_t>(1, std::min<int64_t>(want, mx_ceil(K, kMxChunk))));
 }
 
-template <int FMT, int DT>
-static cudaError_t launch_quantize_t(const void* x, int64_t batch, int64_t items, int64_t rows,
+template <int FMT, int DT, bool LISTED>
+static cudaError_t launch_quantize_l(const void* x, int64_t batch, int64_t items, int64_t rows,
                                      int64_t K, const int32_t* from, const int32_t* to,
                                      int copies, void* packed, int32_t* dev_status, int num_sms,
                                      cudaStream_t stream) {
-  // below one row for each of the warps that an eighth of the blocks hold, a
-  // block takes a row (a whole matrix too, but for the padding rows' zeros)
-  const bool shared_row = items <= int64_t(num_sms) * kMxWarps;
-  const int64_t padded = to != nullptr ? items : mx_ceil(rows, kMxRowTile) * kMxRowTile;
+  // few rows (fewer warps than eight blocks an SM have): a block takes a row
+  const bool shared_row = items <= int64_t(num_sms) * kMxWarps * (LISTED ? 8 : 1);
+  const int64_t padded = LISTED ? items : mx_ceil(rows, kMxRowTile) * kMxRowTile;
   const int64_t xs = rows * K, ps = mx_bytes(rows, K, FMT);
   uint8_t* out = static_cast<uint8_t*>(packed);
   if (shared_row) {
     // mxfp4 blocks along K as well, until every warp has a chunk or two
     const int64_t chunks = mx_ceil(K, kMxChunk);
     const unsigned gy = FMT == LUTQ_MXFP4 ? unsigned(mx_ceil(chunks, 2 * kMxWarps)) : 1u;
-    return launch_pdl(mx_quantize_kernel<FMT, DT, kMxWarps>,
+    return launch_pdl(mx_quantize_kernel<FMT, DT, kMxWarps, LISTED>,
                       dim3(unsigned(padded), gy, unsigned(batch)), dim3(kMxWarps * 32), 0, stream,
                       x, items, rows, K, from, to, copies, out, xs, ps, dev_status);
   }
-  return launch_pdl(mx_quantize_kernel<FMT, DT, 1>,
+  return launch_pdl(mx_quantize_kernel<FMT, DT, 1, LISTED>,
                     dim3(unsigned(mx_ceil(padded, kMxWarps)), 1u, unsigned(batch)),
                     dim3(kMxWarps * 32), 0, stream, x, items, rows, K, from, to, copies, out, xs,
                     ps, dev_status);
+}
+
+template <int FMT, int DT>
+static cudaError_t launch_quantize_t(const void* x, int64_t batch, int64_t items, int64_t rows,
+                                     int64_t K, const int32_t* from, const int32_t* to,
+                                     int copies, void* packed, int32_t* dev_status, int num_sms,
+                                     cudaStream_t stream) {
+  return to != nullptr ? launch_quantize_l<FMT, DT, true>(x, batch, items, rows, K, from, to,
+                                                          copies, packed, dev_status, num_sms,
+                                                          stream)
+                       : launch_quantize_l<FMT, DT, false>(x, batch, items, rows, K, from, to,
+                                                           copies, packed, dev_status, num_sms,
+                                                           stream);
 }
 
 // `items` source rows into a packed buffer of `rows` rows (see the kernel).
