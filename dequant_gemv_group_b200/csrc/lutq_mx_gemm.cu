@@ -511,7 +511,7 @@ cudaError_t make_mx_out_map(CUtensorMap* map, void* y, int64_t M, int64_t N, int
   const int es = dtype == LUTQ_FP32 ? 4 : 2;
   const cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(M)};
   const cuuint64_t strides[1] = {cuuint64_t(N * es)};
-  const cuuint32_t box[2] = {128, 32};
+  const cuuint32_t box[2] = {32, 32};
   return encode(map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
                 y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }

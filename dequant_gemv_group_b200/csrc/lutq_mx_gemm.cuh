@@ -55,7 +55,7 @@ cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64
 // Their scale chunks: rows of 1024 bytes, one or two a chunk.
 cudaError_t make_mx_scale_map(CUtensorMap* map, const void* packed, int64_t rows, int64_t K,
                               int64_t batch, int64_t stride, int fmt);
-// An output [M, N], in boxes of 128 columns x 32 rows.
+// An output [M, N], in boxes of 32 columns x 32 rows.
 cudaError_t make_mx_out_map(CUtensorMap* map, void* y, int64_t M, int64_t N, int dtype);
 
 // The kernel for many tokens (lutq_mx_pair.cu).

@@ -13,8 +13,9 @@
 // 64 (mxfp4) or 96 (nvfp4) columns: the epilogue empties those first, and the
 // next tile's MMAs run while it empties the others.
 //
-// Epilogue: eight warps, 32 columns (tokens) at a time through shared memory
-// and tensor-map stores, which also clip the tile to the output.
+// Epilogue: eight warps, each on its own: 32 rows by 32 columns (tokens) at a
+// time through shared memory and a tensor-map store, which also clips the tile
+// to the output.
 #include <algorithm>
 #include <cstring>
 
@@ -120,8 +121,20 @@ struct PairTiles {
   }
 };
 
+// One value, rounded to the output type, into shared memory.
+template <int DT>
+__device__ __forceinline__ void stage1(uint32_t saddr, float v) {
+  if constexpr (DT == LUTQ_FP32) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(saddr), "f"(v) : "memory");
+  } else {
+    const uint16_t h = DT == LUTQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
+                                       : __half_as_ushort(__float2half_rn(v));
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(saddr), "h"(h) : "memory");
+  }
+}
+
 template <int FMT, int MODE, int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a2,
                    const __grid_constant__ CUtensorMap tmap_b,
@@ -133,14 +146,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   using Cfg = PairCfg<FMT, MODE>;
   constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS;
   constexpr int ES = DT == LUTQ_FP32 ? 4 : 2;
-  constexpr int SLICE = 32 * 128 * ES;  // a staged slice of 32 tokens
+  constexpr int SLICE = 32 * 32 * ES;  // a staged slice: 32 tokens x a warp's 32 rows
   const MxGemmArgs& a = p.g;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int ST = a.stages;
-  uint8_t* staging = smem + ST * Cfg::STAGE;                       // [2 groups][2] slices
-  PairShared* sh = reinterpret_cast<PairShared*>(staging + 4 * SLICE);
+  uint8_t* staging = smem + ST * Cfg::STAGE;  // [8 warps][2] slices
+  PairShared* sh = reinterpret_cast<PairShared*>(staging + 16 * SLICE);
   int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);
   const uint32_t sbase = smem_addr(smem);
   // warp-uniform for the compiler, too
@@ -308,97 +321,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, group = (warp - 2) >> 2;  // four warps cover the 128 lanes
-    const bool leader = (warp - 2) % 4 == 0 && lane == 0;
-    uint8_t* stage0 = staging + group * 2 * SLICE;
+    uint8_t* stage0 = staging + (warp - 2) * 2 * SLICE;
     float* gbs = sh->row_scales[warp - 2];  // nvfp4: the row scales of this warp's tokens
     int n = 0, slot = 0;
     bool ok = true;
-    for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step, ++n) {
-      const int row0 = mt * 256 + int(rank) * 128;
-      const int row = row0 + quarter * 32 + lane;
+    // slices of 32 columns, this group's are column(n, 0), column(n, 1), ...:
+    // those that the next tile's sums share come first, the last ones of an
+    // even tile (columns SECOND..255) and the first ones of an odd tile.
+    // (With two sets the shared columns are the end of the second or the
+    // beginning of the first.)
+    constexpr int NS = Cfg::NT / 32, OWN = NS / 2;
+    auto column_of = [&](int tile, int i) {
+      const int sl = group + 2 * i;
+      return 32 * ((tile & 1) == 0 ? NS - 1 - sl : sl);
+    };
+    // nvfp4: a tile's row scales are fetched while the tile before is worked on
+    float ga[2] = {1.f, 1.f}, ga_next[2] = {1.f, 1.f}, gb_next[OWN];
+    auto fetch = [&](int tile) {
+      const int r = mt * 256 + int(rank) * 128 + quarter * 32 + lane;
+      const int64_t first_token = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      if (r < a.N) {
+#pragma unroll
+        for (int w = 0; w < ND; ++w)
+          ga_next[w] = *reinterpret_cast<const float*>(
+              reinterpret_cast<const uint8_t*>(a.a_rows[w]) + int64_t(expert) * a.a_stride +
+              int64_t(r) * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < OWN; ++i)
+        if (column_of(tile, i) < valid)
+          gb_next[i] = a.b_rows[first_token + column_of(tile, i) + lane];
+    };
+    bool more = tiles.at(first, &expert, &mt, &m0, &valid);
+    if (FMT == LUTQ_NVFP4 && more) fetch(0);
+    for (int64_t t = first; more; t += step, ++n) {
+      const int row = mt * 256 + int(rank) * 128 + quarter * 32 + lane;
+      const int tokens = valid;
       const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
       const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t((n & 1) * Cfg::SECOND);
-      // slices of 32 columns, this group's are order(group), order(group + 2),
-      // ...: those that the next tile's sums share come first, the last ones
-      // of an even tile (columns SECOND..255) and the first ones of an odd
-      // tile.  (With two sets the shared columns are the end of the second or
-      // the beginning of the first.)
-      constexpr int NS = Cfg::NT / 32, OWN = NS / 2;
-      auto column = [&](int i) {
-        const int sl = group + 2 * i;
-        return 32 * ((n & 1) == 0 ? NS - 1 - sl : sl);
-      };
-      float ga[2] = {1.f, 1.f};
+      auto column = [&](int i) { return column_of(n, i); };
       if (FMT == LUTQ_NVFP4) {
-        if (row < a.N) {
 #pragma unroll
-          for (int w = 0; w < ND; ++w)
-            ga[w] = *reinterpret_cast<const float*>(
-                reinterpret_cast<const uint8_t*>(a.a_rows[w]) + int64_t(expert) * a.a_stride +
-                int64_t(row) * 4);
-        }
+        for (int w = 0; w < ND; ++w) ga[w] = ga_next[w];
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < OWN; ++i)
-          if (column(i) < valid) gbs[32 * i + lane] = a.b_rows[token0 + column(i) + lane];
+        for (int i = 0; i < OWN; ++i) gbs[32 * i + lane] = gb_next[i];
         __syncwarp();
       }
+      more = tiles.at(t + step, &expert, &mt, &m0, &valid);  // the tile after this one
       ok = mbar_wait(smem_addr(&sh->acc_full), uint32_t(n) & 1u, abort, kPairWaitNs);
-      // the four warps of a group share the barriers below: they go on
-      // together or not at all
-      if (!group_all(1 + group, 128, ok)) break;
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
 
       // one slice: scale, round, stage, store
       auto finish = [&](int i, uint32_t (&v)[ND][32]) {
         const int c = column(i);
         uint8_t* stg = stage0 + slot * SLICE;
+        const uint32_t sta = smem_addr(stg) + lane * ES;
+        float4 s4[8];  // (all before the first store: it would order the loads)
+        if (FMT == LUTQ_NVFP4) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s4[q] = reinterpret_cast<const float4*>(gbs + 32 * i)[q];
+        }
         // the store that read this buffer last must be done
-        if (leader) bulk_wait_read<1>();
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-        const float4* gb = reinterpret_cast<const float4*>(gbs + 32 * i);
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float4 s4 = make_float4(1.f, 1.f, 1.f, 1.f);
-          if (FMT == LUTQ_NVFP4) s4 = gb[q];
-          const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int l = 0; l < 4; ++l) {
-            const int j = 4 * q + l;
-            float f = __uint_as_float(v[0][j]);
-            if (FMT == LUTQ_NVFP4) f = f * ga[0] * sc[l];
-            if (ND == 2) {
-              float u = __uint_as_float(v[ND - 1][j]);
-              if (FMT == LUTQ_NVFP4) u = u * ga[1] * sc[l];
-              f = pair_silu_mul(f, u);
-            }
-            store1<DT>(stg, j * 128 + quarter * 32 + lane, f);
+        for (int j = 0; j < 32; ++j) {
+          float f = __uint_as_float(v[0][j]), u = __uint_as_float(v[ND - 1][j]);
+          if (FMT == LUTQ_NVFP4) {
+            const float4 q4 = s4[j / 4];
+            const float gb = j % 4 == 0 ? q4.x : j % 4 == 1 ? q4.y : j % 4 == 2 ? q4.z : q4.w;
+            f = f * ga[0] * gb;
+            if (ND == 2) u = u * ga[1] * gb;
           }
+          if (ND == 2) f = pair_silu_mul(f, u);
+          stage1<DT>(sta + j * 32 * ES, f);
         }
         if (p.tma_store) {
           fence_async_shared();
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-          if (leader) {
-            tma_2d_s2g(&tmap_y, row0, int(token0) + c, smem_addr(stg));
+          __syncwarp();
+          if (lane == 0 && row < a.N) {
+            tma_2d_s2g(&tmap_y, row, int(token0) + c, smem_addr(stg));
             bulk_commit();
           }
         } else {
           // rows that no 16-byte copy can write: each warp its own lanes
           __syncwarp();
           if (row < a.N)
-            for (int j = 0; j < 32 && c + j < valid; ++j) {
+            for (int j = 0; j < 32 && c + j < tokens; ++j) {
               const int64_t at = (token0 + c + j) * a.N + row;
               if (ES == 4)
                 static_cast<uint32_t*>(a.y)[at] =
-                    reinterpret_cast<const uint32_t*>(stg)[j * 128 + quarter * 32 + lane];
+                    reinterpret_cast<const uint32_t*>(stg)[j * 32 + lane];
               else
                 static_cast<uint16_t*>(a.y)[at] =
-                    reinterpret_cast<const uint16_t*>(stg)[j * 128 + quarter * 32 + lane];
+                    reinterpret_cast<const uint16_t*>(stg)[j * 32 + lane];
             }
         }
         slot ^= 1;
       };
       auto load = [&](int i, uint32_t (&v)[ND][32]) {
-        if (column(i) < valid) {
+        if (column(i) < tokens) {
 #pragma unroll
           for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + column(i), v[w]);
         }
@@ -413,6 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), 0));
+      if (FMT == LUTQ_NVFP4 && more) fetch(n + 1);
 #pragma unroll
       for (int i = 0; i < OWN; i += 2) {
         if (i > 0) {
@@ -420,11 +445,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           load(i + 1, vb);
           tmem_wait_ld();
         }
-        if (column(i) < valid) finish(i, va);
-        if (column(i + 1) < valid) finish(i + 1, vb);
+        if (column(i) < tokens) finish(i, va);
+        if (column(i + 1) < tokens) finish(i + 1, vb);
       }
     }
-    if (leader) bulk_wait<0>();
+    if (lane == 0) bulk_wait<0>();
   }
 
   __syncwarp();
@@ -443,8 +468,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 template <int FMT, int MODE, int DT>
 static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, int num_sms, cudaStream_t stream) {
   using Cfg = PairCfg<FMT, MODE>;
-  constexpr int SLICE = 32 * 128 * (DT == LUTQ_FP32 ? 4 : 2);
-  const int fixed = 1024 + 4 * SLICE + int(sizeof(PairShared)) +
+  constexpr int SLICE = 32 * 32 * (DT == LUTQ_FP32 ? 4 : 2);
+  const int fixed = 1024 + 16 * SLICE + int(sizeof(PairShared)) +
                     (MODE != kMxPlain ? 8 * p.g.experts : 0);
   constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
   p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::STAGE);
