@@ -225,6 +225,26 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // nvfp4: the scale byte of a block with largest magnitude m (fp32 bits).
 template <int DT>
 __device__ __forceinline__ uint32_t nv_scale_byte(uint32_t m, float g_inv) {
@@ -241,8 +261,10 @@ __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, flo
                                               float g_inv) {
   if constexpr (FMT == LUTQ_MXFP4) {
     const float inv = e8m0_inverse(scale);
+    const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= inv;  // exact: a power of two
+    for (int j = 0; j < 8; j += 2)  // exact: a power of two
+      unpack2(mul2(pack2(v[j], v[j + 1]), inv2), v[j], v[j + 1]);
   } else {
     const float s = e4m3_value(scale);
     if (!(s > 0.f)) {
@@ -252,9 +274,19 @@ __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, flo
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], s * g);
     } else if (nv_one_step(g_inv)) {
-      const float m = rcp_approx(s) * g_inv;
+      // a quotient r and one correction by its remainder x - r (s g): exact
+      // where the quotient has few bits, as at a halfway point (the packed
+      // multiply-adds are cheaper than two integer operations of snap17).
+      // Computed as -(x / (s g)), so that a zero keeps its sign: the codes'
+      // signs are turned back together.
+      const float m = rcp_approx(s) * -g_inv, d = s * g;
+      const uint64_t m2 = pack2(m, m), d2 = pack2(d, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = snap17(v[j] * m);
+      for (int j = 0; j < 8; j += 2) {
+        const uint64_t x2 = pack2(v[j], v[j + 1]), r2 = mul2(x2, m2);
+        unpack2(fma2(fma2(r2, d2, x2), m2, r2), v[j], v[j + 1]);
+      }
+      return e2m1_x8(v) ^ 0x88888888u;
     } else {
       const float m = rcp_approx(s);
 #pragma unroll

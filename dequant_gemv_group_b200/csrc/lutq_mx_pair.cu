@@ -29,6 +29,7 @@ using namespace sm100;
 constexpr uint64_t kPairWaitNs = 2000000000ull;
 constexpr int kPairMaxStages = 8;
 constexpr int kPairThreads = 64 + 256;
+constexpr int kPairPrefetch = 10;     // chunks of weights brought to L2 ahead of the launch
 constexpr int kPairTokenGroup = 16;  // token tiles that share a pass over the weights
 
 template <int FMT, int MODE>
@@ -177,6 +178,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&sh->tmem), 512);
     tmem_relinquish_pair();
+  }
+  // While the work before this launch runs: the first chunks of the first tile
+  // into L2.  (A prefetch reads nothing into the kernel; what that work may
+  // still write, L2 has no stale copy of.)
+  if (MODE == kMxPlain && warp == 0 && elect_one()) {
+    const int64_t per_group = int64_t(kPairTokenGroup) * mx_ceil(a.N, 256);
+    if ((blockIdx.x >> 1) < per_group) {
+      const int width = min(kPairTokenGroup, p.token_tiles);
+      const int arow = int(blockIdx.x >> 1) / width * 256 + int(rank) * 128;
+      for (int c = 0; c < min(a.chunks, kPairPrefetch); ++c)
+        tma_3d_prefetch(&tmap_a, c * 128, arow, 0);
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -183,6 +183,92 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
   if (bad) report(dev_status, LUTQ_ERR_NONFINITE);
 }
 
+// nvfp4, many rows of up to 8192 values: a block takes a row at a time, holds
+// it in registers between the search for its maximum and the rounding, and
+// loads the next row meanwhile, so that every value is read once.
+template <int DT>
+__global__ void __launch_bounds__(kMxWarps * 32)
+    mx_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t K,
+                            uint8_t* __restrict__ packed, int32_t* dev_status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t row_max[2][kMxWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int64_t esize = DT == LUTQ_FP32 ? 4 : 2;
+  const int chunks = int(mx_ceil(K, kMxChunk));
+  const int64_t padded = mx_ceil(rows, kMxRowTile) * kMxRowTile;
+  const uint8_t* xl = static_cast<const uint8_t*>(x) + lane * 8 * esize;
+  uint8_t* codes = packed + lane * 4;
+  uint8_t* scales = packed + mx_scale_off(rows, K) + (lane / 8) * 512;
+  float* row_scales = reinterpret_cast<float*>(packed + mx_row_off(rows, K, LUTQ_NVFP4));
+  bool inside[kMxBatch];
+#pragma unroll
+  for (int u = 0; u < kMxBatch; ++u)
+    inside[u] = int64_t(warp + u * kMxWarps) * kMxChunk + lane * 8 < K;
+  auto load = [&](int64_t r, Raw8<DT> (&raw)[kMxBatch]) {
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      raw[u] = Raw8<DT>{};
+      if (r < rows && inside[u])
+        raw[u] = load_raw8<DT>(xl + r * K * esize, int64_t(warp + u * kMxWarps) * kMxChunk);
+    }
+  };
+  // rows in the order of their scales in the layout: the blocks that run at
+  // the same time write neighbouring words (row i's tile, then i mod 32 of
+  // its quarter (i / 32) mod 4)
+  auto row_of = [&](int64_t i) {
+    return i / kMxRowTile * kMxRowTile + (i & 3) * 32 + ((i & (kMxRowTile - 1)) >> 2);
+  };
+  bool bad = false;
+  Raw8<DT> next[kMxBatch];
+  if (blockIdx.x < padded) load(row_of(blockIdx.x), next);
+  int flip = 0;
+  for (int64_t i = blockIdx.x; i < padded; i += gridDim.x, flip ^= 1) {
+    const int64_t r = row_of(i);
+    Raw8<DT> raw[kMxBatch];
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) raw[u] = next[u];
+    if (i + gridDim.x < padded) load(row_of(i + gridDim.x), next);
+    uint32_t most = 0, m = 0;
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) most = max(most, max_raw8<DT>(raw[u]));
+    if (most >= raw_inf<DT>()) {  // leave out what is not finite
+      most = 0;
+#pragma unroll
+      for (int u = 0; u < kMxBatch; ++u) {
+        float v[8];
+        widen8<DT>(raw[u], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
+      }
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m, max_bits_f32<DT>(most)));
+    if (lane == 0) row_max[flip][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMxWarps; ++w) m = max(m, row_max[flip][w]);
+    const float g = nv_row_scale(m), g_inv = nv_row_scale_inverse(g);
+    uint8_t* cr = codes + r * (K / 2);
+    uint8_t* sr =
+        scales + (r / kMxRowTile) * chunks * mx_chunk_bytes(LUTQ_NVFP4) + mx_scale_slot(r);
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      const int c = warp + u * kMxWarps;
+      if (c >= chunks) break;
+      uint32_t s = 0;
+      const uint32_t q = mx_quantize8<LUTQ_NVFP4, DT>(raw[u], g, g_inv, &s, &bad);
+      uint32_t w = s << (8 * ((lane / 2) & 3));
+      w |= __shfl_xor_sync(0xffffffffu, w, 2);
+      w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      if (r < rows && inside[u]) *reinterpret_cast<uint32_t*>(cr + c * (kMxChunk / 2)) = q;
+      if ((lane & 7) == 0)
+        *reinterpret_cast<uint32_t*>(sr + int64_t(c) * mx_chunk_bytes(LUTQ_NVFP4)) = w;
+    }
+    if (threadIdx.x == 0 && r < rows) row_scales[r] = g;
+  }
+  if (bad) report(dev_status, LUTQ_ERR_NONFINITE);
+}
+
 // The values of 8 codes: (element * scale) * row scale, rounded once.
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kMxWarps * 32)
@@ -292,6 +378,11 @@ static cudaError_t launch_quantize_l(const void* x, int64_t batch, int64_t items
     return launch_pdl(mx_quantize_kernel<FMT, DT, kMxWarps, LISTED>,
                       dim3(unsigned(padded), gy, unsigned(batch)), dim3(kMxWarps * 32), 0, stream,
                       x, items, rows, K, from, to, copies, out, xs, ps, dev_status);
+  }
+  if constexpr (FMT == LUTQ_NVFP4 && !LISTED && DT != LUTQ_FP32) {
+    if (batch == 1 && K <= kMxWarps * kMxBatch * kMxChunk)
+      return launch_pdl(mx_quantize_rows_kernel<DT>, dim3(unsigned(num_sms) * 6),
+                        dim3(kMxWarps * 32), 0, stream, x, rows, K, out, dev_status);
   }
   return launch_pdl(mx_quantize_kernel<FMT, DT, 1, LISTED>,
                     dim3(unsigned(mx_ceil(padded, kMxWarps)), 1u, unsigned(batch)),

@@ -113,6 +113,14 @@ __device__ __forceinline__ void tma_3d_g2s(uint32_t dst, const void* tmap, int32
       : "memory");
 }
 
+// Bring a tensor-map box into L2 (reads nothing into the kernel).
+__device__ __forceinline__ void tma_3d_prefetch(const void* tmap, int32_t c0, int32_t c1,
+                                                int32_t c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(tmap),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // 2-D tensor-map copy shared -> global, in the thread's current bulk group;
 // elements outside the tensor are not written.
 __device__ __forceinline__ void tma_2d_s2g(const void* tmap, int32_t c0, int32_t c1,

@@ -63,7 +63,8 @@ def _bound(y, mag, k, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,k", [(1, 32), (9, 96), (128, 256), (130, 288), (33, 4096)])
+@pytest.mark.parametrize("n,k", [(1, 32), (9, 96), (128, 256), (130, 288), (33, 4096),
+                                 (1301, 352), (1290, 8192), (1250, 8256)])
 def test_quantize_bit_exact(lq, fmt, n, k):
     x = _x(n, k, seed=n + k)
     st = lq.new_status()
