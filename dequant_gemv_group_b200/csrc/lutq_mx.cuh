@@ -19,6 +19,8 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "lutq_common.cuh"
@@ -181,8 +183,8 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
     }
   }
 }
-// The largest magnitude as the type's own bits (16-bit types: two at a time,
-// by unsigned halfword maxima; infinities and NaN come out largest).
+// The largest magnitude as the type's own bits (16-bit types: two at a time, by
+// maxima that keep a NaN; its bits, like an infinity's, are the largest).
 template <int DT>
 __device__ __forceinline__ uint32_t max_raw8(const Raw8<DT>& r) {
   if constexpr (DT == LUTQ_FP32) {
@@ -191,8 +193,12 @@ __device__ __forceinline__ uint32_t max_raw8(const Raw8<DT>& r) {
     for (int j = 0; j < 8; ++j) m = max(m, r.w[j] & 0x7fffffffu);
     return m;
   } else {
-    uint32_t m = __vmaxu2(__vmaxu2(r.w[0] & 0x7fff7fffu, r.w[1] & 0x7fff7fffu),
-                          __vmaxu2(r.w[2] & 0x7fff7fffu, r.w[3] & 0x7fff7fffu));
+    using T2 = std::conditional_t<DT == LUTQ_BF16, __nv_bfloat162, __half2>;
+    T2 h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __habs2(*reinterpret_cast<const T2*>(&r.w[j]));
+    const T2 x = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&x) & 0x7fff7fffu;
     return max(m & 0xffffu, m >> 16);
   }
 }
