@@ -115,16 +115,31 @@ __global__ void __launch_bounds__(256)
   const int64_t d = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 8;
   if (d >= D) return;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int j = 0; j < top_k; ++j) {
-    const int64_t p = t * top_k + j;
-    const int64_t r = slot != nullptr ? slot[p] : uint32_t(ids[p]) < uint32_t(E) ? p : -1;
-    if (r < 0) continue;
-    const float w = weights[p];
-    float v[8];
-    widen8<PT>(load_raw8<PT>(out, r * D + d), v);
+  constexpr int U = 4;  // rows in flight
+  for (int j0 = 0; j0 < top_k; j0 += U) {
+    int64_t r[U];
+    float w[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += w * v[i];
+    for (int u = 0; u < U; ++u) {
+      const int64_t p = t * top_k + j0 + u;
+      r[u] = -1;
+      if (j0 + u < top_k) {
+        r[u] = slot != nullptr ? slot[p] : uint32_t(ids[p]) < uint32_t(E) ? p : -1;
+        w[u] = weights[p];
+      }
+    }
+    Raw8<PT> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r[u] >= 0) raw[u] = load_raw8<PT>(out, r[u] * D + d);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r[u] < 0) continue;
+      float v[8];
+      widen8<PT>(raw[u], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += w[u] * v[i];
+    }
   }
   store8<DT>(y, t * D + d, s);
 }

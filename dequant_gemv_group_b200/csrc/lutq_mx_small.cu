@@ -34,7 +34,9 @@ constexpr int kSmallStages = 12;
 constexpr int kSmallSlots = 64;
 constexpr int kSmallThreads = 320;
 constexpr int kSmallQuantWarp = 6;
-constexpr int kSmallEntry = 4;  // words of an entry of the expert list
+constexpr int kSmallEntry = 4;       // words of an entry of the expert list
+constexpr int32_t kNoExpert = 0x7fffffff;
+constexpr int kSmallLook = 128;
 
 template <int FMT, int MODE>
 struct SmallCfg {
@@ -52,7 +54,7 @@ struct SmallCfg {
   static_assert(COLS <= 256, "");
 };
 
-struct SmallShared {
+struct alignas(16) SmallShared {
   uint64_t full[kSmallStages], empty[kSmallStages];
   uint64_t bfull[kSmallSlots], bempty[kSmallSlots];
   uint64_t acc_full[2], acc_empty[2];
@@ -103,11 +105,14 @@ __global__ void __launch_bounds__(kSmallThreads)
   float* recv = reinterpret_cast<float*>(tokens + slots * Cfg::SLOT);
   SmallShared* sh = reinterpret_cast<SmallShared*>(reinterpret_cast<uint8_t*>(recv) +
                                                    (split > 1 ? Cfg::RECV : 0));
-  // experts: entries {expert, first place in the list, pairs, -}, the list, a
-  // counter for each expert
-  int32_t* entry = reinterpret_cast<int32_t*>(sh + 1);
-  int32_t* list = entry + kSmallEntry * p.pairs;
-  int32_t* cursor = list + p.pairs;
+  // experts: the ids; entries {expert, first place in the list, pairs, -}; the
+  // list; what makes the entries
+  const int padded = (p.pairs + 3) & ~3;
+  int32_t* ids = reinterpret_cast<int32_t*>(sh + 1);
+  int32_t* blocks = ids + padded;
+  int32_t* entry = blocks + padded;
+  int32_t* list = entry + kSmallEntry * padded;
+  int32_t* cursor = list + padded;
   const uint32_t sbase = smem_addr(smem);
   // warp-uniform for the compiler, too
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -143,8 +148,6 @@ __global__ void __launch_bounds__(kSmallThreads)
     tmem_alloc(smem_addr(&sh->tmem), Cfg::TMEM);
     tmem_relinquish();
   }
-  if (MODE != kMxPlain)
-    for (int e = threadIdx.x; e < a.experts; e += kSmallThreads) cursor[e] = 0;
   // The down product follows the gate and up product of the same call, which
   // waited for all work before it: the ids and the weights are there, and
   // only the hidden values must be waited for.
@@ -163,59 +166,130 @@ __global__ void __launch_bounds__(kSmallThreads)
     bulk_g2s(sf, a.a_scales[0] + off, CH, full(s));
     if (ND == 2) bulk_g2s(sf + CH, a.a_scales[1] + off, CH, full(s));
   };
+  if (MODE != kMxPlain) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < padded; i += kSmallThreads) {
+      const int id = i < p.pairs ? p.ids[i] : -1;
+      ids[i] = uint32_t(id) < uint32_t(a.experts) ? id : kNoExpert;
+      if (i >= p.pairs) blocks[i] = 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (split > 1) cluster_arrive_all();  // this block's barriers are set up
   if (MODE != kMxPlain) {
-    for (int i = threadIdx.x; i < p.pairs; i += kSmallThreads) {
-      const int id = p.ids[i];
-      if (uint32_t(id) < uint32_t(a.experts)) atomicAdd(&cursor[id], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // entries of the experts in use, and where their pairs begin
-      int place = 0, n = 0;
-      for (int e0 = 0; e0 < a.experts; e0 += 32) {
-        const int e = e0 + lane, c = e < a.experts ? cursor[e] : 0, k = (c + NT - 1) / NT;
-        int pc = c, pk = k;  // inclusive sums over the lanes
+    // The list of pairs by expert, in their order (the same in all blocks of a
+    // cluster).  Every block makes it before its first copy, so it is made in
+    // the quicker of two ways: few pairs, a thread finds its pair's place by
+    // looking at all others (8 pairs: 2 us quicker than the other way; 148: the
+    // same; 256: 2 us slower); more, counts by expert, a scan, and placing by
+    // warp matches.
+    if (p.pairs <= kSmallLook) {
+      auto look = [&](const int32_t* of, auto&& each) {
+#pragma unroll 1
+        for (int q = 0; q < padded; q += 4) {
+          const int4 d = *reinterpret_cast<const int4*>(of + q);
+          each(q, d.x);
+          each(q + 1, d.y);
+          each(q + 2, d.z);
+          each(q + 3, d.w);
+        }
+      };
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.pairs; i += kSmallThreads) {
+        const int id = ids[i];
+        int place = 0, before = 0, count = 0;
+        look(ids, [&](int q, int o) {
+          place += uint32_t(o) < uint32_t(id);
+          count += o == id;
+          before += o == id && q < i;
+        });
+        if (id == kNoExpert) {
+          blocks[i] = 0;
+          continue;
+        }
+        list[place + before] = i;
+        // the first pair of each 16 of an expert makes an entry, below
+        blocks[i] = before == 0 ? (count + NT - 1) / NT : 0;
+        if (before % NT == 0) {
+          const int left = count - before;
+          cursor[i] = ((place + before) << 8) | (left < NT ? left : NT);
+        }
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.pairs; i += kSmallThreads) {
+        const int id = ids[i];
+        int at = 0, before = 0, all = 0;
+#pragma unroll 1
+        for (int q = 0; q < padded; q += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(ids + q);
+          const int4 n = *reinterpret_cast<const int4*>(blocks + q);
+          at += (uint32_t(o.x) < uint32_t(id) ? n.x : 0) + (uint32_t(o.y) < uint32_t(id) ? n.y : 0) +
+                (uint32_t(o.z) < uint32_t(id) ? n.z : 0) + (uint32_t(o.w) < uint32_t(id) ? n.w : 0);
+          all += n.x + n.y + n.z + n.w;
+          before += (o.x == id && q < i) + (o.y == id && q + 1 < i) + (o.z == id && q + 2 < i) +
+                    (o.w == id && q + 3 < i);
+        }
+        if (i == 0) sh->entries = all;
+        if (id == kNoExpert || before % NT != 0) continue;
+        int32_t* en = entry + kSmallEntry * (at + before / NT);
+        en[0] = id;
+        en[1] = cursor[i] >> 8;
+        en[2] = cursor[i] & 255;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll 1
+      for (int e = threadIdx.x; e < a.experts; e += kSmallThreads) cursor[e] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.pairs; i += kSmallThreads)
+        if (ids[i] != kNoExpert) atomicAdd(&cursor[ids[i]], 1);
+      __syncthreads();
+      if (warp == 0) {
+        // entries of the experts in use, and where their pairs begin
+        int place = 0, n = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+          const int e = e0 + lane, c = e < a.experts ? cursor[e] : 0, k = (c + NT - 1) / NT;
+          int both = c | (k << 16);  // inclusive sums over the lanes
 #pragma unroll
-        for (int x = 1; x < 32; x *= 2) {
-          const int vc = __shfl_up_sync(0xffffffffu, pc, x);
-          const int vk = __shfl_up_sync(0xffffffffu, pk, x);
-          if (lane >= x) {
-            pc += vc;
-            pk += vk;
+          for (int x = 1; x < 32; x *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, both, x);
+            if (lane >= x) both += v;
           }
+          const int pc = both & 0xffff, pk = both >> 16;
+#pragma unroll 1
+          for (int i = 0; i < k; ++i) {
+            int32_t* en = entry + kSmallEntry * (n + pk - k + i);
+            en[0] = e;
+            en[1] = place + pc - c + i * NT;
+            en[2] = min(NT, c - i * NT);
+          }
+          if (e < a.experts) cursor[e] = place + pc - c;
+          both = __shfl_sync(0xffffffffu, both, 31);
+          place += both & 0xffff;
+          n += both >> 16;
         }
-        for (int i = 0; i < k; ++i) {
-          int32_t* en = entry + kSmallEntry * (n + pk - k + i);
-          en[0] = e;
-          en[1] = place + pc - c + i * NT;
-          en[2] = min(NT, c - i * NT);
-        }
-        if (e < a.experts) cursor[e] = place + pc - c;
-        place += __shfl_sync(0xffffffffu, pc, 31);
-        n += __shfl_sync(0xffffffffu, pk, 31);
-      }
-      if (lane == 0) sh->entries = n;
-    }
-    __syncthreads();
-    // in the order of the pairs: all blocks of a cluster must list them alike
-    if (warp == 0) {
-      for (int i0 = 0; i0 < p.pairs; i0 += 32) {
-        const int i = i0 + lane, id = i < p.pairs ? p.ids[i] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, id);
-        const bool in = uint32_t(id) < uint32_t(a.experts);
-        const int at = in ? cursor[id] : 0, before = __popc(same & ((1u << lane) - 1u));
+        if (lane == 0) sh->entries = n;
         __syncwarp();
-        if (in) {
-          list[at + before] = i;
-          if (before == 0) cursor[id] = at + __popc(same);
+#pragma unroll 1
+        for (int i0 = 0; i0 < p.pairs; i0 += 32) {
+          const int i = i0 + lane, id = i < p.pairs ? ids[i] : kNoExpert;
+          const uint32_t same = __match_any_sync(0xffffffffu, id);
+          const int at = id != kNoExpert ? cursor[id] : 0;
+          const int before = __popc(same & ((1u << lane) - 1u));
+          __syncwarp();
+          if (id != kNoExpert) {
+            list[at + before] = i;
+            if (before == 0) cursor[id] = at + __popc(same);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
@@ -591,7 +665,7 @@ static cudaError_t launch_one(const CUtensorMap* t, SmallArgs p, int64_t tiles, 
   const int clusters = int(std::max<int64_t>(
       1, std::min<int64_t>(tiles, int64_t(num_sms) * per_sm / p.split)));
   const int fixed = 1024 + (p.split > 1 ? Cfg::RECV : 0) + int(sizeof(SmallShared)) +
-                    (MODE != kMxPlain ? 4 * ((kSmallEntry + 1) * p.pairs + p.g.experts) : 0);
+                    (MODE != kMxPlain ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts) : 0);
   // the tokens' chunks, as far as four stages of weights leave room
   const int share = int(mx_ceil(chunks, p.split));
   p.slots = std::min(std::min(share, kSmallSlots),

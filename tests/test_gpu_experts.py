@@ -171,7 +171,7 @@ def test_uneven_skipped_and_repeated(lq, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("t,e", [(60, 40), (200, 40)])
+@pytest.mark.parametrize("t,e", [(60, 40), (100, 60), (200, 40)])
 def test_most_tokens_to_one_expert(lq, fmt, t, e):
     """Few tokens an expert on average, but one has more than a tile holds."""
     d, f = 160, 96
