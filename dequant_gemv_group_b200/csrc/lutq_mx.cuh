@@ -257,10 +257,6 @@ __device__ __forceinline__ uint32_t nv_scale_byte(uint32_t m, float g_inv) {
   const float t = __uint_as_float(m) * g_inv;
   return e4m3_byte(DT == LUTQ_FP32 ? t / 6.0f : snap17(t * (1.0f / 6.0f)));
 }
-// Multipliers that take x to x / (s g): the reciprocal of s > 0 times 1 / g,
-// which only passes fp32's range for rows below 2^-100 (then in two steps).
-__device__ __forceinline__ bool nv_one_step(float g_inv) { return g_inv < 0x1p110f; }
-
 // Eight values to their codes, s the block's scale (nvfp4) or unused.
 template <int FMT, int DT>
 __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, float g,
@@ -273,19 +269,23 @@ __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, flo
       unpack2(mul2(pack2(v[j], v[j + 1]), inv2), v[j], v[j + 1]);
   } else {
     const float s = e4m3_value(scale);
-    if (!(s > 0.f)) {
+    if constexpr (DT == LUTQ_FP32) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = copysignf(0.f, v[j]);
-    } else if constexpr (DT == LUTQ_FP32) {
+      for (int j = 0; j < 8; ++j) v[j] = s > 0.f ? __fdiv_rn(v[j], s * g) : copysignf(0.f, v[j]);
+    } else {
+      // rows below 2^-100: 1 / (s g) may pass fp32's range; both sides times 2^64
+      if (g_inv >= 0x1p110f) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], s * g);
-    } else if (nv_one_step(g_inv)) {
+        for (int j = 0; j < 8; ++j) v[j] *= 0x1p64f;
+        g *= 0x1p64f;
+        g_inv *= 0x1p-64f;
+      }
       // a quotient r and one correction by its remainder x - r (s g): exact
       // where the quotient has few bits, as at a halfway point (the packed
       // multiply-adds are cheaper than two integer operations of snap17).
       // Computed as -(x / (s g)), so that a zero keeps its sign: the codes'
-      // signs are turned back together.
-      const float m = rcp_approx(s) * -g_inv, d = s * g;
+      // signs are turned back together.  (s = 0: every quotient is a zero.)
+      const float m = s > 0.f ? rcp_approx(s) * -g_inv : -0.f, d = s * g;
       const uint64_t m2 = pack2(m, m), d2 = pack2(d, d);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -293,10 +293,6 @@ __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, flo
         unpack2(fma2(fma2(r2, d2, x2), m2, r2), v[j], v[j + 1]);
       }
       return e2m1_x8(v) ^ 0x88888888u;
-    } else {
-      const float m = rcp_approx(s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = snap17(v[j] * g_inv * m);
     }
   }
   return e2m1_x8(v);
@@ -314,6 +310,45 @@ __device__ __forceinline__ void store1(void* y, int64_t i, float v) {
   } else {
     static_cast<uint16_t*>(y)[i] = __half_as_ushort(__float2half_rn(v));
   }
+}
+
+// The largest finite magnitude of eight values, as fp32 bits.
+template <int DT>
+__device__ __noinline__ uint32_t finite_max8(const Raw8<DT> raw) {
+  float v[8];
+  widen8<DT>(raw, v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
+  return m;
+}
+
+// Quantize a lane's 8 of a warp's 256 values: lanes 4i..4i+3 hold a block of 32
+// (mxfp4), 2i..2i+1 one of 16 (nvfp4).  Returns the lane's codes; *word: the
+// scale bytes of the four neighbouring blocks that a word of the layout holds.
+template <int FMT, int DT>
+__device__ __forceinline__ uint32_t mx_quantize_lane(const Raw8<DT>& raw, float g, float g_inv,
+                                                     int lane, uint32_t* word, bool* bad) {
+  constexpr int L = FMT == LUTQ_MXFP4 ? 4 : 2;  // lanes per block
+  uint32_t m = max_raw8<DT>(raw);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (FMT == LUTQ_MXFP4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  uint32_t scale, codes = 0u;
+  if (m >= raw_inf<DT>()) {  // a NaN or infinity: the block's scale is NaN
+    *bad = true;
+    scale = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
+  } else {
+    m = max_bits_f32<DT>(m);
+    scale = FMT == LUTQ_MXFP4 ? e8m0_byte(m) : nv_scale_byte<DT>(m, g_inv);
+    float v[8];
+    widen8<DT>(raw, v);
+    codes = mx_codes8<FMT, DT>(v, scale, g, g_inv);
+  }
+  uint32_t w = scale << (8 * ((lane / L) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, L);
+  w |= __shfl_xor_sync(0xffffffffu, w, 2 * L);
+  *word = w;
+  return codes;
 }
 
 // Eight values rounded once to the output type, from element i (a multiple of

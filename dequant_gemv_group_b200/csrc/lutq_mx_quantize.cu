@@ -29,26 +29,6 @@ __device__ __forceinline__ int mx_scale_slot(int64_t r) {
   return int(r & 31) * 16 + int((r >> 5) & 3) * 4;
 }
 
-// Quantize one lane's 8 values; lanes 4i..4i+3 hold a block of 32 (mxfp4),
-// 2i..2i+1 one of 16 (nvfp4).  Returns the codes; *scale the block's byte.
-template <int FMT, int DT>
-__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<DT>& raw, float g, float g_inv,
-                                                 uint32_t* scale, bool* bad) {
-  uint32_t m = max_raw8<DT>(raw);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (FMT == LUTQ_MXFP4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (m >= raw_inf<DT>()) {  // a NaN or infinity: the block's scale is NaN
-    *bad = true;
-    *scale = FMT == LUTQ_MXFP4 ? 0xFFu : 0x7Fu;
-    return 0u;
-  }
-  m = max_bits_f32<DT>(m);
-  float v[8];
-  widen8<DT>(raw, v);
-  *scale = FMT == LUTQ_MXFP4 ? e8m0_byte(m) : nv_scale_byte<DT>(m, g_inv);
-  return mx_codes8<FMT, DT>(v, *scale, g, g_inv);
-}
-
 // WPR warps share a row.  Not LISTED: row r is source and destination row r,
 // and the zero padding below the last row of a tile is written too.  LISTED:
 // item r reads source row from[r] (or r, if from is null) and goes to the
@@ -108,10 +88,7 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
         most = 0;
 #pragma unroll
         for (int u = 0; u < 2 * kMxBatch; ++u) {
-          float v[8];
-          widen8<DT>(raw[u], v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
+          m = max(m, finite_max8<DT>(raw[u]));
         }
       }
       m = max(m, max_bits_f32<DT>(most));
@@ -146,13 +123,9 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
     uint32_t q[kMxBatch], w[kMxBatch];
 #pragma unroll
     for (int u = 0; u < kMxBatch; ++u) {
-      uint32_t s = 0;
-      q[u] = src >= 0 ? mx_quantize8<FMT, DT>(raw[u], g, g_inv, &s, &bad) : 0u;
       // (zeros behind the row's end have the scale byte of zeros: 0)
-      // four scales of a block are one 32-bit word
-      w[u] = s << (8 * ((lane / L) & 3));
-      w[u] |= __shfl_xor_sync(0xffffffffu, w[u], L);
-      w[u] |= __shfl_xor_sync(0xffffffffu, w[u], 2 * L);
+      q[u] = w[u] = 0u;
+      if (src >= 0) q[u] = mx_quantize_lane<FMT, DT>(raw[u], g, g_inv, lane, &w[u], &bad);
     }
     auto store = [&](uint8_t* cr, uint8_t* sr) {
 #pragma unroll
@@ -235,12 +208,7 @@ __global__ void __launch_bounds__(kMxWarps * 32)
     if (most >= raw_inf<DT>()) {  // leave out what is not finite
       most = 0;
 #pragma unroll
-      for (int u = 0; u < kMxBatch; ++u) {
-        float v[8];
-        widen8<DT>(raw[u], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]) < kInfBits ? abs_bits(v[j]) : 0u);
-      }
+      for (int u = 0; u < kMxBatch; ++u) m = max(m, finite_max8<DT>(raw[u]));
     }
     m = __reduce_max_sync(0xffffffffu, max(m, max_bits_f32<DT>(most)));
     if (lane == 0) row_max[flip][warp] = m;
@@ -255,11 +223,8 @@ __global__ void __launch_bounds__(kMxWarps * 32)
     for (int u = 0; u < kMxBatch; ++u) {
       const int c = warp + u * kMxWarps;
       if (c >= chunks) break;
-      uint32_t s = 0;
-      const uint32_t q = mx_quantize8<LUTQ_NVFP4, DT>(raw[u], g, g_inv, &s, &bad);
-      uint32_t w = s << (8 * ((lane / 2) & 3));
-      w |= __shfl_xor_sync(0xffffffffu, w, 2);
-      w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      uint32_t w;
+      const uint32_t q = mx_quantize_lane<LUTQ_NVFP4, DT>(raw[u], g, g_inv, lane, &w, &bad);
       if (r < rows && inside[u]) *reinterpret_cast<uint32_t*>(cr + c * (kMxChunk / 2)) = q;
       if ((lane & 7) == 0)
         *reinterpret_cast<uint32_t*>(sr + int64_t(c) * mx_chunk_bytes(LUTQ_NVFP4)) = w;

@@ -465,15 +465,7 @@ __global__ void __launch_bounds__(kSmallThreads)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t b = max_raw8<DT>(raw[j]);
-              if (b < raw_inf<DT>()) {
-                m = max(m, max_bits_f32<DT>(b));
-              } else {
-                float v[8];
-                widen8<DT>(raw[j], v);
-#pragma unroll
-                for (int l = 0; l < 8; ++l)
-                  m = max(m, abs_bits(v[l]) < kInfBits ? abs_bits(v[l]) : 0u);
-              }
+              m = max(m, b < raw_inf<DT>() ? max_bits_f32<DT>(b) : finite_max8<DT>(raw[j]));
             }
           }
           if (live && lead < per) atomicMax(&sh->my_max[pc][i], m);
