@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
     if (from != nullptr) src = from[item];
     if (src < 0) return;  // (the whole block, where its warps share the row)
   }
+  const int to_lane = LISTED && lane < copies ? to[item * copies + lane] : -1;
   const uint8_t* xr = static_cast<const uint8_t*>(x) +
                       (int64_t(blockIdx.z) * x_stride + src * K + lane * 8) * esize;
   uint8_t* pm = packed + int64_t(blockIdx.z) * packed_stride;
@@ -125,7 +126,8 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
     for (int u = 0; u < kMxBatch; ++u) {
       // (zeros behind the row's end have the scale byte of zeros: 0)
       q[u] = w[u] = 0u;
-      if (src >= 0) q[u] = mx_quantize_lane<FMT, DT>(raw[u], g, g_inv, lane, &w[u], &bad);
+      if (src >= 0 && c + u * step < chunks)
+        q[u] = mx_quantize_lane<FMT, DT>(raw[u], g, g_inv, lane, &w[u], &bad);
     }
     auto store = [&](uint8_t* cr, uint8_t* sr) {
 #pragma unroll
@@ -140,8 +142,9 @@ __global__ void __launch_bounds__(kMxWarps * 32, WPR == 1 && DT != LUTQ_FP32 ? 4
     if (!LISTED) {
       store(own_codes, own_scales);
     } else {
+#pragma unroll 1
       for (int i = 0; i < copies; ++i) {
-        const int r = to[item * copies + i];
+        const int r = i < 32 ? __shfl_sync(0xffffffffu, to_lane, i) : to[item * copies + i];
         if (r >= 0) store(code_row(r), scale_row(r));
       }
     }
@@ -332,7 +335,7 @@ static cudaError_t launch_quantize_l(const void* x, int64_t batch, int64_t items
                                      int copies, void* packed, int32_t* dev_status, int num_sms,
                                      cudaStream_t stream) {
   // few rows (fewer warps than eight blocks an SM have): a block takes a row
-  const bool shared_row = items <= int64_t(num_sms) * kMxWarps * (LISTED ? 8 : 1);
+  const bool shared_row = items <= int64_t(num_sms) * kMxWarps;
   const int64_t padded = LISTED ? items : mx_ceil(rows, kMxRowTile) * kMxRowTile;
   const int64_t xs = rows * K, ps = mx_bytes(rows, K, FMT);
   uint8_t* out = static_cast<uint8_t*>(packed);
