@@ -18,9 +18,13 @@
 namespace lutq {
 
 constexpr int kPlanThreads = 512;
-// Pairs an expert, at most, for the kernel of few tokens.  Measured (64 experts
-// of 4096 x 2048, 60 of 2048 x 1440): SMALL_PAIRS_FIGURES
-constexpr int64_t kSmallPairsMx = 8, kSmallPairsNv = 4;
+// Pairs an expert, at most, for the kernel of few tokens; beyond, tokens are
+// packed first (five launches).  Measured, kernel of few tokens / packed, us:
+//   mxfp4, 4096 x 2048: 8 experts, 32 tokens x 2 (8 pairs each) 37.0 / 37.7,
+//     48 tokens (12) 44.7 / 40.0; 64 experts, 32 tokens x 8 (4) 144 / 153;
+//   nvfp4 (a row's maximum first): 60 experts of 2048 x 1440, 37 tokens x 4
+//     (2.5) 66 / 74; 64 of 4096 x 2048, 32 tokens x 8 (4) 212 / 167.
+constexpr int64_t kSmallPairsMx = 8, kSmallPairsNv = 3;
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {

@@ -110,7 +110,7 @@ def _close(y, ref, slack):
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("t,e,k,d,f", [
-    (1, 4, 2, 256, 128), (1, 8, 8, 512, 96), (2, 3, 1, 64, 32), (5, 8, 2, 288, 160),
+    (1, 4, 2, 256, 128), (1, 8, 8, 512, 96), (1, 2, 1, 1056, 512), (4, 9, 8, 608, 160), (2, 3, 1, 64, 32), (5, 8, 2, 288, 160),
     (16, 16, 4, 512, 256), (17, 6, 3, 256, 320), (40, 8, 2, 384, 192), (130, 4, 4, 256, 256),
     (333, 5, 2, 544, 416), (700, 3, 1, 256, 544)])
 def test_layer(lq, fmt, t, e, k, d, f):
@@ -241,6 +241,22 @@ def test_graph_streams_and_dirty_workspace(lq):
                 got.append(layer.run(x, ids, w, workspace=sp))
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("t,k", [(1, 1), (3, 2), (20, 4)])
+def test_no_expert_at_all(lq, t, k):
+    """Tokens without any expert get zeros, in every kernel's sum."""
+    layer = Layer(lq, 6, 160, 64, "mxfp4")
+    x, _ = _inputs(t, 6, k, 160, seed=1)
+    w = torch.ones(t, k, device="cuda")
+    y = torch.full((t, 160), 7.0, dtype=torch.bfloat16, device="cuda")
+    layer.run(x, torch.full((t, k), -1, dtype=torch.int32, device="cuda"), w, y=y)
+    assert (y == 0).all()
+    ids = torch.full((t, k), 6, dtype=torch.int32, device="cuda")
+    ids[t - 1, k - 1] = 5
+    y.fill_(7.0)
+    layer.run(x, ids, w, y=y)
+    assert (y[:t - 1] == 0).all() and (y[t - 1] != 0).any()
 
 
 def test_empty(lq):
