@@ -6,10 +6,12 @@
 //
 // (token, choice) pairs are laid out by expert: expert e's rows begin at a
 // multiple of 128 (the height of a scale block) and keep the order of the
-// pairs.  Steps, each one launch: plan (rows of every expert), x quantized
-// into its rows, gate and up product with silu, hidden values quantized, down
-// product, weighted sum over a token's choices in their order.  Rows do not
-// depend on one another, so a token's result does not depend on its batch.
+// pairs.  Steps: plan (rows of every expert, two launches), x quantized into
+// its rows, gate and up product with silu, hidden values quantized (by that
+// product for many tokens in mxfp4, else a launch), down product, weighted sum
+// over a token's choices in their order.  Where an expert has a handful of
+// pairs: gate and up, down, sum, with the tokens quantized inside.  Rows do
+// not depend on one another.
 #include <algorithm>
 #include <cstring>
 
@@ -283,7 +285,9 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.K = D;
   a.chunks = int(mx_ceil(D, kMxChunk));
   a.mtiles = int(mx_ceil(F, 128));
+  const bool packed_h = wide && fmt == LUTQ_MXFP4;
   if (wide) {
+    if (packed_h) a.y = ws + s.hq;  // quantized by the product
     err = launch_mx_pair(a, gate, up, w1, ws + s.xq, cap, fmt, kMxGateUp,
                          (used + pairs / 128) * mx_ceil(F, 256), num_sms, stream);
   } else {
@@ -294,7 +298,8 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                          stream);
   }
   if (err != cudaSuccess) return err;
-  if ((err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, pairs, cap, F, fmt, p.slot, p.slot, 1,
+  if (!packed_h &&
+      (err = launch_mx_quantize(ws + s.h, LUTQ_BF16, 1, pairs, cap, F, fmt, p.slot, p.slot, 1,
                                 ws + s.hq, dev_status, num_sms, stream)) != cudaSuccess)
     return err;
 

@@ -13,6 +13,11 @@
 // 64 (mxfp4) or 96 (nvfp4) columns: the epilogue empties those first, and the
 // next tile's MMAs run while it empties the others.
 //
+// Gate and up: two sets of sums, and in mxfp4 the hidden values are quantized
+// from the staged slice (a warp's 32 rows are one block), so that they pass
+// through memory as 4-bit codes.  (nvfp4's row scale needs the whole row: those
+// are written as bf16 and quantized by a launch of their own.)
+//
 // Epilogue: eight warps, each on its own: 32 rows by 32 columns (tokens) at a
 // time through shared memory and a tensor-map store, which also clips the tile
 // to the output.
@@ -132,6 +137,44 @@ __device__ __forceinline__ void stage1(uint32_t saddr, float v) {
                                        : __half_as_ushort(__float2half_rn(v));
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(saddr), "h"(h) : "memory");
   }
+}
+
+// A slice of hidden values (bf16, 32 tokens x 32 rows in shared memory) to a
+// block of codes and its scale byte for each token: lane t takes token t of
+// the slice.  row: the tokens' first row in the packed buffer of a.M x a.N; n:
+// the first of the 32 columns.
+__device__ __forceinline__ bool pack_hidden(const MxGemmArgs& a, const uint8_t* slice, int64_t row,
+                                            int n, int lane) {
+  Raw8<LUTQ_BF16> raw[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    raw[j] = load_raw8<LUTQ_BF16>(slice, lane * 32 + 8 * j);
+    m = max(m, max_raw8<LUTQ_BF16>(raw[j]));
+  }
+  const bool bad = m >= raw_inf<LUTQ_BF16>();
+  const uint32_t scale = bad ? 0xFFu : e8m0_byte(max_bits_f32<LUTQ_BF16>(m));
+  uint8_t* packed = static_cast<uint8_t*>(a.y);
+  const int64_t r = row + lane;
+  if (n < a.N) {
+    uint32_t codes[4] = {0u, 0u, 0u, 0u};
+    if (!bad) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+        widen8<LUTQ_BF16>(raw[j], v);
+        codes[j] = mx_codes8<LUTQ_MXFP4, LUTQ_BF16>(v, scale, 1.f, 1.f);
+      }
+    }
+    *reinterpret_cast<uint4*>(packed + r * (a.N / 2) + n / 2) =
+        make_uint4(codes[0], codes[1], codes[2], codes[3]);
+  }
+  // (columns behind the last are zeros: scale byte 0, as the layout wants)
+  const int64_t chunk = (r / kMxRowTile) * mx_ceil(a.N, kMxChunk) + n / kMxChunk;
+  const int block = n / 32 % 8;
+  packed[mx_scale_off(a.M, a.N) + chunk * mx_chunk_bytes(LUTQ_MXFP4) + (block / 4) * 512 +
+         int(r & 31) * 16 + int((r >> 5) & 3) * 4 + (block & 3)] = uint8_t(scale);
+  return bad;
 }
 
 template <int FMT, int MODE, int DT>
@@ -337,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* stage0 = staging + (warp - 2) * 2 * SLICE;
     float* gbs = sh->row_scales[warp - 2];  // nvfp4: the row scales of this warp's tokens
     int n = 0, slot = 0;
-    bool ok = true;
+    bool ok = true, bad = false;
     // slices of 32 columns, this group's are column(n, 0), column(n, 1), ...:
     // those that the next tile's sums share come first, the last ones of an
     // even tile (columns SECOND..255) and the first ones of an odd tile.
@@ -411,7 +454,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (ND == 2) f = pair_silu_mul(f, u);
           stage1<DT>(sta + j * 32 * ES, f);
         }
-        if (p.tma_store) {
+        if (MODE == kMxGateUp && FMT == LUTQ_MXFP4) {
+          // straight into the down product's operand
+          __syncwarp();
+          const bool nan = pack_hidden(a, stg, token0 + c, row - lane, lane);
+          bad |= nan && c + lane < tokens;
+        } else if (p.tma_store) {
           fence_async_shared();
           __syncwarp();
           if (lane == 0 && row < a.N) {
@@ -463,6 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     if (lane == 0) bulk_wait<0>();
+    if (bad) report(a.dev_status, LUTQ_ERR_NONFINITE);
   }
 
   __syncwarp();
@@ -541,7 +590,8 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   p.g = g;
   p.token_tiles = int(mx_ceil(g.M, nt));
   p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms / 2)));
-  p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0;
+  p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0 &&
+                !(mode == kMxGateUp && fmt == LUTQ_MXFP4);  // (quantized instead)
   if (p.tma_store) {
     if ((err = make_mx_out_map(&m.y, g.y, g.M, g.N, dt)) != cudaSuccess) return err;
   }
