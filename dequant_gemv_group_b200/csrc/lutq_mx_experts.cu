@@ -28,6 +28,12 @@ constexpr int kPlanThreads = 512;
 //     (2.5) 66 / 74; 64 of 4096 x 2048, 32 tokens x 8 (4) 212 / 167.
 constexpr int64_t kSmallPairsMx = 8, kSmallPairsNv = 3;
 
+// More pairs an expert: block pairs (lutq_mx_pair.cu).  Measured, block pairs /
+// lutq_mx_gemm.cu, us, mxfp4: 8 experts of 4096 x 2048, 64 tokens x 2 (16
+// pairs each) 39.8 / 41.1, 120 tokens (30) 41.2 / 45.5, 32 (8) 39.6 / 37.8; 60 of
+// 2048 x 1440, 400 tokens x 4 (27) 85 / 88, 128 (9) 83 / 75.
+constexpr int64_t kWidePairs = 16;
+
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {
   int32_t* counts;  // [E] rows of an expert
@@ -243,7 +249,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   }
   // an expert has at most T rows, T top_k / E on average
   const int nt = mx_tile_tokens(T);
-  const bool wide = mx_ceil(pairs, E) > 32 && T > 64;
+  const bool wide = mx_ceil(pairs, E) > kWidePairs && T > 32;
   const int64_t w1 = mx_bytes(F, D, fmt), w2 = mx_bytes(D, F, fmt);
   const int64_t used = std::min<int64_t>(E, pairs);  // experts in use at most
   CUtensorMap maps[4];
@@ -308,7 +314,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.a_stride = w2;
   a.b_scales = ws + s.hq + mx_scale_off(cap, F);
   a.b_rows = reinterpret_cast<const float*>(ws + s.hq + mx_row_off(cap, F, fmt));
-  const bool bf16_rows = wide && dtype == LUTQ_BF16;
+  const bool bf16_rows = dtype == LUTQ_BF16 && T > 64 && mx_ceil(pairs, E) > 32;
   a.y = ws + s.out;
   a.y_dtype = bf16_rows ? LUTQ_BF16 : LUTQ_FP32;
   a.N = D;

@@ -1,22 +1,24 @@
-// Products of microscaled 4-bit matrices on the tensor cores (tcgen05.mma
-// with block scales): y[m, n] = sum_k x[m, k] w[n, k], both operands E2M1.
+// The experts' products of microscaled 4-bit matrices for a few to some dozen
+// tokens an expert: packed tokens, laid out by expert, with each expert's
+// weights (fewer tokens: lutq_mx_small.cu, more: lutq_mx_pair.cu).
 //
-// The tensor core multiplies the codes and applies both scales itself, so
-// nothing is dequantized: the kernel only moves bytes.  A tile is 128 rows of
-// the weight matrix (the lanes of tensor memory) by NT tokens (its columns);
-// taking the weights as the first operand keeps the tile narrow for small
-// batches, and a warp's 32 lanes are 32 neighbouring outputs of one token.
-// A stage is 256 elements of K: 128 bytes a row of each operand by tensor-map
-// copies with the 128-byte swizzle, the scale chunks by bulk copies, and per
-// stage four MMAs of 64 elements.  Scale blocks go from shared memory to
-// tensor memory with one copy instruction each, ordered before the MMAs.
+// The tensor core multiplies the codes and applies both scales itself
+// (tcgen05.mma with block scales), so nothing is dequantized: the kernel only
+// moves bytes, and is bound by the weights'.  A tile is 128 rows of a weight
+// matrix (the lanes of tensor memory) by NT tokens (its columns); taking the
+// weights as the first operand keeps the tile narrow for few tokens, and a
+// warp's 32 lanes are 32 neighbouring outputs of one token.  A stage is 256
+// elements of K: 128 bytes a row of each operand by tensor-map copies with the
+// 128-byte swizzle, the scale chunks by bulk copies, and per stage four MMAs of
+// 64 elements.  Scale blocks go from shared memory to tensor memory with one
+// copy instruction each, ordered before the MMAs.
 //
-// A cluster of `split` blocks shares a tile by K: block r takes chunks
-// [C r / split, C (r+1) / split), and each block sums its share of the columns
-// over the cluster through distributed shared memory, in rank order, so that
-// results do not depend on timing and no workspace is needed.
+// A cluster of `split` blocks shares a tile by K where tiles are few: block r
+// takes chunks [C r / split, C (r+1) / split), and each block adds up its share
+// of the columns over the cluster through distributed shared memory, in rank
+// order, so that results do not depend on timing and no workspace is needed.
 //
-// Warps: 0 copies, 1 issues, 2..5 read tensor memory and write y.
+// Warps: 0 copies, 1 issues, 2..5 read tensor memory and write.
 #include "lutq_mx_gemm.cuh"
 
 #include <algorithm>
@@ -39,7 +41,7 @@ struct MxCfg {
   static constexpr int BLOCKS = CH / 512;                  // scale blocks per chunk
   static constexpr int A_BYTES = 128 * 128, B_BYTES = NT * 128;
   static constexpr int STAGE = ND * A_BYTES + B_BYTES + (ND + 1) * CH;
-  static constexpr int RECV = ND * NT * 128 * 4;           // partial sums of a split tile
+  static constexpr int SUMS = ND * NT * 128 * 4;           // partial sums of a split tile
   // tensor memory: accumulators (two sets where they fit), then two sets of scales
   static constexpr int SF_COLS = 2 * (ND + 1) * BLOCKS * 4;
   static constexpr int ACC = 2 * ND * NT + SF_COLS <= 512 ? 2 : 1;
@@ -61,52 +63,33 @@ struct MxShared {
 // at the first column of a block: the MMA faults on others ("misaligned
 // address" with scales one column on).
 //
-// Walks the tiles t = first, first + step, ... of a launch: plain products go
-// over the row tiles first, experts' over each expert's tiles in turn.
-template <int MODE>
+// Walks the tiles t = first, first + step, ... of a launch, each expert's in turn.
 struct MxTiles {
   const int32_t* counts;
-  int mtiles, nt, experts, e = 0, e_tiles = 0;
-  int64_t e_first = 0, tokens;
+  int mtiles, nt, experts, e = 0, e_tiles;
+  int64_t e_first = 0;
   __device__ MxTiles(const MxGemmArgs& a, int nt_, const int32_t* counts_)
-      : counts(counts_), mtiles(a.mtiles), nt(nt_), experts(a.experts), tokens(a.M) {
-    if (MODE != kMxPlain) e_tiles = int(mx_ceil(counts[0], nt)) * mtiles;
-  }
+      : counts(counts_), mtiles(a.mtiles), nt(nt_), experts(a.experts),
+        e_tiles(int(mx_ceil(counts_[0], nt_)) * a.mtiles) {}
   // false: no tile t; else its expert, row tile, first token and tokens
   __device__ bool at(int64_t t, int* expert, int* mt, int* m0, int* valid) {
-    if constexpr (MODE == kMxPlain) {
-      const int64_t n = t / mtiles;
-      if (n * nt >= tokens) return false;
-      *expert = 0;
-      *mt = int(t - n * mtiles);
-      *m0 = int(n * nt);
-      *valid = int(min(int64_t(nt), tokens - n * nt));
-      return true;
-    } else {
-      while (t >= e_first + e_tiles) {
-        e_first += e_tiles;
-        if (++e >= experts) {
-          e = experts - 1;
-          e_tiles = 0;
-          return false;
-        }
-        e_tiles = int(mx_ceil(counts[e], nt)) * mtiles;
+    while (t >= e_first + e_tiles) {
+      e_first += e_tiles;
+      if (++e >= experts) {
+        e = experts - 1;
+        e_tiles = 0;
+        return false;
       }
-      const int i = int(t - e_first), n = i / mtiles;
-      *expert = e;
-      *mt = i - n * mtiles;
-      *m0 = n * nt;
-      *valid = min(nt, counts[e] - n * nt);
-      return true;
+      e_tiles = int(mx_ceil(counts[e], nt)) * mtiles;
     }
+    const int i = int(t - e_first), n = i / mtiles;
+    *expert = e;
+    *mt = i - n * mtiles;
+    *m0 = n * nt;
+    *valid = min(nt, counts[e] - n * nt);
+    return true;
   }
 };
-
-__device__ __forceinline__ void store_any(void* y, int dtype, int64_t i, float v) {
-  if (dtype == LUTQ_FP32) store1<LUTQ_FP32>(y, i, v);
-  else if (dtype == LUTQ_BF16) store1<LUTQ_BF16>(y, i, v);
-  else store1<LUTQ_FP16>(y, i, v);
-}
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g / (1.f + __expf(-g)) * u;
@@ -131,8 +114,8 @@ __global__ void __launch_bounds__(192)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int ST = a.stages;
-  float* recv = reinterpret_cast<float*>(smem + ST * Cfg::STAGE);
-  MxShared* sh = reinterpret_cast<MxShared*>(smem + ST * Cfg::STAGE + (split > 1 ? Cfg::RECV : 0));
+  float* sums = reinterpret_cast<float*>(smem + ST * Cfg::STAGE);
+  MxShared* sh = reinterpret_cast<MxShared*>(smem + ST * Cfg::STAGE + (split > 1 ? Cfg::SUMS : 0));
   int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);  // experts' row counts, then bases
   const uint32_t sbase = smem_addr(smem);
   // warp-uniform for the compiler, too
@@ -162,11 +145,9 @@ __global__ void __launch_bounds__(192)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (MODE != kMxPlain) {
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-      counts[e] = a.counts[e];
-      counts[a.experts + e] = a.bases[e];
-    }
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    counts[e] = a.counts[e];
+    counts[a.experts + e] = a.bases[e];
   }
   tc_fence_before();
   __syncthreads();
@@ -177,7 +158,7 @@ __global__ void __launch_bounds__(192)
   const int64_t first = blockIdx.x / split, step = gridDim.x / split;
   const int c0 = int(int64_t(a.chunks) * rank / split);
   const int c1 = int(int64_t(a.chunks) * (rank + 1) / split);
-  MxTiles<MODE> tiles(a, NT, counts);
+  MxTiles tiles(a, NT, counts);
   int expert, mt, m0, valid;
 
   if (warp == 0) {
@@ -187,7 +168,7 @@ __global__ void __launch_bounds__(192)
     int64_t issued = 0;
     bool ok = true;
     for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
-      const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const int row0 = counts[a.experts + expert] + m0;
       const int width = (valid + 15) / 16 * 16;  // columns: in boxes of 16 tokens
       const int64_t a_off = int64_t(expert) * a.a_stride + int64_t(mt) * a.chunks * CH;
       const uint8_t* as = a.a_scales[0] + a_off;
@@ -298,7 +279,7 @@ __global__ void __launch_bounds__(192)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int64_t row = int64_t(mt) * 128 + quarter * 32 + lane;
-      const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
+      const int64_t token0 = counts[a.experts + expert] + m0;
       const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(b * ND * NT);
       float ga[2] = {1.f, 1.f};
       if (FMT == LUTQ_NVFP4 && row < a.N) {
@@ -316,8 +297,8 @@ __global__ void __launch_bounds__(192)
         if (row >= a.N) return;
         const int64_t i = (token0 + m) * a.N + row;
         if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, i, silu_mul(v0, v1));
-        else if (MODE == kMxDown) store1<LUTQ_FP32>(a.y, i, v0);
-        else store_any(a.y, a.y_dtype, i, v0);
+        else if (a.y_dtype == LUTQ_BF16) store1<LUTQ_BF16>(a.y, i, v0);
+        else store1<LUTQ_FP32>(a.y, i, v0);
       };
       if (split == 1) {
 #pragma unroll
@@ -336,27 +317,22 @@ __global__ void __launch_bounds__(192)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[b]));
       } else {
-        // send every column to the block that sums it: recv[rank][w][column][lane]
+        // this block's sums into its own memory, [w][column][row], where the
+        // blocks that add up the columns fetch them
         ok = n == 0 || mbar_wait_cluster(smem_addr(&sh->part_empty), uint32_t(n - 1) & 1u, abort,
                                          kMxWaitNs);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t slot = smem_addr(recv) + (rank * ND * own * 128 + quarter * 32 + lane) * 4;
-#pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-          if (c >= valid) break;
+        float* mine = sums + quarter * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < valid; c += 16) {
           uint32_t v[ND][16];
 #pragma unroll
           for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x16(d + w * NT + c, v[w]);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const int col = c + j;
-            if (col < valid) {
-              const uint32_t to = cluster_map(slot, uint32_t(col / own));
 #pragma unroll
-              for (int w = 0; w < ND; ++w)
-                cluster_st_f32(to + (w * own + col % own) * 512, __uint_as_float(v[w][j]));
-            }
+            for (int w = 0; w < ND; ++w) mine[(w * NT + c + j) * 128] = __uint_as_float(v[w][j]);
           }
         }
         tc_fence_before();
@@ -365,15 +341,26 @@ __global__ void __launch_bounds__(192)
         if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_full), lane));
         ok = mbar_wait_cluster(smem_addr(&sh->part_full), uint32_t(n) & 1u, abort, kMxWaitNs);
         if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll 1
         for (int j = 0; j < own; ++j) {
           const int col = int(rank) * own + j;
           if (col >= valid) break;
-          float v[2] = {0.f, 0.f};
-          for (int r = 0; r < split; ++r)
+          float part[ND][8], sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < ND; ++w)
-              v[w] += recv[((r * ND + w) * own + j) * 128 + quarter * 32 + lane];
-          put(col, v[0], v[ND - 1]);
+          for (int q = 0; q < 8; ++q)
+            if (q < split) {
+#pragma unroll
+              for (int w = 0; w < ND; ++w)
+                part[w][q] = cluster_ld_f32(
+                    cluster_map(smem_addr(mine + (w * NT + col) * 128), uint32_t(q)));
+            }
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < split) {
+#pragma unroll
+              for (int w = 0; w < ND; ++w) sum[w] += part[w][q];
+            }
+          put(col, sum[0], sum[ND - 1]);
         }
         __syncwarp();
         if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_empty), lane));
@@ -409,8 +396,8 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int64_t tiles,
            &split);
   const int clusters =
       int(std::max<int64_t>(1, std::min<int64_t>(tiles, int64_t(num_sms) * (two ? 2 : 1) / split)));
-  const int fixed = 1024 + (split > 1 ? Cfg::RECV : 0) + int(sizeof(MxShared)) +
-                    (MODE != kMxPlain ? 8 * a.experts : 0);
+  const int fixed = 1024 + (split > 1 ? Cfg::SUMS : 0) + int(sizeof(MxShared)) +
+                    8 * a.experts;
   a.stages = std::min(kMxMaxStages, (budget - fixed) / Cfg::STAGE);
   if (a.stages < 2) return cudaErrorInvalidValue;
   const int smem = std::max(fixed + a.stages * Cfg::STAGE, mx_smem_floor(Cfg::TMEM));
@@ -454,9 +441,8 @@ static cudaError_t launch_nt(const CUtensorMap* t, const MxGemmArgs& a, int nt, 
 template <int FMT>
 static cudaError_t launch_mode(const CUtensorMap* t, const MxGemmArgs& a, int mode, int nt,
                                int64_t tiles, int num_sms, cudaStream_t stream) {
-  if (mode == kMxGateUp) return launch_nt<FMT, kMxGateUp>(t, a, nt, tiles, num_sms, stream);
-  if (mode == kMxDown) return launch_nt<FMT, kMxDown>(t, a, nt, tiles, num_sms, stream);
-  return launch_nt<FMT, kMxPlain>(t, a, nt, tiles, num_sms, stream);
+  return mode == kMxGateUp ? launch_nt<FMT, kMxGateUp>(t, a, nt, tiles, num_sms, stream)
+                           : launch_nt<FMT, kMxDown>(t, a, nt, tiles, num_sms, stream);
 }
 
 cudaError_t launch_mx_gemm(const CUtensorMap* t, const MxGemmArgs& a, int fmt, int mode, int nt,
@@ -528,8 +514,6 @@ cudaError_t make_mx_map(CUtensorMap* map, const void* codes, int64_t rows, int64
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-constexpr int64_t kPairMinTokens = 64;
-
 int mx_tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 // y[M, N] = x w^T.  x: the packed tokens, or (values) M <= 16 rows of values.
@@ -556,21 +540,8 @@ cudaError_t launch_mx_product(const void* x, int x_dtype, bool values, int64_t M
   a.b_scales = xp + mx_scale_off(M, K);
   a.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
   a.chunks = int(mx_ceil(K, kMxChunk));
-  const int64_t pair_tiles = mx_ceil(N, 256) * mx_ceil(M, 256);
-  if (M > kPairMinTokens && pair_tiles * 4 >= num_sms)
-    return launch_mx_pair(a, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain, pair_tiles,
-                          num_sms, stream);
-  const int nt = mx_tile_tokens(M);
-  a.mtiles = int(mx_ceil(N, 128));
-  CUtensorMap t[4];
-  std::memset(t, 0, sizeof(t));
-  cudaError_t err;
-  const int64_t xb = mx_bytes(M, K, fmt);
-  if ((err = make_mx_map(&t[0], w, N, K, 1, mx_bytes(N, K, fmt), 128)) != cudaSuccess) return err;
-  if ((err = make_mx_map(&t[2], xp, M, K, 1, xb, nt)) != cudaSuccess) return err;
-  if ((err = make_mx_map(&t[3], xp, M, K, 1, xb, 16)) != cudaSuccess) return err;
-  t[1] = t[0];
-  return launch_mx_gemm(t, a, fmt, kMxPlain, nt, a.mtiles * mx_ceil(M, nt), num_sms, stream);
+  return launch_mx_pair(a, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain,
+                        mx_ceil(N, 256) * mx_ceil(M, 256), num_sms, stream);
 }
 
 }  // namespace lutq

@@ -53,6 +53,7 @@ struct PairCfg {
 struct PairShared {
   uint64_t full[kPairMaxStages], empty[kPairMaxStages];
   uint64_t acc_full, acc_free, drain;
+  uint64_t part_full;  // split tiles
   uint32_t tmem;
   int abort;
   alignas(16) float row_scales[8][128];  // nvfp4: per epilogue warp, its tokens' of a tile
@@ -62,6 +63,7 @@ struct PairArgs {
   MxGemmArgs g;
   int token_tiles;    // plain: ceil(M / NT)
   int pairs;          // pairs of blocks in the launch
+  int split;          // pairs that share a tile by K
   int tma_store;      // y by tensor-map stores (row pitch a multiple of 16 bytes)
 };
 
@@ -177,8 +179,13 @@ __device__ __forceinline__ bool pack_hidden(const MxGemmArgs& a, const uint8_t* 
   return bad;
 }
 
-template <int FMT, int MODE, int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+// SPLIT (plain products with few tiles): the pairs of a cluster share one tile
+// by K, pair i taking chunks [C i / split, C (i+1) / split).  When a block's
+// part is summed, its stages are free: the sums go there, and the pair that
+// finishes a slice of 32 columns (slice s: pair s mod split) fetches and adds
+// them in the order of the pairs.
+template <int FMT, int MODE, int DT, bool SPLIT>
+__global__ void __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a2,
                    const __grid_constant__ CUtensorMap tmap_b,
@@ -202,7 +209,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t sbase = smem_addr(smem);
   // warp-uniform for the compiler, too
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  // place in the pair, the pair in its cluster, the pair's first block
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, leader = crank & ~1u;
+  const int split = SPLIT ? p.split : 1, part = SPLIT ? int(crank >> 1) : 0;
+  const int c0 = SPLIT ? a.chunks * part / split : 0;
+  const int c1 = SPLIT ? a.chunks * (part + 1) / split : a.chunks;
   volatile int* abort = &sh->abort;
   auto full = [&](int s) { return smem_addr(&sh->full[s]); };
   auto empty = [&](int s) { return smem_addr(&sh->empty[s]); };
@@ -215,6 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mbar_init(smem_addr(&sh->acc_full), 1);
     mbar_init(smem_addr(&sh->acc_free), 16);  // eight warps of both blocks
     mbar_init(smem_addr(&sh->drain), 1);
+    mbar_init(smem_addr(&sh->part_full), 8 * split);
     sh->abort = 0;
     mbar_fence_init();
   }
@@ -227,10 +239,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // still write, L2 has no stale copy of.)
   if (MODE == kMxPlain && warp == 0 && elect_one()) {
     const int64_t per_group = int64_t(kPairTokenGroup) * mx_ceil(a.N, 256);
-    if ((blockIdx.x >> 1) < per_group) {
+    const int tile = int(blockIdx.x >> 1) / split;
+    if (tile < per_group) {
       const int width = min(kPairTokenGroup, p.token_tiles);
-      const int arow = int(blockIdx.x >> 1) / width * 256 + int(rank) * 128;
-      for (int c = 0; c < min(a.chunks, kPairPrefetch); ++c)
+      const int arow = tile / width * 256 + int(rank) * 128;
+      for (int c = c0; c < min(c1, c0 + kPairPrefetch); ++c)
         tma_3d_prefetch(&tmap_a, c * 128, arow, 0);
     }
   }
@@ -247,8 +260,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
-  const int64_t first = blockIdx.x >> 1, step = p.pairs;
-  const uint32_t full0 = cluster_map(full(0), 0);  // the first block's barriers
+  const int64_t first = (blockIdx.x >> 1) / split, step = p.pairs / split;
+  const uint32_t full0 = cluster_map(full(0), leader);  // the pair's first block's barriers
   PairTiles<MODE> tiles(p, counts);
   int expert, mt, m0, valid;
 
@@ -268,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint32_t bytes = 2u * uint32_t(ND * (Cfg::A_BYTES + CH) + half * 128 + sb_tiles * CH);
       const int sa_row = (arow / 128) * a.chunks * (CH / 1024);
       const int sb_row = (row0 / kMxRowTile) * a.chunks * (CH / 1024);
-      for (int c = 0; c < a.chunks; ++c) {
+      for (int c = c0; c < c1; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kPairWaitNs);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const uint32_t st = sbase + s * Cfg::STAGE;
@@ -323,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int width = pair_width(valid), sb_tiles = width > kMxRowTile ? 2 : 1;
         const uint32_t idesc = idesc_e2m1(256, width, E8, 0);
         const uint32_t id2 = idesc_e2m1(0, 0, false, 2);  // the scale bytes 2 and 3
-        for (int c = 0; c < a.chunks; ++c, ++it) {
+        for (int c = c0; c < c1; ++c, ++it) {
           ok = mbar_wait(full(s), ph, abort, kPairWaitNs);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
@@ -353,9 +366,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 mma_e2m1_pair<!E8>(d + w * Cfg::NT, st + ((w * Cfg::A_BYTES) >> 4) + 2 * j,
                                    bl + 2 * j, E8 && (j & 1) ? idesc | id2 : idesc,
                                    sf_tmem + 4 * (w * BLOCKS + blk), sb_tmem + 8 * blk,
-                                   (c > 0 || j > 0) ? 1u : 0u);
+                                   (c > c0 || j > 0) ? 1u : 0u);
             }
-            mma_commit_pair(empty(s));
+            mma_commit_pair(empty(s), 3u << leader);
           }
           __syncwarp();
           any = true;
@@ -365,11 +378,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) mma_commit_pair(smem_addr(&sh->acc_full));
+        if (elect_one()) mma_commit_pair(smem_addr(&sh->acc_full), 3u << leader);
         __syncwarp();
       }
       if (__any_sync(0xffffffffu, *abort) && any) {
-        if (elect_one()) mma_commit_pair(smem_addr(&sh->drain));
+        if (elect_one()) mma_commit_pair(smem_addr(&sh->drain), 3u << leader);
         __syncwarp();
         pair_drain(smem_addr(&sh->drain), 0);
       }
@@ -430,14 +443,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
 
       // one slice: scale, round, stage, store
-      auto finish = [&](int i, uint32_t (&v)[ND][32]) {
-        const int c = column(i);
+      auto finish = [&](int c, const float* gbc, uint32_t (&v)[ND][32]) {
         uint8_t* stg = stage0 + slot * SLICE;
         const uint32_t sta = smem_addr(stg) + lane * ES;
         float4 s4[8];  // (all before the first store: it would order the loads)
         if (FMT == LUTQ_NVFP4) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) s4[q] = reinterpret_cast<const float4*>(gbs + 32 * i)[q];
+          for (int q = 0; q < 8; ++q) s4[q] = reinterpret_cast<const float4*>(gbc)[q];
         }
         // the store that read this buffer last must be done
         if (lane == 0) bulk_wait_read<1>();
@@ -488,6 +500,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + column(i), v[w]);
         }
       };
+      if constexpr (SPLIT) {
+        // (one tile a cluster) the sums into the block's stages, which hold
+        // nothing any more, [column][row]: the block of the same place in the
+        // pair that finishes a slice fetches it from there
+        float* mine = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+        uint32_t v[ND][32];
+#pragma unroll 1
+        for (int c = 32 * group; c < tokens; c += 64) {
+          tmem_ld_32x32b_x32(d + c, v[0]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mine[(c + j) * 128] = __uint_as_float(v[0][j]);
+        }
+        __syncwarp();
+        if (lane < split)
+          cluster_arrive(cluster_map(smem_addr(&sh->part_full), 2u * lane + rank));
+        ok = mbar_wait_cluster(smem_addr(&sh->part_full), 0, abort, kPairWaitNs);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+#pragma unroll 1
+        for (int k = group; 32 * (k * split + part) < tokens; k += 2) {
+          const int c = 32 * (k * split + part);
+          float sum[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < split; ++q) {
+            const uint32_t from = cluster_map(smem_addr(mine + c * 128), 2u * uint32_t(q) + rank);
+            float u[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] = cluster_ld_f32(from + j * 512);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[j] += u[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[0][j] = __float_as_uint(sum[j]);
+          if (FMT == LUTQ_NVFP4) {
+            __syncwarp();
+            gbs[lane] = a.b_rows[token0 + c + lane];
+            __syncwarp();
+          }
+          finish(c, gbs, v);
+        }
+        break;
+      }
       // two slices in registers; the shared columns are among the first two of
       // each group, so the next tile's MMAs wait for no more than these loads
       static_assert(Cfg::SHARED_COLS <= 128 && OWN >= 2, "");
@@ -497,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), 0));
+      if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), leader));
       if (FMT == LUTQ_NVFP4 && more) fetch(n + 1);
 #pragma unroll
       for (int i = 0; i < OWN; i += 2) {
@@ -506,8 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           load(i + 1, vb);
           tmem_wait_ld();
         }
-        if (column(i) < tokens) finish(i, va);
-        if (column(i + 1) < tokens) finish(i + 1, vb);
+        if (column(i) < tokens) finish(column(i), gbs + 32 * i, va);
+        if (column(i + 1) < tokens) finish(column(i + 1), gbs + 32 * (i + 1), vb);
       }
     }
     if (lane == 0) bulk_wait<0>();
@@ -527,15 +583,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-template <int FMT, int MODE, int DT>
-static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, int num_sms, cudaStream_t stream) {
+template <int FMT, int MODE, int DT, bool SPLIT>
+static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stream) {
   using Cfg = PairCfg<FMT, MODE>;
   constexpr int SLICE = 32 * 32 * (DT == LUTQ_FP32 ? 4 : 2);
+  constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
   const int fixed = 1024 + 16 * SLICE + int(sizeof(PairShared)) +
                     (MODE != kMxPlain ? 8 * p.g.experts : 0);
-  constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
   p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::STAGE);
-  auto kernel = mx_pair_kernel<FMT, MODE, DT>;
+  // a split tile's sums: up to 8 slices of 16 KB (split 2 or 4)
+  static_assert(!SPLIT || (smem - 1024 - 16 * SLICE - int(sizeof(PairShared))) / Cfg::STAGE *
+                                  Cfg::STAGE >= 8 * 32 * 128 * 4, "");
+  auto kernel = mx_pair_kernel<FMT, MODE, DT, SPLIT>;
   static bool granted[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -546,20 +605,38 @@ static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, int num_sms, cuda
     if (err != cudaSuccess) return err;
     granted[dev] = true;
   }
-  return launch_pdl(kernel, dim3(unsigned(2 * p.pairs)), dim3(kPairThreads), size_t(smem), stream,
-                    m.a[0], m.a[1], m.b, m.b16, m.sa[0], m.sa[1], m.sb, m.y, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * p.pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {unsigned(2 * p.split), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, m.a[0], m.a[1], m.b, m.b16, m.sa[0], m.sa[1], m.sb, m.y,
+                            p);
+}
+
+template <int FMT, int DT>
+static cudaError_t launch_plain(const MxPairMaps& m, const PairArgs& p, cudaStream_t stream) {
+  return p.split > 1 ? launch_one<FMT, kMxPlain, DT, true>(m, p, stream)
+                     : launch_one<FMT, kMxPlain, DT, false>(m, p, stream);
 }
 
 template <int FMT>
-static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode, int num_sms,
+static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode,
                               cudaStream_t stream) {
-  if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16>(m, p, num_sms, stream);
+  if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16, false>(m, p, stream);
   if (mode == kMxDown)
-    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16>(m, p, num_sms, stream)
-                                    : launch_one<FMT, kMxDown, LUTQ_FP32>(m, p, num_sms, stream);
-  if (p.g.y_dtype == LUTQ_BF16) return launch_one<FMT, kMxPlain, LUTQ_BF16>(m, p, num_sms, stream);
-  if (p.g.y_dtype == LUTQ_FP16) return launch_one<FMT, kMxPlain, LUTQ_FP16>(m, p, num_sms, stream);
-  return launch_one<FMT, kMxPlain, LUTQ_FP32>(m, p, num_sms, stream);
+    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16, false>(m, p, stream)
+                                    : launch_one<FMT, kMxDown, LUTQ_FP32, false>(m, p, stream);
+  if (p.g.y_dtype == LUTQ_BF16) return launch_plain<FMT, LUTQ_BF16>(m, p, stream);
+  if (p.g.y_dtype == LUTQ_FP16) return launch_plain<FMT, LUTQ_FP16>(m, p, stream);
+  return launch_plain<FMT, LUTQ_FP32>(m, p, stream);
 }
 
 cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void* weights2,
@@ -589,14 +666,24 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   PairArgs p = {};
   p.g = g;
   p.token_tiles = int(mx_ceil(g.M, nt));
-  p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms / 2)));
+  // Split a plain product's tiles by K while that gives idle pairs work and
+  // saves more chunks (0.3 us each) than the exchange costs (1.5 us for 32
+  // columns, 3 for 256; 4096 x 14336 at 512 tokens 23.6 -> 20.3 us, 512 x 14336
+  // at 128 tokens 22.6 -> 13.0).  Clusters of eight blocks that fill their
+  // multiprocessors leave many unused: sixteen of them ran in two waves.
+  const int slots = num_sms / 2;
+  const int per = tiles <= 16 && g.M <= 128 ? 8 : 12;
+  p.split = 1;
+  if (mode == kMxPlain && tiles <= 8 && g.chunks >= 4 * per) p.split = 4;
+  else if (mode == kMxPlain && tiles <= 32 && 2 * tiles <= slots && g.chunks >= 2 * per) p.split = 2;
+  p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / p.split))) * p.split;
   p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0 &&
                 !(mode == kMxGateUp && fmt == LUTQ_MXFP4);  // (quantized instead)
   if (p.tma_store) {
     if ((err = make_mx_out_map(&m.y, g.y, g.M, g.N, dt)) != cudaSuccess) return err;
   }
-  return fmt == LUTQ_MXFP4 ? launch_fmt<LUTQ_MXFP4>(m, p, mode, num_sms, stream)
-                           : launch_fmt<LUTQ_NVFP4>(m, p, mode, num_sms, stream);
+  return fmt == LUTQ_MXFP4 ? launch_fmt<LUTQ_MXFP4>(m, p, mode, stream)
+                           : launch_fmt<LUTQ_NVFP4>(m, p, mode, stream);
 }
 
 }  // namespace lutq

@@ -47,7 +47,7 @@ struct SmallCfg {
   static constexpr int STAGE = ND * (A_BYTES + CH);
   static constexpr int B_BYTES = kSmallNT * 128;
   static constexpr int SLOT = B_BYTES + CH;             // a chunk of the tokens
-  static constexpr int RECV = ND * kSmallNT * 128 * 4;  // partial sums of a split tile
+  static constexpr int SUMS = ND * kSmallNT * 128 * 4;  // partial sums of a split tile
   static constexpr int SF_COLS = (ND + 1) * BLOCKS * 4;
   static constexpr int COLS = 2 * ND * kSmallNT + 2 * SF_COLS;
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kSmallThreads)
                                              ~uintptr_t(1023));
   const int ST = a.stages, split = p.split, slots = p.slots;
   uint8_t* tokens = smem + ST * Cfg::STAGE;
-  float* recv = reinterpret_cast<float*>(tokens + slots * Cfg::SLOT);
-  SmallShared* sh = reinterpret_cast<SmallShared*>(reinterpret_cast<uint8_t*>(recv) +
-                                                   (split > 1 ? Cfg::RECV : 0));
+  float* sums = reinterpret_cast<float*>(tokens + slots * Cfg::SLOT);
+  SmallShared* sh = reinterpret_cast<SmallShared*>(reinterpret_cast<uint8_t*>(sums) +
+                                                   (split > 1 ? Cfg::SUMS : 0));
   // experts: the ids; entries {expert, first place in the list, pairs, -}; the
   // list; what makes the entries
   const int padded = (p.pairs + 3) & ~3;
@@ -592,18 +592,17 @@ __global__ void __launch_bounds__(kSmallThreads)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh->acc_empty[acc]));
         } else {
-          // send every column to the block that sums it: recv[rank][w][column][lane]
+          // this block's sums into its own memory, [w][column][row], where the
+          // blocks that add up the columns fetch them
           ok = n == 0 || mbar_wait_cluster(smem_addr(&sh->part_empty), uint32_t(n - 1) & 1u, abort,
                                            kSmallWaitNs);
           if (!__all_sync(0xffffffffu, ok)) break;
-          const uint32_t slot = smem_addr(recv) + (rank * ND * own * 128 + quarter * 32 + lane) * 4;
+          float* mine = sums + quarter * 32 + lane;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (j < r.valid) {
-              const uint32_t to = cluster_map(slot, uint32_t(j / own));
 #pragma unroll
-              for (int w = 0; w < ND; ++w)
-                cluster_st_f32(to + (w * own + j % own) * 512, __uint_as_float(v[w][j]));
+              for (int w = 0; w < ND; ++w) mine[(w * NT + j) * 128] = __uint_as_float(v[w][j]);
             }
           __syncwarp();
           if (lane < split) cluster_arrive(cluster_map(smem_addr(&sh->part_full), lane));
@@ -612,11 +611,21 @@ __global__ void __launch_bounds__(kSmallThreads)
           for (int j = 0; j < own; ++j) {
             const int col = int(rank) * own + j;
             if (col >= r.valid) break;
-            float sum[2] = {0.f, 0.f};
-            for (int q = 0; q < split; ++q)
+            float part[ND][8], sum[2] = {0.f, 0.f};
 #pragma unroll
-              for (int w = 0; w < ND; ++w)
-                sum[w] += recv[((q * ND + w) * own + j) * 128 + quarter * 32 + lane];
+            for (int q = 0; q < 8; ++q)
+              if (q < split) {
+#pragma unroll
+                for (int w = 0; w < ND; ++w)
+                  part[w][q] = cluster_ld_f32(
+                      cluster_map(smem_addr(mine + (w * NT + col) * 128), uint32_t(q)));
+              }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < split) {
+#pragma unroll
+                for (int w = 0; w < ND; ++w) sum[w] += part[w][q];
+              }
             put(col, sum[0], sum[ND - 1]);
           }
           __syncwarp();
@@ -656,7 +665,7 @@ static cudaError_t launch_one(const CUtensorMap* t, SmallArgs p, int64_t tiles, 
   mx_split(tiles, chunks, int64_t(num_sms) * per_sm, 8, &p.split);
   const int clusters = int(std::max<int64_t>(
       1, std::min<int64_t>(tiles, int64_t(num_sms) * per_sm / p.split)));
-  const int fixed = 1024 + (p.split > 1 ? Cfg::RECV : 0) + int(sizeof(SmallShared)) +
+  const int fixed = 1024 + (p.split > 1 ? Cfg::SUMS : 0) + int(sizeof(SmallShared)) +
                     (MODE != kMxPlain ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts) : 0);
   // the tokens' chunks, as far as four stages of weights leave room
   const int share = int(mx_ceil(chunks, p.split));

@@ -159,8 +159,12 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void cluster_st_f32(uint32_t caddr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
+// (Loads from another block's memory are in flight together; a warp's stores to
+// it leave one at a time, 0.1 us each, so sums are fetched, not sent.)
+__device__ __forceinline__ float cluster_ld_f32(uint32_t caddr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_st_u32(uint32_t caddr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
@@ -293,12 +297,13 @@ __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t d_tmem, uint32_t lo
       "r"(lo), "n"(kDescHiScales)
       : "memory");
 }
-// Arrive on `bar` in both blocks once this thread's tcgen05 work is done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// Arrive on `bar` in the blocks of `mask` (cluster ranks: both of the pair)
+// once this thread's tcgen05 work is done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(bar),
-      "h"(uint16_t(3))
+      "h"(uint16_t(mask))
       : "memory");
 }
 

@@ -176,6 +176,7 @@ SHAPES = [(1, 1, 32), (1, 128, 256), (2, 7, 96), (3, 256, 512), (8, 1000, 2048),
           (65, 96, 2080), (127, 257, 544), (128, 384, 4096), (129, 1024, 256), (200, 200, 3232),
           (300, 2049, 96), (513, 300, 1056),
           (1, 20000, 512), (4, 1024, 28672), (13, 64, 8224),
+          (40, 300, 14336), (250, 700, 14336), (290, 520, 8192), (70, 1030, 4128),
           # enough tiles for the kernel of block pairs: 1 and 2 token tiles, row pitches that no
           # 16-byte copy can write, tokens beyond one pass over the weights
           (77, 9601, 288), (160, 9480, 64), (300, 8200, 96), (600, 4096, 544), (1000, 2564, 1312),
@@ -198,7 +199,7 @@ def test_products(lq, fmt, m, n, k):
     assert torch.equal(yh, y.to(torch.float16))
     if m <= 16:
         z = lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt, status=st)
-        assert torch.equal(z, y)
+        assert (np.abs(_f64(z) - ref) <= _bound(ref, mag, k, torch.float32)).all()
         assert int(st.item()) == 0
 
 
@@ -208,8 +209,8 @@ def test_gemv_types(lq, fmt, dtype):
     m, n, k = 5, 200, 1120
     x = torch.randn(m, k, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(dtype)
     w = lq.lutq_mx_quantize(workloads.normal_weights(n, k, 0.02, seed=3).cuda(), fmt)
-    y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x.cuda(), fmt), m, w, n, k, fmt)
-    assert torch.equal(lq.lutq_mx_gemv(x.cuda(), w, n, k, fmt), y)
+    y = lq.lutq_mx_gemv(x.cuda(), w, n, k, fmt)
+    assert torch.equal(lq.lutq_mx_gemv(x.bfloat16().cuda(), w, n, k, fmt), y)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -281,8 +282,10 @@ def test_deterministic_and_in_bounds(lq, fmt):
         assert (buf[m * n:] == 7.0).all()
         for _ in range(3):
             assert torch.equal(lq.lutq_mx_gemm(xp, m, wp, n, k, fmt), y)
-            if m <= 16:
-                assert torch.equal(lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt), y)
+        if m <= 16:
+            z = lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt)
+            for _ in range(3):
+                assert torch.equal(lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt), z)
 
 
 def test_empty(lq):
@@ -301,6 +304,7 @@ def test_streams_and_graphs(lq, fmt):
     x, wp, _, _ = _case(lq, m, n, k, fmt, seed=6)
     x = x.cuda()
     want = lq.lutq_mx_gemv(x, wp, n, k, fmt)
+    both = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x, fmt), m, wp, n, k, fmt)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     got = []
@@ -310,7 +314,8 @@ def test_streams_and_graphs(lq, fmt):
                 got.append(lq.lutq_mx_gemv(x, wp, n, k, fmt))
                 got.append(lq.lutq_mx_gemm(lq.lutq_mx_quantize(x, fmt), m, wp, n, k, fmt))
     torch.cuda.synchronize()
-    assert all(torch.equal(g, want) for g in got)
+    assert all(torch.equal(g, want) for g in got[0::2])
+    assert all(torch.equal(g, both) for g in got[1::2])
     xin = torch.zeros_like(x)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -320,4 +325,4 @@ def test_streams_and_graphs(lq, fmt):
         xin.copy_(x * scale)
         graph.replay()
         torch.cuda.synchronize()
-        assert torch.equal(a, want * scale) and torch.equal(b, want * scale)
+        assert torch.equal(a, want * scale) and torch.equal(b, both * scale)
