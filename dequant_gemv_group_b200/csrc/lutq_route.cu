@@ -73,9 +73,10 @@ __device__ __forceinline__ float key_value32(uint32_t k) {
 }
 // Whether 32-bit scores tell the order of the exact ones.  `base` bounds the
 // error of p: sigmoid, 1 / (1 + e) with e off by (2 + 1.2 |z|) ulp and a
-// division by 2 ulp, in all below 4e-7; softmax, by the same with a sum and
-// two multiplications, below 1.2e-6.  `rel` times the score bounds that of the
-// addition of the bias and of a key's lost bits.
+// division by 2 ulp, in all below 4e-7; softmax, e off by 6 2^-24, a sum of P
+// and 5 additions, a division and a product, below (P + 20) 2^-24.  `rel`
+// times the score bounds that of the addition of the bias and of a key's lost
+// bits.
 struct Error32 {
   float base, rel;
 };
@@ -93,7 +94,7 @@ __device__ __forceinline__ int route_select32(const RouteArgs& a, const float (&
                                                float* cs, int lane, int* mine,
                                               bool* ordered) {
   const int E = a.E;
-  const float base = a.score == LUTQ_SCORE_SOFTMAX ? 1.2e-6f : 4e-7f;
+  const float base = a.score == LUTQ_SCORE_SOFTMAX ? float(P + 20) * 0x1p-24f : 4e-7f;
   const Error32 score_error = {base, float(P + 1) * 0x1p-23f};
   const Error32 group_error = {2.f * base, 0x1p-22f};
   float c[P], bias[P];
@@ -397,8 +398,9 @@ cudaError_t launch_route(const void* logits, int dtype, int64_t T, int E, const 
                          int score, int groups, int top_groups, int group_best, int top_k,
                          int renormalize, float scale, int32_t* ids, float* weights,
                          int32_t* dev_status, cudaStream_t stream) {
-  RouteArgs a = {logits, bias,  ids,    weights,    dev_status, T,     dtype, E,
-                 score,  groups, top_groups, group_best, top_k, renormalize, scale, E / groups, 0, 5};
+  RouteArgs a = {logits, bias,       ids,        weights, dev_status,  T,
+                 dtype,  E,          score,      groups,  top_groups,  group_best,
+                 top_k,  renormalize, scale,     E / groups, 0,        5};
   a.per_magic = uint32_t(mx_ceil(int64_t(1) << 20, a.per));
   while ((32 >> a.group_lanes) < groups) --a.group_lanes;
   cudaLaunchConfig_t cfg = {};

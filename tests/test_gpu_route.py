@@ -105,6 +105,9 @@ def test_near_ties_need_64_bits(lq):
 def test_close_calls(lq, score, gap):
     """Logits, biases and group sums about as far apart as 32-bit scores can tell, and closer."""
     g = torch.Generator().manual_seed(int(1 / gap))
+    z = torch.randn(40, 16, generator=g).repeat_interleave(64, 1)
+    z = z + gap * torch.randint(-3, 4, (40, 1024), generator=g)
+    _check(lq, z, 20, bias=(gap * torch.randint(-2, 3, (1024,), generator=g)).float(), score=score)
     base = torch.randn(200, 8, generator=g).repeat_interleave(8, 1)
     z = base + gap * torch.randint(-3, 4, (200, 64), generator=g)
     bias = (gap * torch.randint(-2, 3, (64,), generator=g)).float()
