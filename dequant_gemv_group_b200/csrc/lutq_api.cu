@@ -649,8 +649,10 @@ lutq_status lutq_route(const void* logits, int dtype, int64_t T, int E, const fl
 }
 
 static bool experts_shape_ok(int64_t T, int top_k, int E, int64_t D, int64_t F) {
+  // (tile numbers within an expert's part are 32-bit)
   return T >= 0 && top_k >= 1 && top_k <= 64 && E >= 1 && E <= 1024 && mx_shape_ok(D, D) &&
-         mx_shape_ok(F, F) && T <= (int64_t(1) << 24) && T * top_k <= (int64_t(1) << 24);
+         mx_shape_ok(F, F) && D <= (1 << 20) && F <= (1 << 20) && T <= (int64_t(1) << 24) &&
+         T * top_k <= (int64_t(1) << 24);
 }
 
 int64_t lutq_mx_experts_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F,

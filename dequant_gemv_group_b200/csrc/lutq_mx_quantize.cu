@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kMxWarps * 32)
         if (r < rows && h < groups)
           w |= uint32_t(scales[(z * rows + r) * groups + h]) << (8 * j);
       }
+      if (FMT == LUTQ_NVFP4) w &= 0x7f7f7f7fu;  // magnitudes: the tensor core's scales are unsigned
       *reinterpret_cast<uint32_t*>(sc + c * mx_chunk_bytes(FMT) + lane * 512) = w;
     }
   }
@@ -342,7 +343,8 @@ static cudaError_t launch_quantize_l(const void* x, int64_t batch, int64_t items
   if (shared_row) {
     // mxfp4 blocks along K as well, until every warp has a chunk or two
     const int64_t chunks = mx_ceil(K, kMxChunk);
-    const unsigned gy = FMT == LUTQ_MXFP4 ? unsigned(mx_ceil(chunks, 2 * kMxWarps)) : 1u;
+    const unsigned gy =
+        FMT == LUTQ_MXFP4 ? unsigned(std::min<int64_t>(mx_ceil(chunks, 2 * kMxWarps), 65535)) : 1u;
     return launch_pdl(mx_quantize_kernel<FMT, DT, kMxWarps, LISTED>,
                       dim3(unsigned(padded), gy, unsigned(batch)), dim3(kMxWarps * 32), 0, stream,
                       x, items, rows, K, from, to, copies, out, xs, ps, dev_status);

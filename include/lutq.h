@@ -583,7 +583,7 @@ lutq_status lutq_gemm_typed(const void* x_bf16, int64_t M, const void* packed,
  * 3, 4, 6 and their negatives; code = sign << 3 | index).  A block of
  * consecutive elements along K shares a scale byte:
  *   LUTQ_MXFP4  blocks of 32, E8M0: s = 2^(byte - 127), 0xFF = NaN;
- *   LUTQ_NVFP4  blocks of 16, E4M3, and one fp32 scale g per row.
+ *   LUTQ_NVFP4  blocks of 16, E4M3 without a sign, and one fp32 scale g per row.
  * The value of an element is level * s (* g).
  *
  * Quantization of a block with largest magnitude m:
@@ -622,7 +622,8 @@ int64_t lutq_mx_packed_bytes(int64_t N, int64_t K, int format);
  *   their range).
  * lutq_mx_pack - codes uint8 [batch, N, K/2] (two a byte, element 2i low) and
  *   scale bytes uint8 [batch, N, K/32 or K/16] (and row_scales fp32
- *   [batch, N] for LUTQ_NVFP4, or NULL for 1) into packed matrices.
+ *   [batch, N] for LUTQ_NVFP4, or NULL for 1) into packed matrices; the sign
+ *   bit of an E4M3 byte is dropped.
  * All pointers are device memory, 16-byte aligned; asynchronous on `stream`.
  * batch = 0 or N = 0 does nothing.  LUTQ_ERR_SHAPE: K % 32 != 0, K < 32, or a
  * size out of range (batch above 65535).
@@ -668,8 +669,8 @@ lutq_status lutq_mx_gemv(const void* x, int x_dtype, int64_t M, const void* pack
  * Ties go to the lowest expert (group).  An expert whose logit is -infinity is
  * not available: it does not count in a group's score, comes after all
  * others, lowest first, and its weight is 0 (so a row of -infinity gives
- * experts 0..top_k-1 with weights 0).  A NaN logit counts as -infinity, +infinity as the
- * limit; both report LUTQ_ERR_NONFINITE.
+ * experts 0..top_k-1 with weights 0).  A NaN logit counts as -infinity,
+ * +infinity as the limit; both report LUTQ_ERR_NONFINITE.
  *
  * logits  device [T, E] of `dtype`; bias device fp32 [E] or NULL.
  * ids     device int32 [T, top_k]; weights device fp32 [T, top_k], written.
@@ -700,9 +701,9 @@ lutq_status lutq_route(const void* logits, int dtype, int64_t T, int E, const fl
  * gate, up  device, E packed matrices [F, D]; down: E packed matrices [D, F].
  * workspace device, lutq_mx_experts_workspace_bytes(...) bytes, any contents;
  *         calls that may run at the same time must not share one.
- * T = 0 does nothing.  LUTQ_ERR_SHAPE unless D % 32 == 0, F % 32 == 0,
- * 1 <= E <= 1024, 1 <= top_k <= 64 and T * top_k <= 2^24; ids and weights
- * 4-byte aligned; other errors and dev_status as lutq_mx_gemv
+ * T = 0 does nothing.  LUTQ_ERR_SHAPE unless D % 32 == 0, F % 32 == 0, both at
+ * most 2^20, 1 <= E <= 1024, 1 <= top_k <= 64 and T * top_k <= 2^24; ids and
+ * weights 4-byte aligned; other errors and dev_status as lutq_mx_gemv
  * (LUTQ_ERR_NONFINITE also for hidden values beyond bf16).
  */
 int64_t lutq_mx_experts_workspace_bytes(int64_t T, int top_k, int E, int64_t D, int64_t F,

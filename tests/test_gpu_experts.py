@@ -206,6 +206,70 @@ def test_nonfinite_token_stays_alone(lq):
     assert torch.equal(y[keep], want[keep])
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("t", [1, 12, 40, 300])
+def test_every_size_with_streams_and_graphs(lq, fmt, t):
+    """Few pairs an expert, some, many: a workspace of NaN bytes, two streams at once, a captured
+    call replayed on new inputs.  Always the same bits."""
+    e, k, d, f = 5, 2, 512, 288
+    layer = Layer(lq, e, d, f, fmt, seed=22)
+    nb = lq.lutq_mx_experts_workspace_bytes(t, k, e, d, f, fmt)
+    sets = []
+    for seed in (23, 24):
+        x, z = _inputs(t, e, k, d, seed=seed)
+        ids, w = lq.lutq_route(z, k)
+        sets.append((x, ids, w, layer.run(x, ids, w)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.full((nb,), 255, dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for s, sp, (x, ids, w, want) in zip(streams, spaces, sets):
+            with torch.cuda.stream(s):
+                got.append((layer.run(x, ids, w, workspace=sp), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y, want in got)
+    x, ids, w = (v.clone() for v in sets[0][:3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.run(x, ids, w, workspace=spaces[0])
+    for x2, ids2, w2, want in sets[::-1]:
+        x.copy_(x2)
+        ids.copy_(ids2)
+        w.copy_(w2)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_offsets_beyond_32_bits(lq, fmt):
+    """The last of 64 experts, 4.4 GB into its matrices, gives what the first one gives."""
+    e, d, f = 64, 16384, 8192
+    g = torch.Generator("cuda").manual_seed(2)
+    mats = []
+    for n, k in ((f, d), (f, d), (d, f)):
+        a, b = (lq.lutq_mx_quantize(torch.randn(n, k, device="cuda", generator=g).bfloat16()
+                                    * k ** -0.5, fmt) for _ in range(2))
+        m = a.repeat(e, 1)
+        m[0] = b
+        mats.append(m)
+    for t in (4, 600, 1100):
+        x = torch.randn(t, d, device="cuda", generator=g).bfloat16()
+        w = torch.rand(t, 1, device="cuda", generator=g)
+        ids = torch.zeros(t, 1, dtype=torch.int32, device="cuda")
+        y = lq.lutq_mx_experts(x, ids, w, *mats, f, fmt)
+        other = lq.lutq_mx_experts(x, ids + 1, w, *mats, f, fmt)
+        swap = torch.tensor([0, e - 1], device="cuda")
+        for m in mats:
+            m[swap] = m[swap.flip(0)]
+        assert torch.equal(lq.lutq_mx_experts(x, ids + (e - 1), w, *mats, f, fmt), y)
+        assert not torch.equal(y, other)
+        for m in mats:
+            m[swap] = m[swap.flip(0)]
+
+
 def test_graph_streams_and_dirty_workspace(lq):
     """route -> experts captured and replayed; the workspace's old contents (NaN bytes) do not
     matter; two streams with their own workspaces."""
@@ -257,6 +321,25 @@ def test_no_expert_at_all(lq, t, k):
     y.fill_(7.0)
     layer.run(x, ids, w, y=y)
     assert (y[:t - 1] == 0).all() and (y[t - 1] != 0).any()
+
+
+def test_refusals(lq):
+    layer = Layer(lq, 3, 64, 32, "mxfp4")
+    x, z = _inputs(4, 3, 2, 64, seed=1)
+    ids, w = lq.lutq_route(z, 2)
+    small = torch.empty(lq.lutq_mx_experts_workspace_bytes(4, 2, 3, 64, 32, "mxfp4") - 1,
+                        dtype=torch.uint8, device="cuda")
+    with pytest.raises(lq.LutqError) as e:
+        layer.run(x, ids, w, workspace=small)
+    assert e.value.status == 9
+    for bad in (lambda: layer.run(x, ids[:2], w[:2]), lambda: layer.run(x[:, :32].contiguous(), ids, w),
+                lambda: layer.run(x, ids, w[:, :1].contiguous())):
+        with pytest.raises(lq.LutqError):
+            bad()
+    with pytest.raises(ValueError):
+        layer.run(x, ids.long(), w)
+    with pytest.raises(ValueError):
+        layer.run(x, ids, w.double())
 
 
 def test_empty(lq):

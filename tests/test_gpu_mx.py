@@ -249,7 +249,7 @@ def test_one_hot(lq, fmt):
 
 
 def test_nvfp4_row_scales_from_a_checkpoint(lq):
-    """Row scales that are no powers of two, negative scale-free, and a NULL one."""
+    """Row scales that are no powers of two, and none."""
     n, k, m = 70, 256, 20
     g = torch.Generator().manual_seed(9)
     codes = torch.randint(0, 256, (n, k // 2), generator=g).to(torch.uint8)
@@ -269,6 +269,65 @@ def test_nvfp4_row_scales_from_a_checkpoint(lq):
         assert (np.abs(_f64(y) - ref) <= _bound(ref, mag, k, torch.float32)).all()
 
 
+def test_pack_drops_the_sign_of_e4m3(lq):
+    n, k = 5, 64
+    g = torch.Generator().manual_seed(3)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g).to(torch.uint8).cuda()
+    scales = torch.randint(0, 0x7f, (n, k // 16), generator=g).to(torch.uint8).cuda()
+    wp = lq.lutq_mx_pack(codes, scales, "nvfp4")
+    assert torch.equal(lq.lutq_mx_dequantize(lq.lutq_mx_pack(codes, scales | 0x80, "nvfp4"), n, k,
+                                             "nvfp4"),
+                       lq.lutq_mx_dequantize(wp, n, k, "nvfp4"))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_very_long_row(lq, fmt):
+    """More chunks than a grid has blocks in its second dimension."""
+    k, part = (1 << 28) + 64, 4096
+    w = torch.zeros(1, k, dtype=torch.bfloat16, device="cuda")
+    ends = workloads.normal_weights(1, 2 * part, 1.0, seed=8)
+    w[:, :part], w[:, k - part:] = ends[:, :part].cuda(), ends[:, part:].cuda()
+    back = lq.lutq_mx_dequantize(lq.lutq_mx_quantize(w, fmt), 1, k, fmt)
+    assert (back[:, part:k - part] == 0).all()
+    got = torch.cat([back[:, :part], back[:, k - part:]], 1)
+    want = O.values(*O.quantize(_f64(ends), fmt), fmt)
+    assert np.array_equal(_f64(got), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_beyond_32_bits(lq, fmt):
+    """The last rows of a matrix of 2.3 GB and the last outputs of 5.6 GB are what they are in
+    small ones."""
+    n, k, last = (1 << 20) + 100, 4096, 356
+    w = torch.randn(n, k, dtype=torch.bfloat16, device="cuda",
+                    generator=torch.Generator("cuda").manual_seed(1))
+    x = torch.randn(20, k, device="cuda").bfloat16()
+    wp = lq.lutq_mx_quantize(w, fmt)
+    tail = lq.lutq_mx_quantize(w[n - last:].contiguous(), fmt)
+    back = lq.lutq_mx_dequantize(wp, n, k, fmt)
+    assert torch.equal(back[n - last:], lq.lutq_mx_dequantize(tail, last, k, fmt))
+    del w, back
+    xp = lq.lutq_mx_quantize(x, fmt)
+    tv = _f64(lq.lutq_mx_dequantize(tail, last, k, fmt, dtype=torch.float32))
+    xv = _f64(lq.lutq_mx_dequantize(xp, 20, k, fmt, dtype=torch.float32))
+    ref, mag = O.product(xv, tv)
+    y = _f64(lq.lutq_mx_gemm(xp, 20, wp, n, k, fmt)[:, n - last:])
+    assert (np.abs(y - ref) <= _bound(ref, mag, k, torch.float32)).all()
+    y = _f64(lq.lutq_mx_gemv(x[:3].contiguous(), wp, n, k, fmt)[:, n - last:])
+    assert (np.abs(y - ref[:3]) <= _bound(ref[:3], mag[:3], k, torch.float32)).all()
+    del wp
+    m, n, k = 70000, 40008, 64
+    x = torch.randn(m, k, device="cuda").bfloat16()
+    w = torch.randn(n, k, device="cuda").bfloat16()
+    y = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x, fmt), m, lq.lutq_mx_quantize(w, fmt), n, k, fmt,
+                        dtype=torch.bfloat16)
+    # (one order of the sum whatever the tile: K is a single chunk)
+    z = lq.lutq_mx_gemm(lq.lutq_mx_quantize(x[m - 300:].contiguous(), fmt), 300,
+                        lq.lutq_mx_quantize(w[n - 500:].contiguous(), fmt), 500, k, fmt,
+                        dtype=torch.bfloat16)
+    assert torch.equal(y[m - 300:, n - 500:], z)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_deterministic_and_in_bounds(lq, fmt):
     """Twice the same bits; nothing behind y is written; garbage in the codes' padding and in the
@@ -286,6 +345,33 @@ def test_deterministic_and_in_bounds(lq, fmt):
             z = lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt)
             for _ in range(3):
                 assert torch.equal(lq.lutq_mx_gemv(x.cuda(), wp, n, k, fmt), z)
+
+
+def test_refusals(lq):
+    """What the binding refuses on a GPU: strides, shapes, sizes, alignment."""
+    x = torch.ones(4, 128, dtype=torch.bfloat16, device="cuda")
+    w = lq.lutq_mx_quantize(torch.ones(8, 128, dtype=torch.bfloat16, device="cuda"), "nvfp4")
+    with pytest.raises(ValueError):
+        lq.lutq_mx_quantize(x.t(), "mxfp4")
+    with pytest.raises(ValueError):
+        lq.lutq_mx_quantize(x.double(), "mxfp4")
+    with pytest.raises(ValueError):
+        lq.lutq_mx_gemv(x[:, ::2], w, 8, 64, "nvfp4")
+    for bad in (lambda: lq.lutq_mx_quantize(x[:, :48].contiguous(), "mxfp4"),
+                lambda: lq.lutq_mx_quantize(x[0], "mxfp4"),
+                lambda: lq.lutq_mx_gemv(x, w, 8, 96, "nvfp4"),
+                lambda: lq.lutq_mx_gemv(x, w, 9, 128, "nvfp4"),
+                lambda: lq.lutq_mx_gemv(x, w, 8, 128, "mxfp4"),
+                lambda: lq.lutq_mx_gemv(x.repeat(5, 1), w, 8, 128, "nvfp4"),
+                lambda: lq.lutq_mx_gemm(w, 9, w, 8, 128, "nvfp4"),
+                lambda: lq.lutq_mx_gemm(w, 8, w, 8, 128, "nvfp4", y=torch.empty(8, 9, device="cuda")),
+                lambda: lq.lutq_mx_dequantize(w, 8, 96, "nvfp4"),
+                lambda: lq.lutq_mx_gemv(torch.ones(513, dtype=torch.bfloat16, device="cuda")[1:]
+                                        .view(4, 128), w, 8, 128, "nvfp4")):
+        with pytest.raises(lq.LutqError):
+            bad()
+    with pytest.raises(ValueError):
+        lq.lutq_mx_gemm(w, 8, w, 8, 128, "nvfp4", dtype=torch.float64)
 
 
 def test_empty(lq):

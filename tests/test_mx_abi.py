@@ -105,7 +105,7 @@ def test_experts_arguments(lq):
     assert f(dt=4) == 1 and f(fmt=2) == 1
     assert f(space=None) == 9 and f(nb=need - 1) == 9
     for bad in (dict(t=-1), dict(k=0), dict(k=65), dict(e=0), dict(e=1025), dict(d=48),
-                dict(ff=16), dict(t=1 << 23, k=4)):
+                dict(ff=16), dict(t=1 << 23, k=4), dict(d=(1 << 20) + 32), dict(ff=1 << 21)):
         assert f(**bad) == 2, bad
         if "t" not in bad or bad["t"] > 0:
             a = dict(t=5, k=2, e=8, d=64, ff=32) | bad
