@@ -31,7 +31,9 @@ constexpr int kMxChunk = 256;     // elements of K per scale chunk (128 bytes of
 constexpr int kMxRowTile = 128;   // rows per scale block
 
 __host__ __device__ constexpr int mx_block(int fmt) { return fmt == LUTQ_MXFP4 ? 32 : 16; }
-__host__ __device__ constexpr int mx_chunk_bytes(int fmt) { return fmt == LUTQ_MXFP4 ? 1024 : 2048; }
+__host__ __device__ constexpr int mx_chunk_bytes(int fmt) {
+  return fmt == LUTQ_MXFP4 ? 1024 : 2048;
+}
 __host__ __device__ constexpr int64_t mx_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ constexpr int64_t mx_scale_off(int64_t rows, int64_t K) {
   return mx_ceil(rows * (K / 2), 128) * 128;
@@ -121,32 +123,6 @@ __device__ __forceinline__ float nv_row_scale_inverse(float g) {
 }
 
 constexpr uint32_t kInfBits = 0x7f800000u;
-
-// Eight consecutive values of a row as fp32 from global memory (16 bytes of
-// bf16 or fp16, 32 of fp32); the address is 16-byte aligned.
-template <int DT>
-__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
-  if constexpr (DT == LUTQ_FP32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == LUTQ_BF16) {
-        v[2 * j] = bf16_lo_to_f32(w[j]);
-        v[2 * j + 1] = bf16_hi_to_f32(w[j]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
-    }
-  }
-}
 
 // The same eight values as loaded: 16-bit pairs in four words, or fp32 in eight.
 template <int DT>

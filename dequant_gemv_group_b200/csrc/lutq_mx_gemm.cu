@@ -32,7 +32,6 @@ using namespace sm100;
 
 constexpr uint64_t kMxWaitNs = 2000000000ull;
 constexpr int kMxMaxStages = 8;
-constexpr int kMxMaxExperts = 1024;
 
 template <int FMT, int NT, int MODE>
 struct MxCfg {
@@ -297,7 +296,6 @@ __global__ void __launch_bounds__(192)
         if (row >= a.N) return;
         const int64_t i = (token0 + m) * a.N + row;
         if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, i, silu_mul(v0, v1));
-        else if (a.y_dtype == LUTQ_BF16) store1<LUTQ_BF16>(a.y, i, v0);
         else store1<LUTQ_FP32>(a.y, i, v0);
       };
       if (split == 1) {
@@ -371,7 +369,7 @@ __global__ void __launch_bounds__(192)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (split > 1) cluster_sync_all();  // no block leaves while another may write to it
+  if (split > 1) cluster_sync_all();  // no block leaves while another may fetch from it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM);

@@ -2,9 +2,9 @@
 // thread blocks (cta_group::2), tiles of 256 weight rows by up to 256 tokens.
 //
 // The arithmetic of lutq_mx_gemm.cu, laid out for a dense contraction.  Two
-// blocks on neighbouring multiprocessors issue one MMA of 256 rows: each loads its
-// own 128 weight rows and half of the tokens, so a 256 x 256 tile takes
-// 64 bytes a clock and multiprocessor from L2 at the tensor core's full rate (one
+// blocks on neighbouring multiprocessors issue one MMA of 256 rows: each loads
+// its own 128 weight rows and half of the tokens, so a 256 x 256 tile takes 64
+// bytes a clock and multiprocessor from L2 at the tensor core's full rate (one
 // block alone with 128 x 256 would take 96).  Scales of the tokens are loaded
 // by both blocks, which each need all of them in tensor memory.
 //
@@ -34,7 +34,7 @@ using namespace sm100;
 constexpr uint64_t kPairWaitNs = 2000000000ull;
 constexpr int kPairMaxStages = 8;
 constexpr int kPairThreads = 64 + 256;
-constexpr int kPairPrefetch = 10;     // chunks of weights brought to L2 ahead of the launch
+constexpr int kPairPrefetch = 10;    // chunks of weights brought to L2 ahead of the launch
 constexpr int kPairTokenGroup = 16;  // token tiles that share a pass over the weights
 
 template <int FMT, int MODE>
@@ -53,7 +53,7 @@ struct PairCfg {
 struct PairShared {
   uint64_t full[kPairMaxStages], empty[kPairMaxStages];
   uint64_t acc_full, acc_free, drain;
-  uint64_t part_full;  // split tiles
+  uint64_t part_full;                    // split tiles
   uint32_t tmem;
   int abort;
   alignas(16) float row_scales[8][128];  // nvfp4: per epilogue warp, its tokens' of a tile
@@ -82,9 +82,9 @@ __device__ __forceinline__ void pair_drain(uint32_t bar, uint32_t parity) {
 }
 
 // Tile t of a launch: token tiles vary fastest (in groups), so that a weight
-// tile is read from memory once per group and then from L2.
-// Tiles begin at multiples of 128 tokens (the height of a scale block), a last
-// one is as wide as its tokens need.
+// tile is read from memory once per group and then from L2.  Tiles begin at
+// multiples of 128 tokens (the height of a scale block), a last one is as wide
+// as its tokens need.
 template <int MODE>
 struct PairTiles {
   static constexpr int nt = MODE == kMxGateUp ? 128 : 256;
@@ -674,8 +674,8 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   const int slots = num_sms / 2;
   const int per = tiles <= 16 && g.M <= 128 ? 8 : 12;
   p.split = 1;
-  if (mode == kMxPlain && tiles <= 8 && g.chunks >= 4 * per) p.split = 4;
-  else if (mode == kMxPlain && tiles <= 32 && 2 * tiles <= slots && g.chunks >= 2 * per) p.split = 2;
+  if (mode == kMxPlain && tiles <= 32 && 2 * tiles <= slots && g.chunks >= 2 * per)
+    p.split = tiles <= 8 && g.chunks >= 4 * per ? 4 : 2;
   p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / p.split))) * p.split;
   p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0 &&
                 !(mode == kMxGateUp && fmt == LUTQ_MXFP4);  // (quantized instead)

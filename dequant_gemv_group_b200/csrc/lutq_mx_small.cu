@@ -9,9 +9,9 @@
 // values into codes and scale bytes in shared memory, in the order of the
 // tensor core's 128-byte swizzle; they are loaded a round ahead, and stay as
 // long as a block's tiles have the same tokens (a block takes neighbouring
-// tiles).  A cluster of `split` blocks shares a tile
-// by K, as in lutq_mx_gemm.cu; so neither a workspace nor another launch is
-// needed, and results do not depend on timing.
+// tiles).  A cluster of `split` blocks shares a tile by K, as in
+// lutq_mx_gemm.cu; so neither a workspace nor another launch is needed, and
+// results do not depend on timing.
 //
 // Experts: (token, choice) pairs p = t * top_k + j are listed by expert in
 // shared memory by every block for itself; a tile takes up to 16 pairs of an
@@ -89,7 +89,7 @@ __device__ __forceinline__ void wait_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// DT: the type of the values; OT: of a plain product's output.
+// DT: the type of the values.
 template <int FMT, int MODE, int DT>
 __global__ void __launch_bounds__(kSmallThreads)
     mx_small_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kSmallThreads)
         for (int q = 0; q < padded; q += 4) {
           const int4 o = *reinterpret_cast<const int4*>(ids + q);
           const int4 n = *reinterpret_cast<const int4*>(blocks + q);
-          at += (uint32_t(o.x) < uint32_t(id) ? n.x : 0) + (uint32_t(o.y) < uint32_t(id) ? n.y : 0) +
+          at += (uint32_t(o.x) < uint32_t(id) ? n.x : 0) +
+                (uint32_t(o.y) < uint32_t(id) ? n.y : 0) +
                 (uint32_t(o.z) < uint32_t(id) ? n.z : 0) + (uint32_t(o.w) < uint32_t(id) ? n.w : 0);
           all += n.x + n.y + n.z + n.w;
           before += (o.x == id && q < i) + (o.y == id && q + 1 < i) + (o.z == id && q + 2 < i) +
@@ -475,7 +476,8 @@ __global__ void __launch_bounds__(kSmallThreads)
             met = true;
             if (th < NT)
               for (int k = 0; k < split; ++k)
-                cluster_st_u32(cluster_map(smem_addr(&sh->row_max[rank][th]), k), sh->my_max[0][th]);
+                cluster_st_u32(cluster_map(smem_addr(&sh->row_max[rank][th]), k),
+                               sh->my_max[0][th]);
             __syncwarp();
             if (th < split) cluster_arrive(cluster_map(smem_addr(&sh->max_full), th));
             ok = mbar_wait_cluster(smem_addr(&sh->max_full), 0, abort, kSmallWaitNs);
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   if (MODE == kMxDown) wait_before();  // no thread is done before the work it follows
   tc_fence_before();
   __syncthreads();
-  if (split > 1) cluster_sync_all();  // no block leaves while another may write to it
+  if (split > 1) cluster_sync_all();  // no block leaves while another may fetch from it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM);
@@ -666,7 +668,9 @@ static cudaError_t launch_one(const CUtensorMap* t, SmallArgs p, int64_t tiles, 
   const int clusters = int(std::max<int64_t>(
       1, std::min<int64_t>(tiles, int64_t(num_sms) * per_sm / p.split)));
   const int fixed = 1024 + (p.split > 1 ? Cfg::SUMS : 0) + int(sizeof(SmallShared)) +
-                    (MODE != kMxPlain ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts) : 0);
+                    (MODE != kMxPlain
+                         ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts)
+                         : 0);
   // the tokens' chunks, as far as four stages of weights leave room
   const int share = int(mx_ceil(chunks, p.split));
   p.slots = std::min(std::min(share, kSmallSlots),
