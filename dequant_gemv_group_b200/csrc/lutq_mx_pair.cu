@@ -32,7 +32,7 @@ namespace lutq {
 using namespace sm100;
 
 constexpr uint64_t kPairWaitNs = 2000000000ull;
-constexpr int kPairMaxStages = 8;
+constexpr int kPairMaxStages = 10;
 constexpr int kPairThreads = 64 + 256;
 constexpr int kPairPrefetch = 10;    // chunks of weights brought to L2 ahead of the launch
 constexpr int kPairTokenGroup = 16;  // token tiles that share a pass over the weights
@@ -43,8 +43,12 @@ struct PairCfg {
   static constexpr int NT = 256 / ND;                    // tokens of a tile at most
   static constexpr int CH = mx_chunk_bytes(FMT);
   static constexpr int BLOCKS = CH / 512;
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = NT / 2 * 128;
-  static constexpr int STAGE = ND * A_BYTES + B_BYTES + (ND + 2) * CH;
+  static constexpr int A_BYTES = 128 * 128;
+  // a stage for tiles of up to `width` columns: weights, half of the tokens, scales
+  __host__ __device__ static constexpr int b_bytes(int width) { return width / 2 * 128; }
+  __host__ __device__ static constexpr int stage(int width) {
+    return ND * A_BYTES + b_bytes(width) + (ND + (width > kMxRowTile ? 2 : 1)) * CH;
+  }
   static constexpr int SF_COLS = (ND + 2) * BLOCKS * 4;  // one set; two are kept
   static constexpr int SECOND = (512 - 2 * SF_COLS - 256) / 32 * 32;  // the other tile's sums
   static constexpr int SHARED_COLS = 256 - SECOND;       // columns of both
@@ -64,12 +68,13 @@ struct PairArgs {
   int token_tiles;    // plain: ceil(M / NT)
   int pairs;          // pairs of blocks in the launch
   int split;          // pairs that share a tile by K
+  int width;          // columns of the widest tile: what a stage has room for
   int tma_store;      // y by tensor-map stores (row pitch a multiple of 16 bytes)
 };
 
 // Columns of a tile with `valid` tokens: each block loads half of them, in
 // boxes of 16.
-__device__ __forceinline__ int pair_width(int valid) { return (valid + 31) / 32 * 32; }
+__host__ __device__ __forceinline__ int pair_width(int valid) { return (valid + 31) / 32 * 32; }
 
 __device__ __forceinline__ float pair_silu_mul(float g, float u) {
   return __fdividef(g, 1.f + __expf(-g)) * u;
@@ -203,7 +208,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int ST = a.stages;
-  uint8_t* staging = smem + ST * Cfg::STAGE;  // [8 warps][2] slices
+  const uint32_t b_bytes = Cfg::b_bytes(p.width), stage_bytes = Cfg::stage(p.width);
+  uint8_t* staging = smem + ST * stage_bytes;  // [8 warps][2] slices
   PairShared* sh = reinterpret_cast<PairShared*>(staging + 16 * SLICE);
   int32_t* counts = reinterpret_cast<int32_t*>(sh + 1);
   const uint32_t sbase = smem_addr(smem);
@@ -284,8 +290,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int c = c0; c < c1; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kPairWaitNs);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const uint32_t st = sbase + s * Cfg::STAGE;
-        const uint32_t sb = st + ND * Cfg::A_BYTES, sf = sb + Cfg::B_BYTES;
+        const uint32_t st = sbase + s * stage_bytes;
+        const uint32_t sb = st + ND * Cfg::A_BYTES, sf = sb + b_bytes;
         const uint32_t bar = full0 + 8 * s;
         const int sc = c * (CH / 1024);
         if (elect_one()) {
@@ -340,9 +346,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           ok = mbar_wait(full(s), ph, abort, kPairWaitNs);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          const uint32_t st = desc_lo(sbase + s * Cfg::STAGE);
+          const uint32_t st = desc_lo(sbase + s * stage_bytes);
           const uint32_t bl = st + ((ND * Cfg::A_BYTES) >> 4);
-          const uint32_t sf = bl + (Cfg::B_BYTES >> 4);
+          const uint32_t sf = bl + (b_bytes >> 4);
           const uint32_t sf_tmem = tmem + 512u - uint32_t(2 - (it & 1)) * Cfg::SF_COLS;
           const uint32_t sb_tmem = sf_tmem + ND * BLOCKS * 4;
           if (elect_one()) {
@@ -590,10 +596,11 @@ static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stre
   constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
   const int fixed = 1024 + 16 * SLICE + int(sizeof(PairShared)) +
                     (MODE != kMxPlain ? 8 * p.g.experts : 0);
-  p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::STAGE);
-  // a split tile's sums: up to 8 slices of 16 KB (split 2 or 4)
-  static_assert(!SPLIT || (smem - 1024 - 16 * SLICE - int(sizeof(PairShared))) / Cfg::STAGE *
-                                  Cfg::STAGE >= 8 * 32 * 128 * 4, "");
+  p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::stage(p.width));
+  // A split tile's sums, 512 bytes a column, fit in four stages of any width:
+  // 4 (16 KB + 64 width) >= 512 width for up to 256 columns.
+  static_assert(!SPLIT || (smem - 1024 - 16 * SLICE - int(sizeof(PairShared))) / Cfg::stage(256) >= 4,
+                "");
   auto kernel = mx_pair_kernel<FMT, MODE, DT, SPLIT>;
   static bool granted[64] = {};
   int dev = 0;
@@ -666,6 +673,9 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   PairArgs p = {};
   p.g = g;
   p.token_tiles = int(mx_ceil(g.M, nt));
+  // Few tokens leave room for more stages, which come at the latency of memory
+  // (28672 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 32.0 -> 27.8 us).
+  p.width = mode == kMxPlain ? pair_width(int(std::min<int64_t>(g.M, nt))) : nt;
   // Split a plain product's tiles by K while that gives idle pairs work and
   // saves more chunks (0.3 us each) than the exchange costs (1.5 us for 32
   // columns, 3 for 256; 4096 x 14336 at 512 tokens 23.6 -> 20.3 us, 512 x 14336
