@@ -389,11 +389,10 @@ static cudaError_t launch_one(const CUtensorMap* t, MxGemmArgs a, int64_t tiles,
   // partial sums of a wide gate-and-up tile would leave none for stages
   constexpr bool two = NT <= 32 && Cfg::ND == 1;
   constexpr int budget = two ? 113 * 1024 : kMxSmemMax;
-  int split;
-  mx_split(tiles, a.chunks, int64_t(num_sms) * (two ? 2 : 1), Cfg::ND == 2 && NT > 32 ? 1 : 8,
-           &split);
+  const int split =
+      mx_split(tiles, a.chunks, two ? 2 : 1, num_sms, Cfg::ND == 2 && NT > 32 ? 1 : 8);
   const int clusters =
-      int(std::max<int64_t>(1, std::min<int64_t>(tiles, int64_t(num_sms) * (two ? 2 : 1) / split)));
+      int(std::max<int64_t>(1, std::min(tiles, mx_clusters(split, two ? 2 : 1, num_sms))));
   const int fixed = 1024 + (split > 1 ? Cfg::SUMS : 0) + int(sizeof(MxShared)) +
                     8 * a.experts;
   a.stages = std::min(kMxMaxStages, (budget - fixed) / Cfg::STAGE);

@@ -3,6 +3,8 @@
 
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "lutq_mx.cuh"
 
 namespace lutq {
@@ -69,12 +71,22 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
 // Tokens per tile of mx_gemm_kernel: one tile for up to 128.
 int mx_tile_tokens(int64_t M);
 
-// Split a tile's K over a cluster while that gives idle block slots work and
-// every block two chunks.
-inline void mx_split(int64_t tiles, int chunks, int64_t slots, int most, int* split) {
+// Clusters of s blocks (1, 2, 4, 8) that run at once, per_sm blocks on a
+// multiprocessor.  Clusters of more than two leave multiprocessors over: the
+// 148 hold 33 clusters of 4 and 15 of 8, or 32 of 8 at two blocks each; one
+// more waits for another to end (74 tiles of 2048 x 128 split by 4 at two
+// blocks each: 15.6 us, not split 7.5).
+inline int64_t mx_clusters(int s, int per_sm, int num_sms) {
+  if (s <= 2) return int64_t(num_sms) * per_sm / s;
+  return std::max(1, num_sms * (s == 4 ? 33 * per_sm : per_sm == 2 ? 32 : 15) / 148);
+}
+
+// Split a tile's K over a cluster while that gives idle multiprocessors work
+// and every block a chunk.
+inline int mx_split(int64_t tiles, int chunks, int per_sm, int num_sms, int most) {
   int s = 1;
-  while (s < most && tiles * s * 2 <= slots && chunks >= 2 * s) s *= 2;
-  *split = s;
+  while (s < most && tiles <= mx_clusters(2 * s, per_sm, num_sms) && chunks >= 2 * s) s *= 2;
+  return s;
 }
 
 // A block that holds c of an SM's 512 columns of tensor memory asks for at

@@ -655,30 +655,86 @@ __global__ void __launch_bounds__(kSmallThreads)
 
 // ------------------------------------------------------------------ host side
 
+// A launch's shape: blocks that share a tile by K, blocks on a multiprocessor,
+// and what follows from them.
+struct SmallShape {
+  int split, per_sm, clusters, slots, stages, smem;
+  bool ok;
+};
+
+template <int FMT, int MODE>
+static SmallShape small_shape(const SmallArgs& p, int64_t tiles, int split, int per_sm,
+                              int num_sms) {
+  using Cfg = SmallCfg<FMT, MODE>;
+  const int budget = (per_sm == 2 ? 113 : 227) * 1024;
+  SmallShape s = {split, per_sm};
+  s.clusters = int(std::max<int64_t>(1, std::min(tiles, mx_clusters(split, per_sm, num_sms))));
+  const int fixed = 1024 + (split > 1 ? Cfg::SUMS : 0) + int(sizeof(SmallShared)) +
+                    (MODE != kMxPlain
+                         ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts)
+                         : 0);
+  // the tokens' chunks, as far as four stages of weights leave room
+  s.slots = std::min({int(mx_ceil(p.g.chunks, split)), kSmallSlots,
+                      (budget - fixed - 4 * Cfg::STAGE) / Cfg::SLOT});
+  s.stages = std::min(kSmallStages, (budget - fixed - s.slots * Cfg::SLOT) / Cfg::STAGE);
+  s.smem = std::max(fixed + s.slots * Cfg::SLOT + s.stages * Cfg::STAGE, mx_smem_floor(Cfg::TMEM));
+  s.ok = s.slots >= 1 && (split == 1 || split <= p.g.chunks);
+  return s;
+}
+
+// What a plain product of a shape takes beyond what all of them do, in us: the terms
+// fitted to 1024 x 4096 .. 28672 x 8192 and 8192 x 28672 in both formats at 1,
+// 6 and 16 tokens.  Of the eight shapes it takes one that is 2 % slower than
+// the best on average and 13 % at worst; as many splits as fill two blocks a
+// multiprocessor, the rule before, was 15 % slower on average.
+template <int FMT>
+static float small_cost(const SmallArgs& p, int64_t tiles, const SmallShape& s, int num_sms) {
+  using Cfg = SmallCfg<FMT, kMxPlain>;
+  const int per = s.clusters * s.split > num_sms ? s.per_sm : 1;  // blocks where they are most
+  const float rounds = float(mx_ceil(tiles, s.clusters));
+  const int chunks = int(mx_ceil(p.g.chunks, s.split));  // of a block in a tile
+  int rows = 1;
+  while (rows < p.g.M) rows *= 2;
+  // quantizing: 13 ns a token's chunk, again for every tile if they do not all fit
+  const float quantize = .013f * rows * chunks * per * (chunks <= s.slots ? 1.f : rounds);
+  // weights: 8 TB/s in all, 72 GB/s a multiprocessor, a stage at 1.2 us
+  const float stage = Cfg::STAGE / 1024.f;
+  const float weights = std::max(
+      float(tiles) * p.g.chunks * stage / 8000.f,
+      rounds * chunks * std::max(per * stage / 72.f, 1.2f / s.stages));
+  // adding up; all of shared memory: no start beside the launch before
+  const float rest = (s.split > 1 ? .9f + 1.6f * rounds : .35f * rounds) +
+                     (s.per_sm == 1 ? .6f : 0.f) + .15f * (per - 1);
+  return quantize + weights + rest;
+}
+
 template <int FMT, int MODE, int DT>
 static cudaError_t launch_one(const CUtensorMap* t, SmallArgs p, int64_t tiles, int num_sms,
                               cudaStream_t stream) {
   using Cfg = SmallCfg<FMT, MODE>;
   static_assert(Cfg::TMEM <= 256, "");
-  // two blocks on a multiprocessor where a stage is one matrix
-  constexpr int budget = Cfg::ND == 1 ? 113 * 1024 : 227 * 1024;
-  constexpr int per_sm = Cfg::ND == 1 ? 2 : 1;
-  const int chunks = p.g.chunks;
-  mx_split(tiles, chunks, int64_t(num_sms) * per_sm, 8, &p.split);
-  const int clusters = int(std::max<int64_t>(
-      1, std::min<int64_t>(tiles, int64_t(num_sms) * per_sm / p.split)));
-  const int fixed = 1024 + (p.split > 1 ? Cfg::SUMS : 0) + int(sizeof(SmallShared)) +
-                    (MODE != kMxPlain
-                         ? 4 * ((kSmallEntry + 4) * ((p.pairs + 3) & ~3) + p.g.experts)
-                         : 0);
-  // the tokens' chunks, as far as four stages of weights leave room
-  const int share = int(mx_ceil(chunks, p.split));
-  p.slots = std::min(std::min(share, kSmallSlots),
-                     (budget - fixed - 4 * Cfg::STAGE) / Cfg::SLOT);
-  if (p.slots < 1) return cudaErrorInvalidValue;
-  p.g.stages = std::min(kSmallStages, (budget - fixed - p.slots * Cfg::SLOT) / Cfg::STAGE);
-  const int smem = std::max(fixed + p.slots * Cfg::SLOT + p.g.stages * Cfg::STAGE,
-                            mx_smem_floor(Cfg::TMEM));
+  SmallShape best = {};
+  if constexpr (MODE == kMxPlain) {
+    float least = 0.f;
+    for (int per_sm = 1; per_sm <= 2; ++per_sm)
+      for (int split = 1; split <= 8; split *= 2) {
+        const SmallShape s = small_shape<FMT, MODE>(p, tiles, split, per_sm, num_sms);
+        if (!s.ok) continue;
+        const float cost = small_cost<FMT>(p, tiles, s, num_sms);
+        if (best.ok && cost >= least) continue;
+        best = s;
+        least = cost;
+      }
+  } else {
+    // two blocks on a multiprocessor where a stage is one matrix
+    constexpr int per_sm = Cfg::ND == 1 ? 2 : 1;
+    best = small_shape<FMT, MODE>(p, tiles, mx_split(tiles, p.g.chunks, per_sm, num_sms, 8), per_sm,
+                                  num_sms);
+  }
+  if (!best.ok) return cudaErrorInvalidValue;
+  p.split = best.split;
+  p.slots = best.slots;
+  p.g.stages = best.stages;
   auto kernel = mx_small_kernel<FMT, MODE, DT>;
   static bool granted[64] = {};
   int dev = 0;
@@ -691,9 +747,9 @@ static cudaError_t launch_one(const CUtensorMap* t, SmallArgs p, int64_t tiles, 
     granted[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(clusters * p.split));
+  cfg.gridDim = dim3(unsigned(best.clusters * p.split));
   cfg.blockDim = dim3(kSmallThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.dynamicSmemBytes = size_t(best.smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

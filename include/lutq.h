@@ -643,7 +643,10 @@ lutq_status lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, const floa
  *
  * lutq_mx_gemv - the same for M = 0..16 rows of values x [M, K] of `x_dtype`,
  * quantized inside the kernel exactly as lutq_mx_quantize does: one launch
- * for single tokens and small batches.  LUTQ_ERR_SHAPE if M > 16.
+ * for single tokens and small batches.  LUTQ_ERR_SHAPE if M > 16.  Every block
+ * of threads quantizes x for itself, so for large matrices and more than a few
+ * rows lutq_mx_quantize and lutq_mx_gemm take less time (28672 x 8192 in
+ * LUTQ_NVFP4: 27 us for one row, 36 for six and 45 for sixteen against 3 + 27).
  *
  * Neither needs a workspace; results do not depend on timing, and a row of y
  * not on the other rows of x given the number of rows.  dev_status receives
