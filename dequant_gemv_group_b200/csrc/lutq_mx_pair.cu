@@ -480,9 +480,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else if (p.tma_store) {
           fence_async_shared();
           __syncwarp();
-          if (lane == 0 && row < a.N) {
-            tma_2d_s2g(&tmap_y, row, int(token0) + c, smem_addr(stg));
-            bulk_commit();
+          if (lane == 0) {
+            if (row < a.N) tma_2d_s2g(&tmap_y, row, int(token0) + c, smem_addr(stg));
+            bulk_commit();  // (a group a slice: the wait above counts them)
           }
         } else {
           // rows that no 16-byte copy can write: each warp its own lanes
