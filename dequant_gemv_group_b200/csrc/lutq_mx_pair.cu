@@ -18,6 +18,9 @@
 // through memory as 4-bit codes.  (nvfp4's row scale needs the whole row: those
 // are written as bf16 and quantized by a launch of their own.)
 //
+// Few tokens: tiles of 512 weight rows where that saves a round (tall), or of
+// 256 shared by K where they are fewer than pairs (split).
+//
 // Epilogue: eight warps, each on its own: 32 rows by 32 columns (tokens) at a
 // time through shared memory and a tensor-map store, which also clips the tile
 // to the output.
@@ -35,12 +38,19 @@ constexpr uint64_t kPairWaitNs = 2000000000ull;
 constexpr int kPairMaxStages = 10;
 constexpr int kPairThreads = 64 + 256;
 constexpr int kPairPrefetch = 10;    // chunks of weights brought to L2 ahead of the launch
+constexpr int kPairTallTokens = 192;
 constexpr int kPairTokenGroup = 16;  // token tiles that share a pass over the weights
 
-template <int FMT, int MODE>
+// A pair's tile: plain, split by K over the pairs of a cluster, or tall (512
+// weight rows).
+enum PairTile { kPairPlain = 0, kPairSplit = 1, kPairTall = 2 };
+
+template <int FMT, int MODE, int TILE>
 struct PairCfg {
-  static constexpr int ND = MODE == kMxGateUp ? 2 : 1;
-  static constexpr int NT = 256 / ND;                    // tokens of a tile at most
+  static constexpr bool TALL = TILE == kPairTall;
+  static constexpr int ND = MODE == kMxGateUp || TALL ? 2 : 1;  // sums of 256 weight rows
+  static constexpr int ROWS = TALL ? 512 : 256;          // weight rows of a tile (of a matrix)
+  static constexpr int NT = TALL ? kPairTallTokens : 256 / ND;  // tokens of a tile at most
   static constexpr int CH = mx_chunk_bytes(FMT);
   static constexpr int BLOCKS = CH / 512;
   static constexpr int A_BYTES = 128 * 128;
@@ -50,8 +60,10 @@ struct PairCfg {
     return ND * A_BYTES + b_bytes(width) + (ND + (width > kMxRowTile ? 2 : 1)) * CH;
   }
   static constexpr int SF_COLS = (ND + 2) * BLOCKS * 4;  // one set; two are kept
-  static constexpr int SECOND = (512 - 2 * SF_COLS - 256) / 32 * 32;  // the other tile's sums
-  static constexpr int SHARED_COLS = 256 - SECOND;       // columns of both
+  // where the next tile's sums begin (tall: where these do), and the columns of both
+  static constexpr int SECOND = TALL ? 0 : (512 - 2 * SF_COLS - 256) / 32 * 32;
+  static_assert(!TALL || ND * NT + 2 * SF_COLS <= 512, "");
+  static constexpr int SHARED_COLS = 256 - SECOND;
 };
 
 struct PairShared {
@@ -68,6 +80,7 @@ struct PairArgs {
   int token_tiles;    // plain: ceil(M / NT)
   int pairs;          // pairs of blocks in the launch
   int split;          // pairs that share a tile by K
+  int tall;           // tiles of 512 weight rows
   int width;          // columns of the widest tile: what a stage has room for
   int tma_store;      // y by tensor-map stores (row pitch a multiple of 16 bytes)
 };
@@ -90,14 +103,14 @@ __device__ __forceinline__ void pair_drain(uint32_t bar, uint32_t parity) {
 // tile is read from memory once per group and then from L2.  Tiles begin at
 // multiples of 128 tokens (the height of a scale block), a last one is as wide
 // as its tokens need.
-template <int MODE>
+template <int MODE, int ROWS>
 struct PairTiles {
   static constexpr int nt = MODE == kMxGateUp ? 128 : 256;
   const int32_t* counts;
   int mtiles, experts, token_tiles, e = 0, e_tiles = 0;
   int64_t e_first = 0, tokens;
   __device__ PairTiles(const PairArgs& a, const int32_t* c)
-      : counts(c), mtiles(int(mx_ceil(a.g.N, 256))), experts(a.g.experts),
+      : counts(c), mtiles(int(mx_ceil(a.g.N, ROWS))), experts(a.g.experts),
         token_tiles(a.token_tiles), tokens(a.g.M) {
     if (MODE != kMxPlain) {
       tokens = counts[0];
@@ -189,7 +202,10 @@ __device__ __forceinline__ bool pack_hidden(const MxGemmArgs& a, const uint8_t* 
 // part is summed, its stages are free: the sums go there, and the pair that
 // finishes a slice of 32 columns (slice s: pair s mod split) fetches and adds
 // them in the order of the pairs.
-template <int FMT, int MODE, int DT, bool SPLIT>
+//
+// TALL (plain products of up to 192 tokens): two sums of 256 weight rows by all
+// tokens, so that what a pair fetches of the tokens serves twice the weights.
+template <int FMT, int MODE, int DT, int TILE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a2,
@@ -199,8 +215,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                    const __grid_constant__ CUtensorMap tmap_sa2,
                    const __grid_constant__ CUtensorMap tmap_sb,
                    const __grid_constant__ CUtensorMap tmap_y, const PairArgs p) {
-  using Cfg = PairCfg<FMT, MODE>;
-  constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS;
+  using Cfg = PairCfg<FMT, MODE, TILE>;
+  constexpr bool SPLIT = TILE == kPairSplit, TALL = Cfg::TALL;
+  constexpr int ND = Cfg::ND, CH = Cfg::CH, BLOCKS = Cfg::BLOCKS, ROWS = Cfg::ROWS;
   constexpr int ES = DT == LUTQ_FP32 ? 4 : 2;
   constexpr int SLICE = 32 * 32 * ES;  // a staged slice: 32 tokens x a warp's 32 rows
   const MxGemmArgs& a = p.g;
@@ -244,13 +261,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // into L2.  (A prefetch reads nothing into the kernel; what that work may
   // still write, L2 has no stale copy of.)
   if (MODE == kMxPlain && warp == 0 && elect_one()) {
-    const int64_t per_group = int64_t(kPairTokenGroup) * mx_ceil(a.N, 256);
+    const int64_t per_group = int64_t(kPairTokenGroup) * mx_ceil(a.N, ROWS);
     const int tile = int(blockIdx.x >> 1) / split;
     if (tile < per_group) {
       const int width = min(kPairTokenGroup, p.token_tiles);
-      const int arow = tile / width * 256 + int(rank) * 128;
-      for (int c = c0; c < min(c1, c0 + kPairPrefetch); ++c)
+      const int arow = tile / width * ROWS + int(rank) * 128;
+      for (int c = c0; c < min(c1, c0 + kPairPrefetch / (ROWS / 256)); ++c) {
         tma_3d_prefetch(&tmap_a, c * 128, arow, 0);
+        if (TALL) tma_3d_prefetch(&tmap_a, c * 128, arow + 256, 0);
+      }
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -268,7 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const int64_t first = (blockIdx.x >> 1) / split, step = p.pairs / split;
   const uint32_t full0 = cluster_map(full(0), leader);  // the pair's first block's barriers
-  PairTiles<MODE> tiles(p, counts);
+  PairTiles<MODE, ROWS> tiles(p, counts);
   int expert, mt, m0, valid;
 
   if (warp == 0) {
@@ -279,13 +298,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     for (int64_t t = first; ok && tiles.at(t, &expert, &mt, &m0, &valid); t += step) {
       const int row0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-      const int arow = mt * 256 + int(rank) * 128;
+      const int arow = mt * ROWS + int(rank) * 128;
+      const int arow2 = arow + (TALL ? 256 : 0);  // the second sums' rows
       const int half = pair_width(valid) / 2;
       const int brow = row0 + int(rank) * half;
       // the token scales of one or two tiles of 128 rows
       const int sb_tiles = half > kMxRowTile / 2 ? 2 : 1;
       const uint32_t bytes = 2u * uint32_t(ND * (Cfg::A_BYTES + CH) + half * 128 + sb_tiles * CH);
       const int sa_row = (arow / 128) * a.chunks * (CH / 1024);
+      const int sa_row2 = (arow2 / 128) * a.chunks * (CH / 1024);
       const int sb_row = (row0 / kMxRowTile) * a.chunks * (CH / 1024);
       for (int c = c0; c < c1; ++c) {
         ok = mbar_wait(empty(s), ph, abort, kPairWaitNs);
@@ -297,15 +318,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (elect_one()) {
           if (rank == 0) mbar_expect_tx(full(s), bytes);
           tma_3d_g2s_pair(st, &tmap_a, c * 128, arow, expert, bar);
-          if (ND == 2) tma_3d_g2s_pair(st + Cfg::A_BYTES, &tmap_a2, c * 128, arow, expert, bar);
-          if (2 * half == Cfg::NT) {
+          if (ND == 2) tma_3d_g2s_pair(st + Cfg::A_BYTES, &tmap_a2, c * 128, arow2, expert, bar);
+          if (2 * half == p.width) {
             tma_3d_g2s_pair(sb, &tmap_b, c * 128, brow, 0, bar);
           } else {
             for (int i = 0; i < half; i += 16)
               tma_3d_g2s_pair(sb + i * 128, &tmap_b16, c * 128, brow + i, 0, bar);
           }
           tma_3d_g2s_pair(sf, &tmap_sa, 0, sa_row + sc, expert, bar);
-          if (ND == 2) tma_3d_g2s_pair(sf + CH, &tmap_sa2, 0, sa_row + sc, expert, bar);
+          if (ND == 2) tma_3d_g2s_pair(sf + CH, &tmap_sa2, 0, sa_row2 + sc, expert, bar);
           tma_3d_g2s_pair(sf + ND * CH, &tmap_sb, 0, sb_row + sc, 0, bar);
           if (sb_tiles == 2)
             tma_3d_g2s_pair(sf + (ND + 1) * CH, &tmap_sb, 0,
@@ -408,19 +429,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int NS = Cfg::NT / 32, OWN = NS / 2;
     auto column_of = [&](int tile, int i) {
       const int sl = group + 2 * i;
-      return 32 * ((tile & 1) == 0 ? NS - 1 - sl : sl);
+      return 32 * (!TALL && (tile & 1) == 0 ? NS - 1 - sl : sl);
     };
     // nvfp4: a tile's row scales are fetched while the tile before is worked on
     float ga[2] = {1.f, 1.f}, ga_next[2] = {1.f, 1.f}, gb_next[OWN];
     auto fetch = [&](int tile) {
-      const int r = mt * 256 + int(rank) * 128 + quarter * 32 + lane;
+      const int r = mt * ROWS + int(rank) * 128 + quarter * 32 + lane;
       const int64_t first_token = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
-      if (r < a.N) {
 #pragma unroll
-        for (int w = 0; w < ND; ++w)
+      for (int w = 0; w < ND; ++w) {
+        const int rw = r + (TALL ? 256 * w : 0);
+        if (rw < a.N)
           ga_next[w] = *reinterpret_cast<const float*>(
               reinterpret_cast<const uint8_t*>(a.a_rows[w]) + int64_t(expert) * a.a_stride +
-              int64_t(r) * 4);
+              int64_t(rw) * 4);
       }
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
@@ -430,7 +452,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool more = tiles.at(first, &expert, &mt, &m0, &valid);
     if (FMT == LUTQ_NVFP4 && more) fetch(0);
     for (int64_t t = first; more; t += step, ++n) {
-      const int row = mt * 256 + int(rank) * 128 + quarter * 32 + lane;
+      const int row0 = mt * ROWS + int(rank) * 128 + quarter * 32 + lane;
       const int tokens = valid;
       const int64_t token0 = MODE == kMxPlain ? m0 : counts[a.experts + expert] + m0;
       const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + uint32_t((n & 1) * Cfg::SECOND);
@@ -448,8 +470,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
 
-      // one slice: scale, round, stage, store
-      auto finish = [&](int c, const float* gbc, uint32_t (&v)[ND][32]) {
+      // one slice: scale, round, stage, store (SETS: of one or of two sums)
+      constexpr int SETS = TALL ? 1 : ND;
+      auto finish = [&](int c, const float* gbc, uint32_t (&v)[SETS][32], int set) {
+        const int row = row0 + 256 * set;
+        const float ga0 = TALL && set == 1 ? ga[1] : ga[0];
         uint8_t* stg = stage0 + slot * SLICE;
         const uint32_t sta = smem_addr(stg) + lane * ES;
         float4 s4[8];  // (all before the first store: it would order the loads)
@@ -462,14 +487,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          float f = __uint_as_float(v[0][j]), u = __uint_as_float(v[ND - 1][j]);
+          float f = __uint_as_float(v[0][j]), u = __uint_as_float(v[SETS - 1][j]);
           if (FMT == LUTQ_NVFP4) {
             const float4 q4 = s4[j / 4];
             const float gb = j % 4 == 0 ? q4.x : j % 4 == 1 ? q4.y : j % 4 == 2 ? q4.z : q4.w;
-            f = f * ga[0] * gb;
-            if (ND == 2) u = u * ga[1] * gb;
+            f = f * ga0 * gb;
+            if (SETS == 2) u = u * ga[1] * gb;
           }
-          if (ND == 2) f = pair_silu_mul(f, u);
+          if (SETS == 2) f = pair_silu_mul(f, u);
           stage1<DT>(sta + j * 32 * ES, f);
         }
         if (MODE == kMxGateUp && FMT == LUTQ_MXFP4) {
@@ -500,10 +525,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         slot ^= 1;
       };
-      auto load = [&](int i, uint32_t (&v)[ND][32]) {
+      auto load = [&](int i, uint32_t (&v)[SETS][32]) {
         if (column(i) < tokens) {
 #pragma unroll
-          for (int w = 0; w < ND; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + column(i), v[w]);
+          for (int w = 0; w < SETS; ++w) tmem_ld_32x32b_x32(d + w * Cfg::NT + column(i), v[w]);
         }
       };
       if constexpr (SPLIT) {
@@ -511,7 +536,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // nothing any more, [column][row]: the block of the same place in the
         // pair that finishes a slice fetches it from there
         float* mine = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
-        uint32_t v[ND][32];
+        uint32_t v[1][32];
 #pragma unroll 1
         for (int c = 32 * group; c < tokens; c += 64) {
           tmem_ld_32x32b_x32(d + c, v[0]);
@@ -546,14 +571,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             gbs[lane] = a.b_rows[token0 + c + lane];
             __syncwarp();
           }
-          finish(c, gbs, v);
+          finish(c, gbs, v, 0);
         }
         break;
       }
+      if constexpr (TALL) {
+        uint32_t v[1][32];
+        for (int set = 0; set < 2; ++set) {
+#pragma unroll 1
+          for (int i = 0; column(i) < tokens && i < OWN; ++i) {
+            tmem_ld_32x32b_x32(d + set * Cfg::NT + column(i), v[0]);
+            tmem_wait_ld();
+            finish(column(i), gbs + 32 * i, v, set);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_arrive(cluster_map(smem_addr(&sh->acc_free), leader));
+        if (FMT == LUTQ_NVFP4 && more) fetch(n + 1);
+        continue;
+      }
       // two slices in registers; the shared columns are among the first two of
       // each group, so the next tile's MMAs wait for no more than these loads
-      static_assert(Cfg::SHARED_COLS <= 128 && OWN >= 2, "");
-      uint32_t va[ND][32], vb[ND][32];
+      static_assert(TALL || (Cfg::SHARED_COLS <= 128 && OWN >= 2), "");
+      uint32_t va[SETS][32], vb[SETS][32];
       load(0, va);
       load(1, vb);
       tmem_wait_ld();
@@ -568,8 +609,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           load(i + 1, vb);
           tmem_wait_ld();
         }
-        if (column(i) < tokens) finish(column(i), gbs + 32 * i, va);
-        if (column(i + 1) < tokens) finish(column(i + 1), gbs + 32 * (i + 1), vb);
+        if (column(i) < tokens) finish(column(i), gbs + 32 * i, va, 0);
+        if (column(i + 1) < tokens) finish(column(i + 1), gbs + 32 * (i + 1), vb, 0);
       }
     }
     if (lane == 0) bulk_wait<0>();
@@ -589,9 +630,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-template <int FMT, int MODE, int DT, bool SPLIT>
+template <int FMT, int MODE, int DT, int TILE>
 static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stream) {
-  using Cfg = PairCfg<FMT, MODE>;
+  using Cfg = PairCfg<FMT, MODE, TILE>;
   constexpr int SLICE = 32 * 32 * (DT == LUTQ_FP32 ? 4 : 2);
   constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
   const int fixed = 1024 + 16 * SLICE + int(sizeof(PairShared)) +
@@ -599,9 +640,9 @@ static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stre
   p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::stage(p.width));
   // A split tile's sums, 512 bytes a column, fit in four stages of any width:
   // 4 (16 KB + 64 width) >= 512 width for up to 256 columns.
-  static_assert(!SPLIT || (smem - 1024 - 16 * SLICE - int(sizeof(PairShared))) / Cfg::stage(256) >= 4,
+  static_assert(TILE != kPairSplit || (smem - 1024 - 16 * SLICE - int(sizeof(PairShared))) / Cfg::stage(256) >= 4,
                 "");
-  auto kernel = mx_pair_kernel<FMT, MODE, DT, SPLIT>;
+  auto kernel = mx_pair_kernel<FMT, MODE, DT, TILE>;
   static bool granted[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -630,17 +671,18 @@ static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stre
 
 template <int FMT, int DT>
 static cudaError_t launch_plain(const MxPairMaps& m, const PairArgs& p, cudaStream_t stream) {
-  return p.split > 1 ? launch_one<FMT, kMxPlain, DT, true>(m, p, stream)
-                     : launch_one<FMT, kMxPlain, DT, false>(m, p, stream);
+  if (p.tall) return launch_one<FMT, kMxPlain, DT, kPairTall>(m, p, stream);
+  return p.split > 1 ? launch_one<FMT, kMxPlain, DT, kPairSplit>(m, p, stream)
+                     : launch_one<FMT, kMxPlain, DT, kPairPlain>(m, p, stream);
 }
 
 template <int FMT>
 static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode,
                               cudaStream_t stream) {
-  if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16, false>(m, p, stream);
+  if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16, kPairPlain>(m, p, stream);
   if (mode == kMxDown)
-    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16, false>(m, p, stream)
-                                    : launch_one<FMT, kMxDown, LUTQ_FP32, false>(m, p, stream);
+    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16, kPairPlain>(m, p, stream)
+                                    : launch_one<FMT, kMxDown, LUTQ_FP32, kPairPlain>(m, p, stream);
   if (p.g.y_dtype == LUTQ_BF16) return launch_plain<FMT, LUTQ_BF16>(m, p, stream);
   if (p.g.y_dtype == LUTQ_FP16) return launch_plain<FMT, LUTQ_FP16>(m, p, stream);
   return launch_plain<FMT, LUTQ_FP32>(m, p, stream);
@@ -663,7 +705,9 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   }
   const int64_t t_bytes = mx_bytes(token_rows, g.K, fmt);
   const int nt = mode == kMxGateUp ? 128 : 256;
-  if ((err = make_mx_map(&m.b, tokens, token_rows, g.K, 1, t_bytes, nt / 2)) != cudaSuccess)
+  // columns of the widest tile: all tokens, or the most that a tile has
+  const int width = mode == kMxPlain ? pair_width(int(std::min<int64_t>(g.M, nt))) : nt;
+  if ((err = make_mx_map(&m.b, tokens, token_rows, g.K, 1, t_bytes, width / 2)) != cudaSuccess)
     return err;
   if ((err = make_mx_map(&m.b16, tokens, token_rows, g.K, 1, t_bytes, 16)) != cudaSuccess)
     return err;
@@ -675,7 +719,7 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   p.token_tiles = int(mx_ceil(g.M, nt));
   // Few tokens leave room for more stages, which come at the latency of memory
   // (28672 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 32.0 -> 27.8 us).
-  p.width = mode == kMxPlain ? pair_width(int(std::min<int64_t>(g.M, nt))) : nt;
+  p.width = width;
   // Split a plain product's tiles by K while that gives idle pairs work and
   // saves more chunks (0.3 us each) than the exchange costs (1.5 us for 32
   // columns, 3 for 256; 4096 x 14336 at 512 tokens 23.6 -> 20.3 us, 512 x 14336
@@ -686,6 +730,23 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   p.split = 1;
   if (mode == kMxPlain && tiles <= 32 && 2 * tiles <= slots && g.chunks >= 2 * per)
     p.split = tiles <= 8 && g.chunks >= 4 * per ? 4 : 2;
+  // Tall tiles where they save a round: what bounds a tile is what its pair
+  // fetches, 85 GB/s a multiprocessor.  28672 x 8192 in nvfp4 at 133 tokens: 2
+  // rounds of 32 KB a chunk and block take 35.2 us, 1 of 50 KB 30.5; at 17
+  // tokens 2 of 22 KB 27.8, 1 of 40 KB 24.9.
+  if (mode == kMxPlain && p.split == 1 && width <= kPairTallTokens) {
+    auto fetched = [&](int nd) {
+      const int a_bytes = 128 * 128 + mx_chunk_bytes(fmt);
+      const int b_bytes = width * 64 + (width > kMxRowTile ? 2 : 1) * mx_chunk_bytes(fmt);
+      return mx_ceil(mx_ceil(g.N, 256 * nd), slots) * (nd * a_bytes + b_bytes);
+    };
+    p.tall = fetched(2) < fetched(1);
+    if (p.tall) {
+      tiles = mx_ceil(g.N, 512);
+      m.a[1] = m.a[0];
+      m.sa[1] = m.sa[0];
+    }
+  }
   p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / p.split))) * p.split;
   p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0 &&
                 !(mode == kMxGateUp && fmt == LUTQ_MXFP4);  // (quantized instead)

@@ -177,10 +177,12 @@ SHAPES = [(1, 1, 32), (1, 128, 256), (2, 7, 96), (3, 256, 512), (8, 1000, 2048),
           (300, 2049, 96), (513, 300, 1056),
           (1, 20000, 512), (4, 1024, 28672), (13, 64, 8224),
           (40, 300, 14336), (250, 700, 14336), (290, 520, 8192), (70, 1030, 4128),
-          # enough tiles for the kernel of block pairs: 1 and 2 token tiles, row pitches that no
-          # 16-byte copy can write, tokens beyond one pass over the weights
+          # more tiles than pairs of blocks: 1 and 2 token tiles, row pitches that no 16-byte copy
+          # can write, tokens beyond one pass over the weights
           (77, 9601, 288), (160, 9480, 64), (300, 8200, 96), (600, 4096, 544), (1000, 2564, 1312),
-          (4099, 640, 160)]
+          (4099, 640, 160),
+          # tiles of 512 weight rows: one round and several, rows behind the last
+          (17, 19456, 288), (133, 19333, 544), (192, 37890, 96), (90, 76200, 64), (161, 57600, 1056)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
