@@ -6,10 +6,10 @@
 //
 // (token, choice) pairs are laid out by expert: expert e's rows begin at a
 // multiple of 128 (the height of a scale block) and keep the order of the
-// pairs.  Steps: plan (rows of every expert, two launches), x quantized into
-// its rows, gate and up product with silu, hidden values quantized (by that
-// product for many tokens in mxfp4, else a launch), down product, weighted sum
-// over a token's choices in their order.  Where an expert has a handful of
+// pairs.  Steps: plan (rows of every expert), x quantized into its rows, gate
+// and up product with silu, hidden values quantized (by that product for many
+// tokens in mxfp4, else a launch), down product, weighted sum over a token's
+// choices in their order.  Where an expert has a handful of
 // pairs: gate and up, down, sum, with the tokens quantized inside.  Rows do
 // not depend on one another.
 #include <algorithm>
@@ -21,7 +21,7 @@ namespace lutq {
 
 constexpr int kPlanThreads = 512;
 // Pairs an expert, at most, for the kernel of few tokens; beyond, tokens are
-// packed first (five launches).  Measured, kernel of few tokens / packed, us:
+// packed first (six launches).  Measured, kernel of few tokens / packed, us:
 //   mxfp4, 4096 x 2048: 8 experts, 32 tokens x 2 (8 pairs each) 37.0 / 37.7,
 //     48 tokens (12) 44.7 / 40.0; 64 experts, 32 tokens x 8 (4) 144 / 153;
 //   nvfp4 (a row's maximum first): 60 experts of 2048 x 1440, 37 tokens x 4
@@ -48,21 +48,32 @@ __device__ __forceinline__ int4 load_ids(const int32_t* ids, int i, int end, boo
                    i + 2 < end ? ids[i + 2] : -1, i + 3 < end ? ids[i + 3] : -1);
 }
 
-// Two launches of a block for each expert e.  The first counts its pairs.  The
-// second adds up the rows before its own from all counts and hands its rows
-// out: each warp owns a run of pairs, 128 at a time, and a scan over the
-// warps' and the lanes' counts keeps the pairs' order.
-template <bool PLACE>
+// A block for each expert e adds up the rows before its own from all experts'
+// counts and hands its rows out: each warp owns a run of pairs, 128 at a time,
+// and a scan over the warps' and the lanes' counts keeps the pairs' order.
+// PLAN_ALL: every block counts all experts' pairs itself; many pairs: a launch
+// before (PLAN_COUNT) counts them, each block its expert's.  The layer with one
+// launch / two: 80 pairs 29.1 / 29.9 us, 1600 85.3 / 86.3, 8192 101.8 / 102.0,
+// 32768 185.8 / 179.6.
+enum { PLAN_COUNT, PLAN_PLACE, PLAN_ALL };
+constexpr int kPlanAll = 1 << 13;
+template <int STEP>
 __global__ void __launch_bounds__(kPlanThreads)
     moe_plan_kernel(const int32_t* __restrict__ ids, int pairs, int E, MoePlan p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int W = kPlanThreads / 32;
+  constexpr bool ALL = STEP == PLAN_ALL;
   __shared__ int32_t warp_count[W];
   __shared__ int32_t base_s;
+  __shared__ int32_t of[ALL ? 1024 : 1];  // pairs of every expert
   const int e = blockIdx.x, th = threadIdx.x, lane = th & 31, warp = th >> 5;
   const bool aligned = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
   if (th == 0) base_s = 0;
+  if (ALL) {
+    for (int i = th; i < E; i += kPlanThreads) of[i] = 0;
+    __syncthreads();
+  }
   const int run = (pairs + W * 128 - 1) / (W * 128) * 128;
   const int i0 = min(pairs, warp * run), i1 = min(pairs, i0 + run);
   int mine = 0;
@@ -70,19 +81,24 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = i0 + 4 * lane; i < i1; i += 128) {
     const int4 d = load_ids(ids, i, i1, aligned);
     mine += (d.x == e) + (d.y == e) + (d.z == e) + (d.w == e);
+    if (ALL) {
+      if (uint32_t(d.x) < uint32_t(e)) atomicAdd(&of[d.x], 1);
+      if (uint32_t(d.y) < uint32_t(e)) atomicAdd(&of[d.y], 1);
+      if (uint32_t(d.z) < uint32_t(e)) atomicAdd(&of[d.z], 1);
+      if (uint32_t(d.w) < uint32_t(e)) atomicAdd(&of[d.w], 1);
+    }
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) warp_count[warp] = mine;
   __syncthreads();
-  if (!PLACE) {
-    if (warp == 0) {
-      const int c = __reduce_add_sync(0xffffffffu, lane < W ? warp_count[lane] : 0);
-      if (lane == 0) p.counts[e] = c;
-    }
-    return;
+  if (STEP != PLAN_PLACE && warp == 0) {
+    const int c = __reduce_add_sync(0xffffffffu, lane < W ? warp_count[lane] : 0);
+    if (lane == 0) p.counts[e] = c;
   }
+  if (STEP == PLAN_COUNT) return;
   int before = 0;
-  for (int i = th; i < e; i += kPlanThreads) before += (p.counts[i] + 127) / 128 * 128;
+  for (int i = th; i < e; i += kPlanThreads)
+    before += ((ALL ? of[i] : p.counts[i]) + 127) / 128 * 128;
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) atomicAdd(&base_s, before);
   __syncthreads();
@@ -262,12 +278,15 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                : make_mx_map(&maps[3], rows, cap, width, 1, mx_bytes(cap, width, fmt), 16);
   };
 
-  if ((err = launch_pdl(moe_plan_kernel<false>, dim3(unsigned(E)), dim3(kPlanThreads), 0, stream,
-                        ids, pairs, E, p)) != cudaSuccess)
-    return err;
-  if ((err = launch_pdl(moe_plan_kernel<true>, dim3(unsigned(E)), dim3(kPlanThreads), 0, stream,
-                        ids, pairs, E, p)) != cudaSuccess)
-    return err;
+  auto plan = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(unsigned(E)), dim3(kPlanThreads), 0, stream, ids, pairs, E, p);
+  };
+  if (pairs <= kPlanAll) {
+    err = plan(moe_plan_kernel<PLAN_ALL>);
+  } else if ((err = plan(moe_plan_kernel<PLAN_COUNT>)) == cudaSuccess) {
+    err = plan(moe_plan_kernel<PLAN_PLACE>);
+  }
+  if (err != cudaSuccess) return err;
   if ((err = launch_mx_quantize(x, dtype, 1, T, cap, D, fmt, nullptr, p.slot, top_k, ws + s.xq,
                                 dev_status, num_sms, stream)) != cudaSuccess)
     return err;
