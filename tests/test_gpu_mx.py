@@ -216,6 +216,26 @@ def test_gemv_types(lq, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", [
+    (16, 12288, 7168), (6, 12288, 7168), (16, 8192, 8192), (5, 28672, 2080), (16, 28672, 8192),
+    (16, 14336, 4096), (2, 38000, 1056), (16, 2304, 28704), (9, 9600, 14336), (16, 40000, 2080),
+    (1, 9472, 2048), (7, 4736, 4096), (3, 4097, 4128)])
+def test_few_tokens_of_large_matrices(lq, fmt, m, n, k):
+    """One tile a block and several, split or not, tokens kept in shared memory or not: against
+    fp64 products of the values."""
+    g = torch.Generator("cuda").manual_seed(n + m)
+    w = lq.lutq_mx_quantize(torch.randn(n, k, device="cuda", generator=g).bfloat16(), fmt)
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    x[m // 2] *= 8
+    xv, wv = (lq.lutq_mx_dequantize(p, r, k, fmt, dtype=torch.float32).double()
+              for p, r in ((lq.lutq_mx_quantize(x, fmt), m), (w, n)))
+    ref, mag = _f64(xv @ wv.t()), _f64(xv.abs() @ wv.abs().t())
+    y = lq.lutq_mx_gemv(x, w, n, k, fmt)
+    assert (np.abs(_f64(y) - ref) <= _bound(ref, mag, k, torch.float32)).all()
+    assert torch.equal(lq.lutq_mx_gemv(x, w, n, k, fmt), y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m", [1, 16, 40, 150, 700])
 def test_exact_sums(lq, fmt, m):
     """Small integers in scales of 1: every partial sum is exact, so y is too, in every tile."""
