@@ -723,7 +723,7 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   p.g = g;
   p.token_tiles = int(mx_ceil(g.M, nt));
   // Few tokens leave room for more stages, which come at the latency of memory
-  // (28672 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 32.0 -> 27.8 us).
+  // (9472 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 15.2 -> 13.5 us).
   p.width = width;
   // Split a plain product's tiles by K while that gives idle pairs work and
   // saves more chunks (0.3 us each) than the exchange costs (1.5 us for 32
