@@ -131,10 +131,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // y[t] = sum_j weights[t, j] * out[slot[t, j]] in fp32, rounded once.  Without
 // slots, a pair's row is its own number (and counts if its id is an expert).
-// PT: the type of the rows (see launch_mx_experts).
-template <int DT, int PT>
+template <int DT>
 __global__ void __launch_bounds__(256)
-    moe_combine_kernel(const void* __restrict__ out, const int32_t* __restrict__ slot,
+    moe_combine_kernel(const float* __restrict__ out, const int32_t* __restrict__ slot,
                        const int32_t* __restrict__ ids, int E, const float* __restrict__ weights,
                        int top_k, int64_t D, void* y) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -156,15 +155,15 @@ __global__ void __launch_bounds__(256)
         w[u] = weights[p];
       }
     }
-    Raw8<PT> raw[U];
+    Raw8<LUTQ_FP32> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r[u] >= 0) raw[u] = load_raw8<PT>(out, r[u] * D + d);
+      if (r[u] >= 0) raw[u] = load_raw8<LUTQ_FP32>(out, r[u] * D + d);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (r[u] < 0) continue;
       float v[8];
-      widen8<PT>(raw[u], v);
+      widen8<LUTQ_FP32>(raw[u], v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += w[u] * v[i];
     }
@@ -222,24 +221,18 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
-  // A pair's output row is fp32, except for bf16 tokens in batches whose rows
-  // would go through memory: there it is rounded to bf16 first.
-  // That costs the result one more rounding of its own size (each of the top_k
-  // rows is off by at most 2^-8 of itself, the sum's own rounding is another
-  // 2^-8), and halves the largest traffic of the layer: 4096 tokens x 8 x 4096
-  // are 537 MB in fp32, written and read once.
-  auto combine = [&](const int32_t* slot, bool bf16_rows) {
+  // The pairs' rows stay in fp32 until they are summed.  (Rounded to bf16 they
+  // would be half the bytes, and the sum off by up to 2^-8 of each of them.)
+  auto combine = [&](const int32_t* slot) {
     const unsigned threads = unsigned(std::min<int64_t>(256, mx_ceil(D / 8, 32) * 32));
     auto go = [&](auto kernel) {
       return launch_pdl(kernel, dim3(unsigned(T), unsigned(mx_ceil(D, 2048))), dim3(threads), 0,
-                        stream, static_cast<const void*>(ws + s.out), slot, ids, E, weights,
+                        stream, reinterpret_cast<const float*>(ws + s.out), slot, ids, E, weights,
                         top_k, D, y);
     };
-    if (dtype == LUTQ_BF16)
-      return bf16_rows ? go(moe_combine_kernel<LUTQ_BF16, LUTQ_BF16>)
-                       : go(moe_combine_kernel<LUTQ_BF16, LUTQ_FP32>);
-    if (dtype == LUTQ_FP16) return go(moe_combine_kernel<LUTQ_FP16, LUTQ_FP32>);
-    return go(moe_combine_kernel<LUTQ_FP32, LUTQ_FP32>);
+    if (dtype == LUTQ_BF16) return go(moe_combine_kernel<LUTQ_BF16>);
+    if (dtype == LUTQ_FP16) return go(moe_combine_kernel<LUTQ_FP16>);
+    return go(moe_combine_kernel<LUTQ_FP32>);
   };
   const int64_t small = fmt == LUTQ_MXFP4 ? kSmallPairsMx : kSmallPairsNv;
   if (mx_small_fits(pairs, E) && pairs <= small * std::min(E, pairs)) {
@@ -261,7 +254,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     a.N = D;
     a.K = F;
     err = launch_mx_small(a, down, nullptr, fmt, kMxDown, ids, pairs, top_k, num_sms, stream);
-    return err != cudaSuccess ? err : combine(nullptr, false);
+    return err != cudaSuccess ? err : combine(nullptr);
   }
   // an expert has at most T rows, T top_k / E on average
   const int nt = mx_tile_tokens(T);
@@ -333,9 +326,8 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   a.a_stride = w2;
   a.b_scales = ws + s.hq + mx_scale_off(cap, F);
   a.b_rows = reinterpret_cast<const float*>(ws + s.hq + mx_row_off(cap, F, fmt));
-  const bool bf16_rows = dtype == LUTQ_BF16 && T > 64 && mx_ceil(pairs, E) > 32;
   a.y = ws + s.out;
-  a.y_dtype = bf16_rows ? LUTQ_BF16 : LUTQ_FP32;
+  a.y_dtype = LUTQ_FP32;
   a.N = D;
   a.K = F;
   a.chunks = int(mx_ceil(F, kMxChunk));
@@ -351,7 +343,7 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
                          stream);
   }
   if (err != cudaSuccess) return err;
-  return combine(p.slot, bf16_rows);
+  return combine(p.slot);
 }
 
 }  // namespace lutq

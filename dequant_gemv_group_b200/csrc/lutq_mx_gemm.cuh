@@ -14,7 +14,7 @@ namespace lutq {
 enum MxMode {
   kMxPlain = 0,   // y[m, n] = sum_k x[m, k] w[n, k]
   kMxGateUp = 1,  // per expert: h = silu(x gate^T) * (x up^T), rounded to bf16
-  kMxDown = 2,    // per expert: out = h down^T, fp32 (or bf16, block pairs)
+  kMxDown = 2,    // per expert: out = h down^T, fp32
 };
 
 struct MxGemmArgs {

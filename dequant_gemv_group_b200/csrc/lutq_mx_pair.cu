@@ -685,9 +685,7 @@ template <int FMT>
 static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode,
                               cudaStream_t stream) {
   if (mode == kMxGateUp) return launch_one<FMT, kMxGateUp, LUTQ_BF16, kPairPlain>(m, p, stream);
-  if (mode == kMxDown)
-    return p.g.y_dtype == LUTQ_BF16 ? launch_one<FMT, kMxDown, LUTQ_BF16, kPairPlain>(m, p, stream)
-                                    : launch_one<FMT, kMxDown, LUTQ_FP32, kPairPlain>(m, p, stream);
+  if (mode == kMxDown) return launch_one<FMT, kMxDown, LUTQ_FP32, kPairPlain>(m, p, stream);
   if (p.g.y_dtype == LUTQ_BF16) return launch_plain<FMT, LUTQ_BF16>(m, p, stream);
   if (p.g.y_dtype == LUTQ_FP16) return launch_plain<FMT, LUTQ_FP16>(m, p, stream);
   return launch_plain<FMT, LUTQ_FP32>(m, p, stream);

@@ -692,10 +692,8 @@ lutq_status lutq_route(const void* logits, int dtype, int64_t T, int E, const fl
  * lutq_mx_experts - the feed-forward layer of a mixture of experts:
  *   y[t] = sum_j weights[t, j] * W_down_e h_e,  e = ids[t, j],
  *   h_e = bf16(silu(W_gate_e q(x[t])) * (W_up_e q(x[t]))) quantized again,
- * q the quantization above; silu(v) = v / (1 + exp(-v)); the sum over j in
- * fp32 in the order of j, y rounded once.  For bf16 tokens in large batches
- * (T > 64 and more than 32 pairs an expert on average) the rows W_down_e h_e
- * are rounded to bf16 before the sum.
+ * q the quantization above; silu(v) = v / (1 + exp(-v)); the rows W_down_e h_e
+ * and the sum over j in fp32 in the order of j, y rounded once.
  *
  * x       device [T, D] of `dtype`; y device [T, D] of the same type.
  * ids     device int32 [T, top_k]; an id outside 0..E-1 contributes nothing
