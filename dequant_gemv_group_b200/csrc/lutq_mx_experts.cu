@@ -6,7 +6,9 @@
 //
 // (token, choice) pairs are laid out by expert: expert e's rows begin at a
 // multiple of 128 (the height of a scale block) and keep the order of the
-// pairs.  Steps: plan (rows of every expert), x quantized into its rows, gate
+// pairs.  So does every tile of up to nt rows (fewer than 128 for small
+// batches: an expert has more rows than one tile only where tokens name it
+// more than once).  Steps: plan (rows of every expert), x quantized into its rows, gate
 // and up product with silu, hidden values quantized (by that product for many
 // tokens in mxfp4, else a launch), down product, weighted sum over a token's
 // choices in their order.  Where an expert has a handful of
@@ -36,10 +38,19 @@ constexpr int64_t kWidePairs = 16;
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {
-  int32_t* counts;  // [E] rows of an expert
+  int32_t* counts;  // [E] pairs of an expert
   int32_t* bases;   // [E] its first row
   int32_t* slot;    // [pairs] a pair's row, or -1 (id outside 0..E-1)
+  int nt_log2;      // pairs of a tile, a power of two up to 128
 };
+// The place of an expert's i-th pair behind its first row, and the rows of n
+// pairs: tiles begin at multiples of 128 rows.
+__device__ __forceinline__ int moe_place(const MoePlan& p, int i) {
+  return (i >> p.nt_log2) * 128 + (i & ((1 << p.nt_log2) - 1));
+}
+__device__ __forceinline__ int moe_height(const MoePlan& p, int n) {
+  return ((n + (1 << p.nt_log2) - 1) >> p.nt_log2) * 128;
+}
 
 // Four ids from place i on, -1 behind the end.
 __device__ __forceinline__ int4 load_ids(const int32_t* ids, int i, int end, bool aligned) {
@@ -98,18 +109,19 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (STEP == PLAN_COUNT) return;
   int before = 0;
   for (int i = th; i < e; i += kPlanThreads)
-    before += ((ALL ? of[i] : p.counts[i]) + 127) / 128 * 128;
+    before += moe_height(p, ALL ? of[i] : p.counts[i]);
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) atomicAdd(&base_s, before);
   __syncthreads();
-  int row = base_s;
-  if (th == 0) p.bases[e] = row;
+  const int base = base_s;
+  if (th == 0) p.bases[e] = base;
   if (e == 0) {  // pairs of no expert
     for (int i = i0 + lane; i < i1; i += 32)
       if (uint32_t(ids[i]) >= uint32_t(E)) p.slot[i] = -1;
   }
   if (mine == 0) return;
-  for (int w = 0; w < warp; ++w) row += warp_count[w];
+  int first = 0;  // pairs of this expert in the warps before, then in the places before
+  for (int w = 0; w < warp; ++w) first += warp_count[w];
   for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
     const int4 d = load_ids(ids, i, i1, aligned);
     const int n = (d.x == e) + (d.y == e) + (d.z == e) + (d.w == e);
@@ -120,12 +132,12 @@ __global__ void __launch_bounds__(kPlanThreads)
       const int v = __shfl_up_sync(0xffffffffu, scan, x);
       if (lane >= x) scan += v;
     }
-    int r = row + scan - n;
-    if (d.x == e) p.slot[i] = r++;
-    if (d.y == e) p.slot[i + 1] = r++;
-    if (d.z == e) p.slot[i + 2] = r++;
-    if (d.w == e) p.slot[i + 3] = r++;
-    row += __shfl_sync(0xffffffffu, scan, 31);
+    int r = first + scan - n;
+    if (d.x == e) p.slot[i] = base + moe_place(p, r++);
+    if (d.y == e) p.slot[i + 1] = base + moe_place(p, r++);
+    if (d.z == e) p.slot[i + 2] = base + moe_place(p, r++);
+    if (d.w == e) p.slot[i + 3] = base + moe_place(p, r++);
+    first += __shfl_sync(0xffffffffu, scan, 31);
   }
 }
 
@@ -178,10 +190,13 @@ cudaError_t launch_mx_quantize(const void* x, int dtype, int64_t batch, int64_t 
                                const int32_t* to, int copies, void* packed, int32_t* dev_status,
                                int num_sms, cudaStream_t stream);
 
-// Rows of all experts at most: every pair, and each expert in use padded to 128.
+// Rows of all experts at most.  Tiles of 128: every pair, and each expert in
+// use padded to 128.  Narrower tiles have room for T pairs or more, so the
+// tiles that are not their expert's last are at most top_k.  (Both bounds for
+// any T: the space for a batch also holds a smaller one.)
 static int64_t moe_rows(int64_t T, int top_k, int E) {
-  const int64_t pairs = T * top_k;
-  return mx_ceil(pairs + 127 * std::min<int64_t>(E, pairs), 128) * 128;
+  const int64_t pairs = T * top_k, used = std::min<int64_t>(E, pairs);
+  return 128 * std::max(mx_ceil(pairs + 127 * used, 128), used + top_k);
 }
 
 struct MoeSpace {
@@ -218,9 +233,15 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const MoeSpace s = moe_space(T, top_k, E, D, F, fmt);
   auto ints = [&](int64_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-  const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot)};
   const int64_t cap = moe_rows(T, top_k, E);
   const int pairs = int(T * top_k);
+  // pairs of a tile: an expert has T top_k / E on average, and no more than T
+  // unless a token names it more than once (block pairs: whole runs of rows)
+  const bool wide = mx_ceil(pairs, E) > kWidePairs && T > 32;
+  const int nt = wide ? 128 : mx_tile_tokens(T);
+  int nt_log2 = 4;
+  while (1 << nt_log2 < nt) ++nt_log2;
+  const MoePlan p = {ints(s.counts), ints(s.bases), ints(s.slot), nt_log2};
   // The pairs' rows stay in fp32 until they are summed.  (Rounded to bf16 they
   // would be half the bytes, and the sum off by up to 2^-8 of each of them.)
   auto combine = [&](const int32_t* slot) {
@@ -256,9 +277,6 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     err = launch_mx_small(a, down, nullptr, fmt, kMxDown, ids, pairs, top_k, num_sms, stream);
     return err != cudaSuccess ? err : combine(nullptr);
   }
-  // an expert has at most T rows, T top_k / E on average
-  const int nt = mx_tile_tokens(T);
-  const bool wide = mx_ceil(pairs, E) > kWidePairs && T > 32;
   const int64_t w1 = mx_bytes(F, D, fmt), w2 = mx_bytes(D, F, fmt);
   const int64_t used = std::min<int64_t>(E, pairs);  // experts in use at most
   CUtensorMap maps[4];

@@ -57,10 +57,10 @@ struct MxShared {
   int abort;
 };
 
-// A tile begins at a multiple of 128 tokens, the height of a scale block
-// (narrower tiles only where one holds all tokens), so that its scales begin
-// at the first column of a block: the MMA faults on others ("misaligned
-// address" with scales one column on).
+// A tile begins at a multiple of 128 rows of the packed tokens, the height of a
+// scale block (an expert's n-th tile of nt tokens at its row 128 n), so that
+// its scales begin at the first column and lane of a block: the MMA faults on
+// others ("misaligned address" with scales one column on).
 //
 // Walks the tiles t = first, first + step, ... of a launch, each expert's in turn.
 struct MxTiles {
@@ -70,7 +70,7 @@ struct MxTiles {
   __device__ MxTiles(const MxGemmArgs& a, int nt_, const int32_t* counts_)
       : counts(counts_), mtiles(a.mtiles), nt(nt_), experts(a.experts),
         e_tiles(int(mx_ceil(counts_[0], nt_)) * a.mtiles) {}
-  // false: no tile t; else its expert, row tile, first token and tokens
+  // false: no tile t; else its expert, row tile, first row of tokens and tokens
   __device__ bool at(int64_t t, int* expert, int* mt, int* m0, int* valid) {
     while (t >= e_first + e_tiles) {
       e_first += e_tiles;
@@ -84,7 +84,7 @@ struct MxTiles {
     const int i = int(t - e_first), n = i / mtiles;
     *expert = e;
     *mt = i - n * mtiles;
-    *m0 = n * nt;
+    *m0 = n * 128;
     *valid = min(nt, counts[e] - n * nt);
     return true;
   }

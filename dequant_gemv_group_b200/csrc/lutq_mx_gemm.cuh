@@ -32,7 +32,7 @@ struct MxGemmArgs {
   int chunks;                  // ceil(K / 256)
   int mtiles;                  // ceil(N / 128)
   int stages;
-  // experts: how many rows each has and where they begin (multiples of 128)
+  // experts: how many tokens each has and their first rows (multiples of 128)
   const int32_t* counts;
   const int32_t* bases;
   int experts;
