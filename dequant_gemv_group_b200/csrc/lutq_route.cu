@@ -96,7 +96,6 @@ __device__ __forceinline__ int route_select32(const RouteArgs& a, const float (&
   const int E = a.E;
   const float base = a.score == LUTQ_SCORE_SOFTMAX ? float(P + 20) * 0x1p-24f : 4e-7f;
   const Error32 score_error = {base, float(P + 1) * 0x1p-23f};
-  const Error32 group_error = {2.f * base, 0x1p-22f};
   float c[P], bias[P];
 #pragma unroll
   for (int i = 0; i < P; ++i)
@@ -143,21 +142,29 @@ __device__ __forceinline__ int route_select32(const RouteArgs& a, const float (&
       b1 = fmaxf(fmaxf(b1, o1), fminf(b0, o0));
       b0 = fmaxf(b0, o0);
     }
-    const float best = a.group_best == 2 && b1 > -INFINITY ? b0 + b1 : b0;
+    const bool two = a.group_best == 2 && b1 > -INFINITY;
+    const float best = two ? b0 + b1 : b0;
+    // How far off: by both scores' p, and by the roundings of both biased scores
+    // and of their sum, each below 2^-24 of itself.  The scores may cancel, so it
+    // is their magnitudes that count.  (-infinity: exact)
+    const float off =
+        best > -INFINITY ? 2.f * base + 0x1p-22f * (fabsf(b0) + (two ? fabsf(b1) : 0.f)) : 0.f;
     uint32_t gk = gr < a.groups && (lane & (L - 1)) == 0 ? order_key32(best) : 0u;
-    uint32_t kept = 0, last = 0;
+    const bool scored = gk != 0u;
+    uint32_t kept = 0;
     for (int i = 0; i < a.top_groups; ++i) {
-      last = __reduce_max_sync(0xffffffffu, gk);
-      // (equal ones leave together; then the order is not clear below)
+      const uint32_t last = __reduce_max_sync(0xffffffffu, gk);
+      // (equal ones leave together; then the order is not clear)
       const uint32_t who = __ballot_sync(0xffffffffu, gk == last);
       clear = clear && (who & (who - 1u)) == 0u;
       kept |= 1u << ((__ffs(who) - 1) >> a.group_lanes);
       if (gk == last) gk = 0u;
     }
-    const uint32_t next = __reduce_max_sync(0xffffffffu, gk);
-    if (next != 0u)
-      clear = clear && clearly_above(key_value32(last), key_value32(next), group_error);
-    if (!clear) return 0;
+    // the lowest that a kept group can be, the highest that another can be
+    const uint32_t low = __reduce_min_sync(
+        0xffffffffu, scored && gk == 0u ? order_key32(best - off) : 0xffffffffu);
+    const uint32_t high = __reduce_max_sync(0xffffffffu, gk != 0u ? order_key32(best + off) : 0u);
+    if (!clear || low <= high) return 0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (!((kept >> group_of(a, lane + 32 * i)) & 1u)) c[i] = -INFINITY;
