@@ -592,7 +592,7 @@ def lutq_mx_quantize(w: torch.Tensor, fmt: str, packed: Optional[torch.Tensor] =
 def lutq_mx_dequantize(packed: torch.Tensor, n: int, k: int, fmt: str, dtype=torch.bfloat16,
                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a packed matrix [bytes] as [n, k], or of [B, bytes] as [B, n, k]."""
-    nb = lutq_mx_packed_bytes(n, k, fmt)
+    nb = lutq_mx_packed_bytes(n, k, fmt) if n else 0
     b = packed.shape[0] if packed.dim() == 2 else 1
     _mx_need(packed, b * nb if nb >= 0 else -1, "packed")
     out = _mx_out(out, (b, n, k) if packed.dim() == 2 else (n, k), dtype, packed, "out")
