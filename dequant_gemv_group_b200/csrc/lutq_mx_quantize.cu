@@ -237,7 +237,16 @@ __global__ void __launch_bounds__(kMxWarps * 32)
   if (bad) report(dev_status, LUTQ_ERR_NONFINITE);
 }
 
-// The values of 8 codes: (element * scale) * row scale, rounded once.
+// a * b cut toward zero, with the last bit set if anything was cut off: rounded
+// to 16 bits from there, the exact product is rounded once.
+__device__ __forceinline__ float mul_odd(float a, float b) {
+  const float p = __fmul_rz(a, b), rest = fmaf(a, b, -p);
+  return rest < 0.f || rest > 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+
+// The values of 8 codes: (element * scale) * row scale, rounded once.  The first
+// product has 6 bits at most; the second is exact in fp32 if the row scale is a
+// power of two (as the quantizer's are), and may have 30 bits otherwise.
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kMxWarps * 32)
     mx_dequantize_kernel(const uint8_t* __restrict__ packed, int64_t rows, int64_t K,
@@ -256,6 +265,7 @@ __global__ void __launch_bounds__(kMxWarps * 32)
                       (lane / (4 * L)) * 512 + ((lane / L) & 3);
   float g = 1.f;
   if (FMT == LUTQ_NVFP4) g = reinterpret_cast<const float*>(pm + mx_row_off(rows, K, FMT))[r];
+  const bool odd = FMT == LUTQ_NVFP4 && DT != LUTQ_FP32 && (__float_as_uint(g) & 0x7fffffu) != 0u;
   const int64_t base = (int64_t(blockIdx.z) * rows + r) * K;
   constexpr int U = 2 * kMxBatch;
   for (int64_t c = blockIdx.y; c < chunks; c += int64_t(gridDim.y) * U) {
@@ -277,7 +287,14 @@ __global__ void __launch_bounds__(kMxWarps * 32)
       float v[8];
       e2m1_values8(q[u], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
+      for (int j = 0; j < 8; ++j) v[j] *= s;
+      if (odd) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = mul_odd(v[j], g);
+      } else if (FMT == LUTQ_NVFP4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= g;
+      }
       store8<DT>(out, base + k, v);
     }
   }

@@ -618,8 +618,9 @@ int64_t lutq_mx_packed_bytes(int64_t N, int64_t K, int format);
 /*
  * lutq_mx_quantize - W [batch, N, K] of `dtype` into `batch` packed matrices.
  * lutq_mx_dequantize - the values of packed matrices as `dtype`
- *   [batch, N, K], rounded once (exact in bf16 and fp32 but for results below
- *   their range).
+ *   [batch, N, K], rounded once; exact in bf16 and fp32 where the row scale is
+ *   a power of two, as lutq_mx_quantize's are.  (Results below the type's
+ *   normal range may be off by one more rounding.)
  * lutq_mx_pack - codes uint8 [batch, N, K/2] (two a byte, element 2i low) and
  *   scale bytes uint8 [batch, N, K/32 or K/16] (and row_scales fp32
  *   [batch, N] for LUTQ_NVFP4, or NULL for 1) into packed matrices; the sign
