@@ -274,6 +274,21 @@ __device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t scale, flo
   return e2m1_x8(v);
 }
 
+// silu(g) * u of a hidden value, the same for every batch size: with t =
+// exp(-|g|), g / (1 + t) or g t / (1 + t), whose divisor lies in [1, 2], so that
+// the quotient needs no special cases: a product with the approximate
+// reciprocal and one correction by its remainder.  exp is off by at most 2 units
+// of 2^-23 (in t and 1 + t together less than that), the four roundings by 2^-24
+// each: less than 2^-21 in all, before the rounding to bf16.  (The fast
+// exponential's error grows with |g|, to 2^-18 at -88, and the fast division
+// gives 0 for a divisor above 2^126: hidden values moved by a bf16 step, or
+// became 0.)
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float t = expf(-fabsf(g)), d = 1.f + t, r = rcp_approx(d);
+  const float n = g < 0.f ? g * t : g, q = n * r;
+  return fmaf(fmaf(-q, d, n), r, q) * u;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Value v rounded once to the output type, at element i of y.

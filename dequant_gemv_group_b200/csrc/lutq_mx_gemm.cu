@@ -90,10 +90,6 @@ struct MxTiles {
   }
 };
 
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  return g / (1.f + __expf(-g)) * u;
-}
-
 // Bounded wait for work already in flight, whatever the abort flag says.
 __device__ __forceinline__ void mx_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_ns();

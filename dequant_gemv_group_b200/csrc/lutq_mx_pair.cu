@@ -90,10 +90,6 @@ struct PairArgs {
 // boxes of 16.
 __host__ __device__ __forceinline__ int pair_width(int valid) { return (valid + 31) / 32 * 32; }
 
-__device__ __forceinline__ float pair_silu_mul(float g, float u) {
-  return __fdividef(g, 1.f + __expf(-g)) * u;
-}
-
 __device__ __forceinline__ void pair_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -498,7 +494,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             f = f * ga0 * gb;
             if (SETS == 2) u = u * ga[1] * gb;
           }
-          if (SETS == 2) f = pair_silu_mul(f, u);
+          if (SETS == 2) f = silu_mul(f, u);
           stage1<DT>(sta + j * 32 * ES, f);
         }
         if (MODE == kMxGateUp && FMT == LUTQ_MXFP4) {

@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kSmallThreads)
           }
           if (row >= a.N) return;
           const int64_t at = int64_t(MODE == kMxPlain ? m : list[r.at + m]) * a.N + row;
-          if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, at, v0 / (1.f + __expf(-v0)) * v1);
+          if (MODE == kMxGateUp) store1<LUTQ_BF16>(a.y, at, silu_mul(v0, v1));
           else if (MODE == kMxDown) store1<LUTQ_FP32>(a.y, at, v0);
           else if (a.y_dtype == LUTQ_FP32) store1<LUTQ_FP32>(a.y, at, v0);
           else if (a.y_dtype == LUTQ_BF16) store1<LUTQ_BF16>(a.y, at, v0);
