@@ -87,6 +87,7 @@ _SIGS = {
     "lutq_mx_dequantize": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp]),
     "lutq_mx_pack": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
     "lutq_mx_gemm": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp]),
+    "lutq_mx_gemm_plan": (_i32, [_i64, _i64, _i64, _i32, _i32, _vp]),
     "lutq_mx_gemv": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp]),
     "lutq_route": (_i32, [_vp, _i32, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                           ctypes.c_float, _vp, _vp, _vp, _vp]),
@@ -642,6 +643,13 @@ def lutq_mx_gemm(x_packed: torch.Tensor, m: int, packed: torch.Tensor, n: int, k
                             y.data_ptr(), _dtype(dtype, "dtype"), _ptr(status),
                             _here(packed, x_packed, y, status)), "lutq_mx_gemm")
     return y
+
+
+def lutq_mx_gemm_plan(m: int, n: int, k: int, fmt: str, num_sms: int) -> dict:
+    """How lutq_mx_gemm divides a product among pairs of thread blocks (host only)."""
+    out = (ctypes.c_int32 * 4)()
+    _check(lib.lutq_mx_gemm_plan(m, n, k, _format(fmt), num_sms, out), "lutq_mx_gemm_plan")
+    return dict(zip(("rows", "tokens", "split", "pairs"), list(out)))
 
 
 def lutq_mx_gemv(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, fmt: str,

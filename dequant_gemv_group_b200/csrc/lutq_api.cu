@@ -7,7 +7,7 @@
 
 #include "lutq.h"
 #include "lutq_trace.h"
-#include "lutq_mx.cuh"
+#include "lutq_mx_gemm.cuh"
 
 namespace lutq {
 cudaError_t launch_quantize(const void* W, int64_t N, int64_t K, const void* codebook, int bits,
@@ -618,6 +618,19 @@ lutq_status lutq_mx_gemm(const void* x_packed, int64_t M, const void* packed, in
   LUTQ_TRACE_RANGE("lutq_mx_gemm");
   return mx_product(x_packed, LUTQ_BF16, false, M, packed, N, K, format, y, y_dtype, dev_status,
                     stream);
+}
+
+lutq_status lutq_mx_gemm_plan(int64_t M, int64_t N, int64_t K, int format, int num_sms,
+                              int32_t* plan) {
+  LUTQ_TRACE_RANGE("lutq_mx_gemm_plan");
+  if (!mx_format_ok(format) || plan == nullptr || num_sms < 1) return LUTQ_ERR_INVALID_ARG;
+  if (!mx_shape_ok(N, K) || M < 1 || M >= (int64_t(1) << 30)) return LUTQ_ERR_SHAPE;
+  const lutq::MxPairPlan p = lutq::mx_pair_plan(M, N, K, format, num_sms);
+  plan[0] = p.tall ? 512 : 256;
+  plan[1] = p.width;
+  plan[2] = p.split;
+  plan[3] = p.pairs;
+  return LUTQ_OK;
 }
 
 lutq_status lutq_mx_gemv(const void* x, int x_dtype, int64_t M, const void* packed, int64_t N,

@@ -533,8 +533,8 @@ cudaError_t launch_mx_product(const void* x, int x_dtype, bool values, int64_t M
   a.b_scales = xp + mx_scale_off(M, K);
   a.b_rows = reinterpret_cast<const float*>(xp + mx_row_off(M, K, fmt));
   a.chunks = int(mx_ceil(K, kMxChunk));
-  return launch_mx_pair(a, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain,
-                        mx_ceil(N, 256) * mx_ceil(M, 256), num_sms, stream);
+  return launch_mx_pair(a, w, nullptr, mx_bytes(N, K, fmt), xp, M, fmt, kMxPlain, 0, num_sms,
+                        stream);
 }
 
 }  // namespace lutq

@@ -60,7 +60,18 @@ cudaError_t make_mx_scale_map(CUtensorMap* map, const void* packed, int64_t rows
 // An output [M, N], in boxes of 32 columns x 32 rows.
 cudaError_t make_mx_out_map(CUtensorMap* map, void* y, int64_t M, int64_t N, int dtype);
 
-// The kernel for many tokens (lutq_mx_pair.cu).
+// The division of a plain product among block pairs (lutq_mx_pair.cu).
+struct MxPairPlan {
+  int width;      // columns of the widest tile: all tokens, or the most that a tile has
+  int64_t tiles;
+  int split;      // pairs that share a tile by K; more than one: each tile has its own
+  int tall;       // tiles of 512 weight rows instead of 256
+  int pairs;      // pairs of blocks in the launch
+  int slices;     // a warp's staged slices
+};
+MxPairPlan mx_pair_plan(int64_t M, int64_t N, int64_t K, int fmt, int num_sms);
+
+// The kernel for many tokens (lutq_mx_pair.cu).  tiles: of experts, at most.
 struct MxPairMaps {
   CUtensorMap a[2], b, b16, sa[2], sb, y;
 };

@@ -687,6 +687,43 @@ static cudaError_t launch_fmt(const MxPairMaps& m, const PairArgs& p, int mode,
   return launch_plain<FMT, LUTQ_FP32>(m, p, stream);
 }
 
+// How a plain product (lutq_mx_gemm) is divided: see lutq_mx_gemm_plan.
+MxPairPlan mx_pair_plan(int64_t M, int64_t N, int64_t K, int fmt, int num_sms) {
+  MxPairPlan p = {};
+  p.width = pair_width(int(std::min<int64_t>(M, 256)));
+  p.tiles = mx_ceil(N, 256) * mx_ceil(M, 256);
+  const int chunks = int(mx_ceil(K, kMxChunk)), slots = std::max(1, num_sms / 2);
+  // Split tiles by K while that gives idle pairs work and saves more chunks (0.3 us
+  // each) than the exchange costs (1.5 us for 32 columns, 3 for 256; 4096 x 14336
+  // at 512 tokens 23.6 -> 20.3 us, 512 x 14336 at 128 tokens 22.6 -> 13.0).
+  // Clusters of eight blocks that fill their multiprocessors leave many unused:
+  // sixteen of them ran in two waves.  (Every tile needs pairs of its own.)
+  const int per = p.tiles <= 16 && M <= 128 ? 8 : 12;
+  p.split = 1;
+  if (p.tiles <= 32 && 2 * p.tiles <= slots && chunks >= 2 * per)
+    p.split = p.tiles <= 8 && 4 * p.tiles <= slots && chunks >= 4 * per ? 4 : 2;
+  // Tall tiles where they save a round: what bounds a tile is what its pair
+  // fetches, 85 GB/s a multiprocessor.  28672 x 8192 in nvfp4 at 133 tokens: 2
+  // rounds of 32 KB a chunk and block take 35.2 us, 1 of 50 KB 30.5; at 17
+  // tokens 2 of 22 KB 27.8, 1 of 40 KB 24.9.
+  if (p.split == 1 && p.width <= kPairTallTokens) {
+    auto fetched = [&](int nd) {
+      const int a_bytes = 128 * 128 + mx_chunk_bytes(fmt);
+      const int b_bytes = p.width * 64 + (p.width > kMxRowTile ? 2 : 1) * mx_chunk_bytes(fmt);
+      return mx_ceil(mx_ceil(N, 256 * nd), slots) * (nd * a_bytes + b_bytes);
+    };
+    p.tall = fetched(2) < fetched(1);
+    if (p.tall) p.tiles = mx_ceil(N, 512);
+  }
+  p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(p.tiles, slots / p.split))) * p.split;
+  // Slices are staged while the next tile's MMAs run, two a warp; where there
+  // is no next tile, or it waits for these anyway (tall), one, and a stage more
+  // instead (133 tokens x 9472 x 8192 in nvfp4 16.2 -> 15.7 us, 28672 30.5 ->
+  // 29.7; in mxfp4 14.6 -> 14.3, 27.3 -> 27.9).
+  p.slices = p.tall || p.tiles * p.split <= p.pairs ? 1 : 2;
+  return p;
+}
+
 cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void* weights2,
                            int64_t w_bytes, const void* tokens, int64_t token_rows, int fmt,
                            int mode, int64_t tiles, int num_sms, cudaStream_t stream) {
@@ -704,54 +741,35 @@ cudaError_t launch_mx_pair(const MxGemmArgs& g, const void* weights, const void*
   }
   const int64_t t_bytes = mx_bytes(token_rows, g.K, fmt);
   const int nt = mode == kMxGateUp ? 128 : 256;
-  // columns of the widest tile: all tokens, or the most that a tile has
-  const int width = mode == kMxPlain ? pair_width(int(std::min<int64_t>(g.M, nt))) : nt;
-  if ((err = make_mx_map(&m.b, tokens, token_rows, g.K, 1, t_bytes, width / 2)) != cudaSuccess)
+  PairArgs p = {};
+  p.g = g;
+  p.token_tiles = int(mx_ceil(g.M, nt));
+  if (mode == kMxPlain) {
+    // Few tokens leave room for more stages, which come at the latency of memory
+    // (9472 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 15.2 -> 13.5 us).
+    const MxPairPlan plan = mx_pair_plan(g.M, g.N, g.K, fmt, num_sms);
+    p.width = plan.width;
+    p.split = plan.split;
+    p.tall = plan.tall;
+    p.pairs = plan.pairs;
+    p.slices = plan.slices;
+    if (p.tall) {
+      m.a[1] = m.a[0];
+      m.sa[1] = m.sa[0];
+    }
+  } else {
+    p.width = nt;
+    p.split = 1;
+    p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms / 2)));
+    p.slices = 2;
+  }
+  if ((err = make_mx_map(&m.b, tokens, token_rows, g.K, 1, t_bytes, p.width / 2)) != cudaSuccess)
     return err;
   if ((err = make_mx_map(&m.b16, tokens, token_rows, g.K, 1, t_bytes, 16)) != cudaSuccess)
     return err;
   if ((err = make_mx_scale_map(&m.sb, tokens, token_rows, g.K, 1, t_bytes, fmt)) != cudaSuccess)
     return err;
   const int dt = mode == kMxGateUp ? int(LUTQ_BF16) : g.y_dtype;
-  PairArgs p = {};
-  p.g = g;
-  p.token_tiles = int(mx_ceil(g.M, nt));
-  // Few tokens leave room for more stages, which come at the latency of memory
-  // (9472 x 8192 in nvfp4, 17 tokens: 8 stages for 4, 15.2 -> 13.5 us).
-  p.width = width;
-  // Split a plain product's tiles by K while that gives idle pairs work and
-  // saves more chunks (0.3 us each) than the exchange costs (1.5 us for 32
-  // columns, 3 for 256; 4096 x 14336 at 512 tokens 23.6 -> 20.3 us, 512 x 14336
-  // at 128 tokens 22.6 -> 13.0).  Clusters of eight blocks that fill their
-  // multiprocessors leave many unused: sixteen of them ran in two waves.
-  const int slots = num_sms / 2;
-  const int per = tiles <= 16 && g.M <= 128 ? 8 : 12;
-  p.split = 1;
-  if (mode == kMxPlain && tiles <= 32 && 2 * tiles <= slots && g.chunks >= 2 * per)
-    p.split = tiles <= 8 && g.chunks >= 4 * per ? 4 : 2;
-  // Tall tiles where they save a round: what bounds a tile is what its pair
-  // fetches, 85 GB/s a multiprocessor.  28672 x 8192 in nvfp4 at 133 tokens: 2
-  // rounds of 32 KB a chunk and block take 35.2 us, 1 of 50 KB 30.5; at 17
-  // tokens 2 of 22 KB 27.8, 1 of 40 KB 24.9.
-  if (mode == kMxPlain && p.split == 1 && width <= kPairTallTokens) {
-    auto fetched = [&](int nd) {
-      const int a_bytes = 128 * 128 + mx_chunk_bytes(fmt);
-      const int b_bytes = width * 64 + (width > kMxRowTile ? 2 : 1) * mx_chunk_bytes(fmt);
-      return mx_ceil(mx_ceil(g.N, 256 * nd), slots) * (nd * a_bytes + b_bytes);
-    };
-    p.tall = fetched(2) < fetched(1);
-    if (p.tall) {
-      tiles = mx_ceil(g.N, 512);
-      m.a[1] = m.a[0];
-      m.sa[1] = m.sa[0];
-    }
-  }
-  p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(tiles, slots / p.split))) * p.split;
-  // Slices are staged while the next tile's MMAs run, two a warp; where there
-  // is no next tile, or it waits for these anyway (tall), one, and a stage more
-  // instead (133 tokens x 9472 x 8192 in nvfp4 16.2 -> 15.7 us, 28672 30.5 ->
-  // 29.7; in mxfp4 14.6 -> 14.3, 27.3 -> 27.9).
-  p.slices = mode == kMxPlain && (p.tall || tiles * p.split <= p.pairs) ? 1 : 2;
   p.tma_store = (g.N * (dt == LUTQ_FP32 ? 4 : 2)) % 16 == 0 &&
                 !(mode == kMxGateUp && fmt == LUTQ_MXFP4);  // (quantized instead)
   if (p.tma_store) {

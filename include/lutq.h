@@ -661,6 +661,20 @@ lutq_status lutq_mx_gemv(const void* x, int x_dtype, int64_t M, const void* pack
                          void* stream);
 
 /*
+ * lutq_mx_gemm_plan - how lutq_mx_gemm divides a product among pairs of thread
+ * blocks on a GPU with num_sms multiprocessors (host only; for inspection and
+ * tests).  plan[4] receives {rows, tokens, split, pairs}: tiles of `rows` (256
+ * or 512) rows of w and up to `tokens` of x's rows (the last ones of a product
+ * of more than 256 may have fewer), ceil(N / rows) * ceil(M / 256) of them;
+ * `split` neighbouring pairs share a tile by K, each its part of the 256-wide
+ * chunks; `pairs` pairs in all, so pairs / split tiles at a time.  With split >
+ * 1 each group of pairs has exactly one tile.  Errors as lutq_mx_gemm for M >=
+ * 1; LUTQ_ERR_INVALID_ARG for a NULL plan or num_sms < 1.
+ */
+lutq_status lutq_mx_gemm_plan(int64_t M, int64_t N, int64_t K, int format, int num_sms,
+                              int32_t* plan);
+
+/*
  * lutq_route - routing of T tokens to E experts.  For each token, in fp64:
  *   p_e = exp(z_e) / sum exp(z)  (LUTQ_SCORE_SOFTMAX) or 1 / (1 + exp(-z_e))
  *   (LUTQ_SCORE_SIGMOID) of its logits z; c_e = p_e + bias_e (bias may be
