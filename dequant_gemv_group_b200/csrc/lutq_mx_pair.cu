@@ -635,9 +635,17 @@ static cudaError_t launch_one(const MxPairMaps& m, PairArgs p, cudaStream_t stre
   using Cfg = PairCfg<FMT, MODE, TILE>;
   constexpr int SLICE = 32 * 32 * (DT == LUTQ_FP32 ? 4 : 2);
   constexpr int smem = 227 * 1024;  // all of it: the block holds all of tensor memory
-  const int fixed = 1024 + 8 * p.slices * SLICE + int(sizeof(PairShared)) +
-                    (MODE != kMxPlain ? 8 * p.g.experts : 0);
-  p.g.stages = std::min(kPairMaxStages, (smem - fixed) / Cfg::stage(p.width));
+  auto stages = [&](int slices) {
+    const int fixed = 1024 + 8 * slices * SLICE + int(sizeof(PairShared)) +
+                      (MODE != kMxPlain ? 8 * p.g.experts : 0);
+    return std::min(kPairMaxStages, (smem - fixed) / Cfg::stage(p.width));
+  };
+  // Tall tiles: a second staged slice where it does not cost a stage.  28672 x
+  // 8192, one slice / two, us: nvfp4, 133 tokens 31.2 / 32.8, 192 (where one
+  // gives no stage more) 35.3 / 35.1; mxfp4, 192 tokens 30.2 / 31.3, 133 (no
+  // stage more) 28.4 / 27.9; alike at 57344 x 8192, 24576 x 4096, 20480 x 5120.
+  if (Cfg::TALL) p.slices = stages(1) > stages(2) ? 1 : 2;
+  p.g.stages = stages(p.slices);
   // A split tile's sums, 512 bytes a column, fit in four stages of any width:
   // 4 (16 KB + 64 width) >= 512 width for up to 256 columns.
   static_assert(TILE != kPairSplit ||
@@ -717,10 +725,9 @@ MxPairPlan mx_pair_plan(int64_t M, int64_t N, int64_t K, int fmt, int num_sms) {
   }
   p.pairs = int(std::max<int64_t>(1, std::min<int64_t>(p.tiles, slots / p.split))) * p.split;
   // Slices are staged while the next tile's MMAs run, two a warp; where there
-  // is no next tile, or it waits for these anyway (tall), one, and a stage more
-  // instead (133 tokens x 9472 x 8192 in nvfp4 16.2 -> 15.7 us, 28672 30.5 ->
-  // 29.7; in mxfp4 14.6 -> 14.3, 27.3 -> 27.9).
-  p.slices = p.tall || p.tiles * p.split <= p.pairs ? 1 : 2;
+  // is no next tile, one, and a stage more instead (133 tokens x 9472 x 8192 in
+  // nvfp4 16.2 -> 15.7 us, in mxfp4 14.6 -> 14.3).  (Tall: see launch_one.)
+  p.slices = p.tiles * p.split <= p.pairs ? 1 : 2;
   return p;
 }
 
