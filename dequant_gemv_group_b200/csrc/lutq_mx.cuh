@@ -368,7 +368,10 @@ __device__ __forceinline__ void store8(void* y, int64_t i, const float (&v)[8]) 
 
 // Launch with the next kernel of the stream allowed to start early: every
 // kernel of this family waits for the one before it (griddepcontrol.wait)
-// before it reads or writes anything.
+// before it reads or writes anything.  One exception: the down product of few
+// tokens reads ids, weights and their scales before its wait.  It may only be
+// launched straight after the gate and up product of the same call, which lets
+// it start (launch_dependents) after its own wait for all that came before.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args... args) {

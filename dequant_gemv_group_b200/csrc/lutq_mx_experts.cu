@@ -269,6 +269,8 @@ cudaError_t launch_mx_experts(const void* x, int dtype, int64_t T, const int32_t
     cudaError_t err = launch_mx_small(a, gate, up, fmt, kMxGateUp, ids, pairs, top_k, num_sms,
                                       stream);
     if (err != cudaSuccess) return err;
+    // (nothing may come in between: this one reads ids and weights before it
+    // waits for the launch before it, see launch_pdl)
     a.x = ws + s.h;
     a.x_dtype = LUTQ_BF16;
     a.y = ws + s.out;

@@ -148,9 +148,10 @@ __global__ void __launch_bounds__(kSmallThreads)
     tmem_alloc(smem_addr(&sh->tmem), Cfg::TMEM);
     tmem_relinquish();
   }
-  // The down product follows the gate and up product of the same call, which
-  // waited for all work before it: the ids and the weights are there, and
-  // only the hidden values must be waited for.
+  // The down product follows straight after the gate and up product of the same
+  // call, which waited for all work before it and only then let this launch
+  // start: the ids and the weights are there, and only the hidden values must
+  // be waited for.
   if (MODE != kMxDown) wait_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
