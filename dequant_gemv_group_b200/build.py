@@ -6,8 +6,9 @@ Run as ``python dequant_gemv_group_b200/build.py [--variant nvtx|bounds]
 
   liblutq.so         the product;
   liblutq_nvtx.so    -DLUTQ_NVTX: every C-ABI call opens an NVTX range;
-  liblutq_bounds.so  -DLUTQ_BOUNDS: the kernels check their indices against
-                     the buffers' extents and report LUTQ_ERR_BOUNDS.
+  liblutq_bounds.so  -DLUTQ_BOUNDS: the lookup-table products check their
+                     indices against the buffers' extents and report
+                     LUTQ_ERR_BOUNDS.
 
 The binding loads the default library unless LUTQ_LIB_VARIANT names a variant.
 Sources compile in parallel; ptxas' register, spill and shared-memory report

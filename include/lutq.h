@@ -61,10 +61,11 @@ typedef enum {
  * lutq_build_flags - how this library was compiled: a bit mask of
  * LUTQ_BUILD_NVTX (every C-ABI call opens an NVTX range named after the call,
  * for Nsight timelines; compiled with -DLUTQ_NVTX) and LUTQ_BUILD_BOUNDS (the
- * kernels check their global, shared and tensor-memory indices against the
- * buffers' extents and report LUTQ_ERR_BOUNDS through dev_status instead of
- * making the access; compiled with -DLUTQ_BOUNDS, slower, for debugging).
- * The default build returns 0.  No GPU use.
+ * lookup-table products check their global, shared and tensor-memory indices
+ * against the buffers' extents and report LUTQ_ERR_BOUNDS through dev_status
+ * instead of making the access; compiled with -DLUTQ_BOUNDS, slower, for
+ * debugging; the lutq_mx_* kernels and lutq_route have no such checks).  The
+ * default build returns 0.  No GPU use.
  *
  * No counterpart in the paper: these are tooling options of the library.
  */
