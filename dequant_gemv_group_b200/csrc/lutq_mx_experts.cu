@@ -23,18 +23,24 @@ namespace lutq {
 
 constexpr int kPlanThreads = 512;
 // Pairs an expert, at most, for the kernel of few tokens; beyond, tokens are
-// packed first (six launches).  Measured, kernel of few tokens / packed, us:
-//   mxfp4, 4096 x 2048: 8 experts, 32 tokens x 2 (8 pairs each) 37.0 / 37.7,
-//     48 tokens (12) 44.7 / 40.0; 64 experts, 32 tokens x 8 (4) 144 / 153;
-//   nvfp4 (a row's maximum first): 60 experts of 2048 x 1440, 37 tokens x 4
-//     (2.5) 66 / 74; 64 of 4096 x 2048, 32 tokens x 8 (4) 212 / 167.
+// packed first (six launches).  Measured, kernel of few tokens / packed, us, by
+// pairs an expert:
+//   mxfp4: 8 experts of 4096 x 2048: 6 33.4 / 35.7, 8 36.6 / 35.9, 12 43.2 /
+//     38.2; 64 of 4096 x 2048: 4 148 / 154, 8 158 / 158; 60 of 2048 x 1440: 6
+//     67.4 / 69.9, 8 73.2 / 71.8;
+//   nvfp4 (a row's maximum first): 64 of 4096 x 2048: 2.5 145 / 154, 3 187 /
+//     159, 4 171 / 163; 60 of 2048 x 1440: 3 65.9 / 71.9, 4 74.3 / 72.9, 8 99 /
+//     83; 8 of 4096 x 2048: 3 33.9 / 38.6, 4 36.4 / 39.5, 6 49.5 / 40.4.
 constexpr int64_t kSmallPairsMx = 8, kSmallPairsNv = 3;
 
 // More pairs an expert: block pairs (lutq_mx_pair.cu).  Measured, block pairs /
-// lutq_mx_gemm.cu, us, mxfp4: 8 experts of 4096 x 2048, 64 tokens x 2 (16
-// pairs each) 39.8 / 41.1, 120 tokens (30) 41.2 / 45.5, 32 (8) 39.6 / 37.8; 60 of
-// 2048 x 1440, 400 tokens x 4 (27) 85 / 88, 128 (9) 83 / 75.
-constexpr int64_t kWidePairs = 16;
+// lutq_mx_gemm.cu, us, by pairs an expert:
+//   mxfp4: 8 experts of 4096 x 2048: 16 40.5 / 39.3, 24 41.4 / 41.4, 30 42.5 /
+//     42.8; 60 of 2048 x 1440: 16 86.6 / 77.9, 27 87.5 / 84.3; 64 of 4096 x
+//     1024: 25 116 / 111;
+//   nvfp4: 47.2 / 45.3, 47.5 / 47.4, 48.7 / 49.8; 105 / 96, 107.8 / 107.7;
+//     132 / 137.
+constexpr int64_t kWidePairs = 24;
 
 // The plan of a call (int32 arrays in the workspace).
 struct MoePlan {
@@ -63,9 +69,9 @@ __device__ __forceinline__ int4 load_ids(const int32_t* ids, int i, int end, boo
 // counts and hands its rows out: each warp owns a run of pairs, 128 at a time,
 // and a scan over the warps' and the lanes' counts keeps the pairs' order.
 // PLAN_ALL: every block counts all experts' pairs itself; many pairs: a launch
-// before (PLAN_COUNT) counts them, each block its expert's.  The layer with one
-// launch / two: 80 pairs 29.1 / 29.9 us, 1600 85.3 / 86.3, 8192 101.8 / 102.0,
-// 32768 185.8 / 179.6.
+// before (PLAN_COUNT) counts them, each block its expert's.  A layer with one
+// launch / two: 1600 pairs 88.9 / 89.1 us, 8192 181.8 / 181.5 and 127.5 / 127.9
+// (64 and 256 experts), 16384 294 / 291, 32768 498 / 488.
 enum { PLAN_COUNT, PLAN_PLACE, PLAN_ALL };
 constexpr int kPlanAll = 1 << 13;
 template <int STEP>
