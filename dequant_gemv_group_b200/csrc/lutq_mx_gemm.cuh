@@ -86,7 +86,9 @@ int mx_tile_tokens(int64_t M);
 // multiprocessor.  Clusters of more than two leave multiprocessors over: the
 // 148 hold 33 clusters of 4 and 15 of 8, or 32 of 8 at two blocks each; one
 // more waits for another to end (74 tiles of 2048 x 128 split by 4 at two
-// blocks each: 15.6 us, not split 7.5).
+// blocks each: 15.6 us, not split 7.5).  These counts are one board's, and
+// others may hold one more or less; that costs time, never a tile, and a rule
+// in constants gives the same sums on all boards.
 inline int64_t mx_clusters(int s, int per_sm, int num_sms) {
   if (s <= 2) return int64_t(num_sms) * per_sm / s;
   return std::max(1, num_sms * (s == 4 ? 33 * per_sm : per_sm == 2 ? 32 : 15) / 148);

@@ -691,7 +691,7 @@ lutq_status lutq_mx_gemm_plan(int64_t M, int64_t N, int64_t K, int format, int n
  * experts 0..top_k-1 with weights 0).  A NaN logit counts as -infinity,
  * +infinity as the limit; both report LUTQ_ERR_NONFINITE.
  *
- * logits  device [T, E] of `dtype`; bias device fp32 [E] or NULL.
+ * logits  device [T, E] of `dtype`; bias device fp32 [E], finite, or NULL.
  * ids     device int32 [T, top_k]; weights device fp32 [T, top_k], written.
  * T = 0 does nothing.  Returns LUTQ_ERR_SHAPE unless 1 <= E <= 1024,
  * E % groups == 0, groups <= 32, 1 <= top_groups <= groups, group_best 1 or 2,
