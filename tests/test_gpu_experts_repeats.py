@@ -7,9 +7,10 @@ from test_gpu_experts import Layer, _close, _inputs, lq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-# (between the kernels for a handful of pairs an expert and for many)
+# packed tokens in narrow tiles; in tiles of 128; block pairs; the kernel of few tokens
 CASES = [(1, 4, 64), (2, 4, 64), (16, 4, 4), (16, 1, 2), (20, 2, 3), (32, 3, 4), (33, 8, 4),
-         (50, 16, 4), (64, 20, 5)]
+         (50, 16, 4), (64, 20, 5), (70, 30, 6), (40, 4, 4), (150, 5, 3), (4, 64, 32), (8, 64, 40),
+         (2, 40, 9)]
 
 
 def _ids(t, e, k, how):
